@@ -43,6 +43,11 @@ SIGNATURES = [
     ("gptq_hessian", _I, [_VP, _I64, _I64, _VP, _VP]),
     ("gptq_inverse_cholesky", _I, [_VP, _I64, _VP, _VP, _VP]),
     ("gptq_quantize_pack_int4", _I, [_VP, _VP, _I64, _I64, _I32, _I32, _VP, _VP, _VP, _I, _VP]),
+    ("quantize_mxfp4", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP]),
+    ("dequant_mxfp4", _I, [_VP, _VP, _I64, _I64, _VP, _I, _VP]),
+    ("mxfp4_matmul", _I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _I, _VP]),
+    ("mxfp4_grouped_matmul", _I, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I, _VP]),
+    ("w4a16_grouped_matmul", _I, [_VP, _I, _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP]),
     ("w4_status_string", ctypes.c_char_p, [_I]),
     ("w4_last_error", ctypes.c_char_p, []),
     ("w4_version", ctypes.c_char_p, []),
@@ -401,6 +406,147 @@ def w4a8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, s
             raise ValueError("workspace must be a 1-D uint8 tensor")
         _gpu(workspace)
         _check(lib.w4a8_matmul_ws(*args, _ptr(workspace), workspace.numel(), _stream(dev)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit floating point and the products by expert
+# ---------------------------------------------------------------------------
+def _launch(dev: torch.device, fn, *args) -> None:
+    """Call fn with dev's current stream, on dev whichever device is current."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)))
+
+
+def _mx_blocks(k: int) -> int:
+    if k <= 0 or k % 32:
+        raise ValueError(f"K = {k} is not a positive multiple of 32")
+    return k // 32
+
+
+def _check_mx(packed: torch.Tensor, scales: torch.Tensor, names: Tuple[str, str], lead: int) -> Tuple[int, ...]:
+    """packed uint8 [..., K/2] and scales uint8 [..., K/32] of `lead` leading dimensions; returns (..., K)."""
+    if packed.dim() != lead + 1:
+        raise ValueError(f"{names[0]} must be a {lead + 1}-D tensor, got {packed.dim()} dimensions")
+    shape = tuple(int(d) for d in packed.shape)
+    k = 2 * shape[-1]
+    _expect(packed, names[0], shape, (torch.uint8,))
+    _expect(scales, names[1], (*shape[:-1], _mx_blocks(k)), (torch.uint8,))
+    return (*shape[:-1], k)
+
+
+Y_DTYPES = (torch.float32, torch.bfloat16)
+
+
+def _y_out(out: Optional[torch.Tensor], out_dtype: torch.dtype, shape, dev: torch.device) -> torch.Tensor:
+    if out is None:
+        if out_dtype not in Y_DTYPES:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        return torch.empty(shape, dtype=out_dtype, device=dev)
+    _expect(out, "out", shape, Y_DTYPES)
+    if _gpu(out) != dev:
+        raise ValueError("all tensors must be on the same device")
+    return out
+
+
+def quantize_mxfp4(w: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """W or x [N, K] (fp32 or bf16) -> (packed uint8 [N, K/2], scales uint8 [N, K/32])."""
+    n, k = _matrix(w, "w")
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"w has dtype {w.dtype}, expected float32 or bfloat16")
+    nb = _mx_blocks(k)
+    if out is not None:
+        _expect(out[0], "packed", (n, k // 2), (torch.uint8,))
+        _expect(out[1], "scales", (n, nb), (torch.uint8,))
+        dev = _gpu(w, *out)
+        packed, scales = out
+    else:
+        dev = _gpu(w)
+        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((n, nb), dtype=torch.uint8, device=dev)
+    _launch(dev, load().quantize_mxfp4, _ptr(w), _dtype_code(w.dtype), n, k, _ptr(packed), _ptr(scales))
+    return packed, scales
+
+
+def dequant_mxfp4(packed: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None):
+    """(packed, scales) -> the values [N, K] in out_dtype."""
+    n, k = _check_mx(packed, scales, ("packed", "scales"), 1)
+    if out is not None:
+        _expect(out, "out", (n, k), tuple(_DT))
+        dev = _gpu(packed, scales, out)
+        w = out
+    else:
+        _dtype_code(out_dtype)
+        dev = _gpu(packed, scales)
+        w = torch.empty((n, k), dtype=out_dtype, device=dev)
+    _launch(dev, load().dequant_mxfp4, _ptr(packed), _ptr(scales), n, k, _ptr(w), _dtype_code(w.dtype))
+    return w
+
+
+def mxfp4_matmul(xq: torch.Tensor, xs: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                 out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None):
+    """y [M, N] = dequant(xq) . dequant(W)^T, both operands from quantize_mxfp4."""
+    m, k = _check_mx(xq, xs, ("xq", "xs"), 1)
+    n, kw = _check_mx(packed, scales, ("packed", "scales"), 1)
+    if kw != k:
+        raise ValueError(f"packed has {kw} columns of codes, xq has K={k}")
+    dev = _gpu(xq, xs, packed, scales)
+    y = _y_out(out, out_dtype, (m, n), dev)
+    _launch(dev, load().mxfp4_matmul, _ptr(xq), _ptr(xs), m, k, _ptr(packed), _ptr(scales), n, _ptr(y),
+            _dtype_code(y.dtype))
+    return y
+
+
+def mxfp4_grouped_matmul(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
+                         scales: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                         out: Optional[torch.Tensor] = None):
+    """y [T, N]: rows offsets[e] .. offsets[e+1]-1 of x times expert e's W^T.
+
+    xq uint8 [T, K/2] and xs [T, K/32]; packed [E, N, K/2] and scales
+    [E, N, K/32]; offsets int32 [E + 1], rising, on the GPU (never read on the
+    host).  Rows that no expert owns are not written: without out= they hold
+    whatever the new tensor held."""
+    t, k = _check_mx(xq, xs, ("xq", "xs"), 1)
+    e, n, kw = _check_mx(packed, scales, ("packed", "scales"), 2)
+    if kw != k:
+        raise ValueError(f"packed has {kw} columns of codes, xq has K={k}")
+    _expect(offsets, "offsets", (e + 1,), (torch.int32,))
+    dev = _gpu(xq, xs, offsets, packed, scales)
+    y = _y_out(out, out_dtype, (t, n), dev)
+    _launch(dev, load().mxfp4_grouped_matmul, _ptr(xq), _ptr(xs), t, k, _ptr(offsets), e, _ptr(packed),
+            _ptr(scales), n, _ptr(y), _dtype_code(y.dtype))
+    return y
+
+
+def w4a16_grouped_matmul(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                         zeros: torch.Tensor, group_size: int, out_dtype: Optional[torch.dtype] = None,
+                         out: Optional[torch.Tensor] = None):
+    """y [T, N]: rows offsets[e] .. offsets[e+1]-1 of x [T, K] (bf16 or fp32)
+    times expert e's dequant(W)^T; out_dtype defaults to x's dtype.
+
+    packed [E, N, K/2], scales and zeros [E, N, K/g] in the INT4 format;
+    offsets int32 [E + 1], rising, on the GPU (never read on the host).  Rows
+    that no expert owns are not written: without out= they hold whatever the
+    new tensor held."""
+    t, k = _matrix(x, "x")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
+    if packed.dim() != 3:
+        raise ValueError(f"packed must be a 3-D tensor, got {packed.dim()} dimensions")
+    e, n = int(packed.shape[0]), int(packed.shape[1])
+    _expect(packed, "packed", (e, n, k // 2), (torch.uint8,))
+    ng = _ngroups(k, group_size)
+    _expect(scales, "scales", (e, n, ng), SZ_DTYPES)
+    _expect(zeros, "zeros", (e, n, ng), (scales.dtype,))
+    _expect(offsets, "offsets", (e + 1,), (torch.int32,))
+    dev = _gpu(x, offsets, packed, scales, zeros)
+    y = _y_out(out, out_dtype or x.dtype, (t, n), dev)
+    _launch(dev, load().w4a16_grouped_matmul, _ptr(x), _dtype_code(x.dtype), t, k, _ptr(offsets), e, _ptr(packed),
+            _ptr(scales), _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(y), _dtype_code(y.dtype))
     return y
 
 

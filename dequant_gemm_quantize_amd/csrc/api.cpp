@@ -447,4 +447,115 @@ int w4a8_matmul_ws(const int8_t* xq, const float* x_scale, int64_t m, int64_t k,
                      group_size, y, y_dtype, workspace, workspace_bytes, stream);
 }
 
+// ---- microscaled 4-bit floating point and the products by expert ---------------
+
+// Block scales (one byte each): the pointer itself is 4-byte aligned.
+static int check_ptr4(const char* fn, const char* name, const void* p) {
+  if (p == nullptr) return fail(W4_EINVAL, "%s: %s is NULL", fn, name);
+  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+    return fail(W4_EINVAL, "%s: %s is not 4-byte aligned", fn, name);
+  return W4_OK;
+}
+
+// Rows and experts of a grouped product, after check_weights: n * k is within
+// its limit, so experts * n * k is checked against the same limit here.
+static int check_groups(const char* fn, int64_t t, int64_t k, int64_t n, int64_t experts) {
+  W4_TRY(check_tokens(fn, t, k, n));
+  if (t > w4::kGroupedMaxRows)
+    return fail(W4_EINVAL, "%s: t = %lld rows, at most %lld", fn, (long long)t,
+                (long long)w4::kGroupedMaxRows);
+  if (experts < 0 || experts > w4::kGroupedMaxExperts)
+    return fail(W4_EINVAL, "%s: experts = %lld must lie in [0, %lld]", fn, (long long)experts,
+                (long long)w4::kGroupedMaxExperts);
+  if (n > 0 && experts > kMaxElems / (n * k)) return fail(W4_EINVAL, "%s: experts * n * k is too large", fn);
+  return W4_OK;
+}
+
+static int check_y(const char* fn, int y_dtype) {
+  if (y_dtype != W4_F32 && y_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: y dtype %d must be W4_F32 or W4_BF16", fn, y_dtype);
+  return W4_OK;
+}
+
+int quantize_mxfp4(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* packed, uint8_t* scales,
+                   hipStream_t stream) {
+  static const char* fn = "quantize_mxfp4";
+  W4_TRY(check_weights(fn, n, k, 32, W4_F32));
+  if (w_dtype != W4_F32 && w_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: w dtype %d must be W4_F32 or W4_BF16", fn, w_dtype);
+  if (n == 0) return ok();
+  W4_TRY(check_ptr(fn, "w", w));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr4(fn, "scales", scales));
+  return hip_status(w4::launch_quantize_mxfp4(w, w_dtype, n, k, packed, scales, stream), fn);
+}
+
+int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64_t k, void* w_out,
+                  int out_dtype, hipStream_t stream) {
+  static const char* fn = "dequant_mxfp4";
+  W4_TRY(check_weights(fn, n, k, 32, W4_F32));
+  if (out_dtype != W4_F32 && out_dtype != W4_F16 && out_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: out dtype %d must be W4_F32, W4_F16 or W4_BF16", fn, out_dtype);
+  if (n == 0) return ok();
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr4(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "w_out", w_out));
+  return hip_status(w4::launch_dequant_mxfp4(packed, scales, n, k, w_out, out_dtype, stream), fn);
+}
+
+int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                 const uint8_t* scales, int64_t n, void* y, int y_dtype, hipStream_t stream) {
+  static const char* fn = "mxfp4_matmul";
+  W4_TRY(check_weights(fn, n, k, 32, W4_F32));
+  W4_TRY(check_y(fn, y_dtype));
+  W4_TRY(check_tokens(fn, m, k, n));
+  if (m == 0 || n == 0) return ok();
+  W4_TRY(check_ptr(fn, "xq", xq));
+  W4_TRY(check_ptr4(fn, "xs", xs));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr4(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "y", y));
+  return hip_status(w4::launch_mx_rows(xq, xs, m, k, packed, scales, n, y, y_dtype, nullptr, 0, stream), fn);
+}
+
+int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_t k, const int32_t* offsets,
+                         int64_t experts, const uint8_t* packed, const uint8_t* scales, int64_t n, void* y,
+                         int y_dtype, hipStream_t stream) {
+  static const char* fn = "mxfp4_grouped_matmul";
+  W4_TRY(check_weights(fn, n, k, 32, W4_F32));
+  W4_TRY(check_y(fn, y_dtype));
+  W4_TRY(check_groups(fn, t, k, n, experts));
+  if (t == 0 || n == 0 || experts == 0) return ok();
+  W4_TRY(check_ptr(fn, "xq", xq));
+  W4_TRY(check_ptr4(fn, "xs", xs));
+  W4_TRY(check_ptr4(fn, "offsets", offsets));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr4(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "y", y));
+  return hip_status(w4::launch_mx_rows(xq, xs, t, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
+                    fn);
+}
+
+int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const int32_t* offsets,
+                         int64_t experts, const uint8_t* packed, const void* scales, const void* zeros,
+                         int sz_dtype, int64_t n, int32_t group_size, void* y, int y_dtype,
+                         hipStream_t stream) {
+  static const char* fn = "w4a16_grouped_matmul";
+  W4_TRY(check_weights(fn, n, k, group_size, sz_dtype));
+  if (x_dtype != W4_F32 && x_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: x dtype %d must be W4_F32 or W4_BF16", fn, x_dtype);
+  W4_TRY(check_y(fn, y_dtype));
+  W4_TRY(check_groups(fn, t, k, n, experts));
+  if (t == 0 || n == 0 || experts == 0) return ok();
+  W4_TRY(check_ptr(fn, "x", x));
+  W4_TRY(check_ptr4(fn, "offsets", offsets));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "zeros", zeros));
+  W4_TRY(check_ptr(fn, "y", y));
+  return hip_status(w4::launch_w4a16_grouped(x, x_dtype, t, k, offsets, (int)experts, packed, scales, zeros,
+                                             sz_dtype, n, group_size, y, y_dtype, stream),
+                    fn);
+}
+
 }  // extern "C"

@@ -107,5 +107,22 @@ hipError_t launch_w4a8_generic(const int8_t* xq, const float* xs, int64_t m, int
                                const uint8_t* packed, const void* scales, const void* zeros,
                                int sz_dtype, int64_t n, int g, void* y, int y_dtype,
                                hipStream_t st);
+// MXFP4: quantize, dequantize.
+hipError_t launch_quantize_mxfp4(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* packed,
+                                 uint8_t* scales, hipStream_t st);
+hipError_t launch_dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64_t k,
+                                void* out, int out_dtype, hipStream_t st);
+// MXFP4 products; by expert when offsets is not null (device memory, experts
+// + 1 entries bounding each expert's rows), dense otherwise.
+hipError_t launch_mx_rows(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                          const uint8_t* scales, int64_t n, void* y, int y_dtype, const int* offsets,
+                          int experts, hipStream_t st);
+// W4A16 by expert.
+hipError_t launch_w4a16_grouped(const void* x, int x_dtype, int64_t t, int64_t k, const int* offsets,
+                                int experts, const uint8_t* packed, const void* scales, const void* zeros,
+                                int sz_dtype, int64_t n, int g, void* y, int y_dtype, hipStream_t st);
+// Limits of the products by expert: tile numbers stay below 2^31.
+constexpr int64_t kGroupedMaxRows = (int64_t)1 << 24;
+constexpr int64_t kGroupedMaxExperts = 65536;
 
 }  // namespace w4

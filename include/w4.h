@@ -323,6 +323,71 @@ int gptq_quantize_pack_int4(float* w, const double* u, int64_t n, int64_t k, int
                             int32_t symmetric, uint8_t* packed, void* scales, void* zeros,
                             int sz_dtype, hipStream_t stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4, OCP Microscaling Formats v1.0) --
+ * a second 4-bit format, for weights and for activations, whose products run
+ * on the matrix cores' own 4-bit inputs.
+ *
+ *  - A block is 32 consecutive elements of a row; K % 32 == 0.
+ *  - scales is uint8 [N, K/32]: byte b stands for 2^(b - 127), 255 for NaN.
+ *  - packed is uint8 [N, K/2] in the nibble order of the INT4 format.  A code
+ *    is a sign bit and E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *  - scales needs 4-byte alignment only.
+ *
+ * quantize_mxfp4 -- with amax = max |block| (w is [N, K], weights or
+ *   activations, w_dtype W4_F32 or W4_BF16):
+ *     E = max(floor(log2(amax)) - 2, -127)  (-127 for a block of zeros)
+ *     code = w / 2^E rounded to the nearest E2M1 value, ties to the even code,
+ *            at most 6 in magnitude, the sign kept
+ *   A block that holds an infinity or a NaN gets the byte 255 and codes 0, so
+ *   it dequantizes to NaN.  Bit-exact.
+ * dequant_mxfp4 -- w_out[n, k] = value of the code * 2^(byte - 127), exact in
+ *   float32, rounded (nearest-even) to out_dtype (W4_F32, W4_F16, W4_BF16).
+ */
+int quantize_mxfp4(const void* w, int w_dtype, int64_t n, int64_t k, uint8_t* packed, uint8_t* scales,
+                   hipStream_t stream);
+int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64_t k, void* w_out,
+                  int out_dtype, hipStream_t stream);
+
+/*
+ * mxfp4_matmul -- y [M, N] = dequant(xq) . dequant(W)^T with both operands in
+ * MXFP4: xq [M, K/2] and xs [M, K/32] from quantize_mxfp4 of the activations,
+ * packed and scales those of the weights.  Products are exact; sums are
+ * float32 and rounded once to y_dtype (W4_BF16 or W4_F32).  Deterministic.
+ */
+int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                 const uint8_t* scales, int64_t n, void* y, int y_dtype, hipStream_t stream);
+
+/*
+ * Products by expert: E weight matrices of one shape, and T rows of x sorted
+ * by expert.  offsets is E + 1 int32 values in device memory (4-byte aligned)
+ * with 0 <= offsets[0] <= ... <= offsets[E] <= T; expert e multiplies rows
+ * offsets[e] .. offsets[e + 1] - 1.  An expert may have no row.  Rows of y
+ * before offsets[0] and from offsets[E] on are left as they were.
+ *
+ * The offsets are read on the device only: the call waits for nothing and
+ * can be captured into a graph and replayed with other offsets in the same
+ * buffer.  Offsets that fall or leave 0..T give unspecified (but
+ * memory-safe) results.
+ *
+ *   T <= 2^24, E <= 65536, E*N*K <= 2^36 (W4_EINVAL beyond them).
+ *   T == 0, N == 0 or E == 0 is a valid empty call.
+ *
+ * mxfp4_grouped_matmul -- packed [E, N, K/2], scales [E, N, K/32], otherwise
+ *   as mxfp4_matmul.
+ * w4a16_grouped_matmul -- packed [E, N, K/2], scales and zeros [E, N, K/g] in
+ *   the INT4 format, x [T, K] W4_BF16 or W4_F32, y W4_BF16 or W4_F32.  The
+ *   code less its zero-point multiplies x exactly, and a group's float32 sum
+ *   takes its scale: no weight is rounded.  Deterministic.
+ */
+int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_t k, const int32_t* offsets,
+                         int64_t experts, const uint8_t* packed, const uint8_t* scales, int64_t n, void* y,
+                         int y_dtype, hipStream_t stream);
+int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const int32_t* offsets,
+                         int64_t experts, const uint8_t* packed, const void* scales, const void* zeros,
+                         int sz_dtype, int64_t n, int32_t group_size, void* y, int y_dtype,
+                         hipStream_t stream);
+
 /* Static description of a w4_status value (never NULL). */
 const char* w4_status_string(int status);
 
