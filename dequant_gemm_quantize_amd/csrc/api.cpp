@@ -503,6 +503,18 @@ int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64
   return hip_status(w4::launch_dequant_mxfp4(packed, scales, n, k, w_out, out_dtype, stream), fn);
 }
 
+// Kernel choice by the rows that one weight matrix has (on average, by expert).
+static int mx_product(const char* fn, const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k,
+                      const int32_t* offsets, int64_t experts, const uint8_t* packed, const uint8_t* scales,
+                      int64_t n, void* y, int y_dtype, hipStream_t stream) {
+  const int64_t rows = offsets != nullptr ? m / experts : m;
+  if (rows > 64 && w4::mx_gemm_fits(k))
+    return hip_status(w4::launch_mx_gemm(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
+                      fn);
+  return hip_status(w4::launch_mx_rows(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
+                    fn);
+}
+
 int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                  const uint8_t* scales, int64_t n, void* y, int y_dtype, hipStream_t stream) {
   static const char* fn = "mxfp4_matmul";
@@ -515,7 +527,7 @@ int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, con
   W4_TRY(check_ptr(fn, "packed", packed));
   W4_TRY(check_ptr4(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "y", y));
-  return hip_status(w4::launch_mx_rows(xq, xs, m, k, packed, scales, n, y, y_dtype, nullptr, 0, stream), fn);
+  return mx_product(fn, xq, xs, m, k, nullptr, 0, packed, scales, n, y, y_dtype, stream);
 }
 
 int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_t k, const int32_t* offsets,
@@ -532,8 +544,7 @@ int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_
   W4_TRY(check_ptr(fn, "packed", packed));
   W4_TRY(check_ptr4(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "y", y));
-  return hip_status(w4::launch_mx_rows(xq, xs, t, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
-                    fn);
+  return mx_product(fn, xq, xs, t, k, offsets, experts, packed, scales, n, y, y_dtype, stream);
 }
 
 int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const int32_t* offsets,

@@ -1,0 +1,373 @@
+// MXFP4 product for many rows, dense or by expert:
+//   y[m, n] = sum over blocks b of 2^(xs + ws - 254) * sum_{k in b} xv wv
+// on v_mfma_scale_f32_32x32x64_f8f6f4: lane (r = lane % 32, h = lane / 32) holds
+// 16 bytes (one block of 32 columns) of row r of each operand and that
+// block's scale byte, so the scales cost no instruction of their own.
+#include <type_traits>
+
+#include "grouped.h"
+#include "w4_common.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStepBytes = 128;  // a K step: 256 columns, one 128-byte line of a row
+
+// Raw buffer resource that answers reads past `bytes` with zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc_n(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// 16 bytes a lane from the resource at the lane's offset to LDS at dst + 16
+// lane (dst the same in every lane), without passing through registers.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 mx_operand(u32x4 v) {
+  return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+}
+
+template <int J>
+__device__ __forceinline__ f32x16 mx_mfma(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, J, (int)sa, J, (int)sb);
+}
+
+// Tile t of tiles_m x tiles_n in bands of 8 M tiles (the last may have fewer).
+__device__ __forceinline__ void band(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  const uint32_t b = t / (8 * tiles_n), in = t - b * 8 * tiles_n;
+  const uint32_t width = tiles_m - 8 * b < 8 ? tiles_m - 8 * b : 8;
+  tn = in / width;
+  tm = 8 * b + in % width;
+}
+
+constexpr uint32_t kPastEnd = 0x80000000u;  // beyond every resource: their sizes stay below 2^31
+
+// Workgroup tile BM x BN of WR x WC waves, each 32 MI x 32 NJ outputs.
+template <int BM_, int BN_, int WR_, int WC_, int S_> struct MxTile {
+  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, S = S_;
+  static constexpr int NW = WR * WC, NT = 64 * NW;
+  static constexpr int MI = BM / (32 * WR), NJ = BN / (32 * WC);
+  static constexpr int LA = BM / (8 * NW), LB = BN / (8 * NW);  // 1 KB loads per wave and step
+  static constexpr int A_STAGE = BM * kStepBytes, B_STAGE = BN * kStepBytes, STAGE = A_STAGE + B_STAGE;
+  static constexpr size_t lds = (size_t)S * STAGE;
+};
+
+}  // namespace
+
+template <typename T, typename TY, bool GROUPED>
+__global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
+                                                      int64_t M, int64_t K, const uint8_t* __restrict__ packed,
+                                                      const uint8_t* __restrict__ scales, int64_t N,
+                                                      void* __restrict__ y, const int* __restrict__ offsets,
+                                                      int experts, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr int MI = T::MI, NJ = T::NJ, LA = T::LA, LB = T::LB, S = T::S;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smx[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w / T::WC, wn = w % T::WC;
+
+  // ---- tile: each XCD (workgroup number mod 8) takes a contiguous eighth of
+  // the list, which goes through bands of 8 M tiles, in a band N tile by N
+  // tile: the 32 tiles that an XCD has at a time read 8 + 4 operand tiles
+  int64_t m0, mend, n0;
+  const uint8_t* wp = packed;
+  const uint8_t* sp = scales;
+  {
+    uint32_t total = tiles_m * tiles_n;
+    if constexpr (GROUPED) total = (uint32_t)grouped_tiles(offsets, experts, (int)M, T::BM, lane) * tiles_n;
+    const uint32_t per = (total + 7) / 8, t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || t >= total) return;
+    if constexpr (GROUPED) {
+      GroupTile g;
+      if (!find_group_tile(offsets, experts, (int)M, T::BM, tiles_n, t, lane, g)) return;
+      const uint32_t own = (uint32_t)(g.rows + T::BM - 1) / T::BM;
+      uint32_t tm, tn;
+      band(g.tile, own, tiles_n, tm, tn);
+      m0 = g.row0 + (int64_t)T::BM * tm;
+      n0 = (int64_t)T::BN * tn;
+      mend = g.row0 + g.rows;
+      wp += (int64_t)g.expert * N * (K / 2);
+      sp += (int64_t)g.expert * N * (K / 32);
+    } else {
+      uint32_t tm, tn;
+      band(t, tiles_m, tiles_n, tm, tn);
+      m0 = (int64_t)T::BM * tm;
+      n0 = (int64_t)T::BN * tn;
+      mend = M;
+    }
+  }
+  const uint32_t half = (uint32_t)(K / 2), kb = (uint32_t)(K / 32);
+  const int mrows = (int)(mend - m0 < T::BM ? mend - m0 : T::BM);
+  const int nrows = (int)(N - n0 < T::BN ? N - n0 : T::BN);
+
+  // Rows past the tile's are past the resource and read as zero.
+  const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(xq + m0 * half), mrows * half);
+  const __amdgpu_buffer_rsrc_t br = buf_rsrc_n(uniform_ptr(wp + n0 * half), nrows * half);
+  const __amdgpu_buffer_rsrc_t asr = buf_rsrc_n(uniform_ptr(xs + m0 * kb), mrows * kb);
+  const __amdgpu_buffer_rsrc_t bsr = buf_rsrc_n(uniform_ptr(sp + n0 * kb), nrows * kb);
+
+  // ---- memory -> LDS, 8 rows x 128 bytes per load.  Lane l writes the 16
+  // bytes at 16 l: row l / 8, slot l % 8.  Slot s of row r holds chunk
+  // s ^ ((r / 2) % 8) of the row's eight, so that the 16 rows a fragment read
+  // touches at once lie in 16 different places of 256 bytes.
+  const int lrow = lane >> 3, slot = lane & 7;
+  uint32_t ao[LA], bo[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i) {
+    const int row = 8 * (w * LA + i) + lrow;
+    ao[i] = (uint32_t)row * half + 16u * (slot ^ ((row >> 1) & 7));
+  }
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    const int row = 8 * (w * LB + i) + lrow;
+    bo[i] = (uint32_t)row * half + 16u * (slot ^ ((row >> 1) & 7));
+  }
+  const int nks = (int)((half + kStepBytes - 1) / kStepBytes);
+  // The step is part of the checked offset, so nothing past the tile's rows is
+  // read.  K % 256 == 128: the last step's second half is the next row's; its
+  // scales, both operands', read as 2^-127, and the products, below 2^-240,
+  // add nothing.  Steps past the last one lie outside the resource.
+  auto issue = [&](int ks, int stage) {
+    uint8_t* base = smx + stage * T::STAGE;
+    const uint32_t o = ks < nks ? (uint32_t)ks * kStepBytes : kPastEnd;
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      load_lds(ar, base + 1024 * (w * LA + i), ao[i] + o);
+#pragma unroll
+    for (int i = 0; i < LB; ++i)
+      load_lds(br, base + T::A_STAGE + 1024 * (w * LB + i), bo[i] + o);
+  };
+
+  // ---- scales: lane (r, h) of fragment f loads 16 of the 32 scale bytes of
+  // row r for four K steps; two exchanges between the wave's halves leave it
+  // with one word a step, the scales of blocks 4 h .. 4 h + 3 of that step.
+  const int r = lane & 31, h = lane >> 5;
+  auto scale_load = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t row, int chunk) -> u32x4 {
+    const uint32_t o = 32u * chunk + 16u * h;
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, row * kb + o, 0, 0));
+  };
+  // Words past the row's end (the next row's, or zero past the resource, whose
+  // end is checked word by word) become zero, which is 2^-127.
+  auto scale_mask = [&](u32x4 v, int chunk) -> u32x4 {
+    const int left = (int)kb - 32 * chunk - 16 * h;  // scale bytes of the row from the lane's first on
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 4 * i < left ? v[i] : 0u;
+    return v;
+  };
+  auto exchange = [&](u32x4 v) -> u32x4 {
+    const auto p = __builtin_amdgcn_permlane32_swap(v.x, v.y, false, false);
+    const auto q = __builtin_amdgcn_permlane32_swap(v.z, v.w, false, false);
+    return u32x4{p[0], q[0], p[1], q[1]};  // steps 0, 1, 2, 3
+  };
+  u32x4 sa[MI], sb[NJ], na[MI], nb[NJ];
+  auto scales_issue = [&](int chunk) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) na[i] = scale_load(asr, 32 * (wm * MI + i) + r, chunk);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) nb[j] = scale_load(bsr, 32 * (wn * NJ + j) + r, chunk);
+  };
+
+  f32x16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  // fragment addresses: chunk 4 h + J of row r
+  const int x = (r >> 1) & 7;
+  const uint8_t* af = smx + (32 * MI * wm + r) * kStepBytes;
+  const uint8_t* bf = smx + T::A_STAGE + (32 * NJ * wn + r) * kStepBytes;
+  int fo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) fo[j] = 16 * ((4 * h + j) ^ x);
+  // Fragments of quarter J of a K step, in two register sets: the reads of a
+  // quarter run under the previous quarter's MFMAs.
+  u32x4 av[2][MI], bv[2][NJ];
+  auto frag = [&](int stage, auto jc) {
+    constexpr int J = decltype(jc)::value;
+    const uint8_t* a = af + stage * T::STAGE + fo[J];
+    const uint8_t* b = bf + stage * T::STAGE + fo[J];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) av[J & 1][i] = *(const u32x4*)(a + 32 * kStepBytes * i);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bv[J & 1][j] = *(const u32x4*)(b + 32 * kStepBytes * j);
+  };
+  auto mma = [&](auto jc, auto uc) {
+    constexpr int J = decltype(jc)::value, U = decltype(uc)::value;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mx_mfma<J>(bv[J & 1][j], av[J & 1][i], acc[i][j], sb[j][U], sa[i][U]);
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  constexpr std::integral_constant<int, 2> c2{};
+  constexpr std::integral_constant<int, 3> c3{};
+
+  scales_issue(0);
+#pragma unroll
+  for (int p = 0; p < S; ++p) issue(p, p);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) na[i] = exchange(scale_mask(na[i], 0));
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) nb[j] = exchange(scale_mask(nb[j], 0));
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  frag(0, c0);
+
+  // One K step.  Before its last quarter every wave has read all of the
+  // step's stage into registers and waited for its own share of the next
+  // stage; behind the barrier the next stage is whole and this one is free.
+  // Nothing here is conditional on the accumulators' path: a branch around
+  // MFMAs would make the compiler move 256 accumulators where it joins.
+  auto step = [&](int ks, auto u) {
+    constexpr int U = decltype(u)::value;
+    const int stage = ks % S;
+    if constexpr (U == 0) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sa[i] = na[i];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sb[j] = nb[j];
+    }
+    frag(stage, c1);
+    mma(c0, u);
+    __builtin_amdgcn_sched_barrier(0);
+    frag(stage, c2);
+    mma(c1, u);
+    __builtin_amdgcn_sched_barrier(0);
+    frag(stage, c3);
+    mma(c2, u);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if constexpr (U == 3) {  // the scales have arrived; their exchange waits for no newer load here
+#pragma unroll
+      for (int i = 0; i < MI; ++i) na[i] = exchange(scale_mask(na[i], ks / 4 + 1));
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) nb[j] = exchange(scale_mask(nb[j], ks / 4 + 1));
+    }
+    if constexpr (U == 0) scales_issue(ks / 4 + 1);
+    issue(ks + S, stage);
+    frag((ks + 1) % S, c0);
+    mma(c3, u);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int ks = 0;
+  for (; ks + 4 <= nks; ks += 4) {
+    step(ks, c0);
+    step(ks + 1, c1);
+    step(ks + 2, c2);
+    step(ks + 3, c3);
+  }
+  if (ks < nks) {
+    step(ks, c0);
+    if (ks + 1 < nks) {
+      step(ks + 1, c1);
+      if (ks + 2 < nks) step(ks + 2, c2);
+    }
+  }
+
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
+
+  // ---- results.  Register e of acc[i][j] holds y row r, column 8 (e / 4) +
+  // 4 h + e % 4 of its 32 x 32 block (the weights are the first operand), so
+  // four registers are four consecutive columns.  Each wave turns 32 rows at
+  // a time around in its own part of LDS and stores them in whole rows of 16
+  // bytes a lane; stores of single elements took three times as long.  Slot
+  // c ^ (row % SW) of a row holds its 16-byte chunk c: no bank conflicts.
+  __builtin_amdgcn_s_barrier();  // every wave is done with its fragments
+  constexpr int CB = 32 * NJ * (int)sizeof(TY);  // bytes of a row of the wave's block
+  constexpr int CH = CB / 16;                    // its chunks
+  constexpr int SW = (CH & -CH) < 16 ? (CH & -CH) : 16;
+  constexpr int PER = 16 / (int)sizeof(TY);      // elements of a chunk
+  static_assert(T::NW * 32 * CB <= (int)T::lds, "the waves' turning places fit in LDS");
+  uint8_t* turn = smx + w * 32 * CB;
+  const int64_t mb = m0 + 32 * MI * wm, nb0 = n0 + 32 * NJ * wn;
+  const bool wide = N % PER == 0;  // rows of y start at 16-byte addresses
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
+                    v3 = acc[i][j][4 * q + 3];
+        const int col = 32 * j + 8 * q + 4 * h;
+        uint8_t* dst = turn + r * CB + 16 * ((col / PER) ^ (r & (SW - 1)));
+        if constexpr (sizeof(TY) == 4) {
+          *(f32x4*)dst = f32x4{v0, v1, v2, v3};
+        } else {
+          u32x2 b;
+          b.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v0, (__bf16)v1});
+          b.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v2, (__bf16)v3});
+          *(u32x2*)(dst + 8 * h) = b;
+        }
+      }
+    if (wide) {
+#pragma unroll
+      for (int t = 0; t < 32 * CH / 64; ++t) {
+        const int at = 64 * t + lane, row = at / CH, c = at % CH;
+        const u32x4 v = *(const u32x4*)(turn + row * CB + 16 * (c ^ (row & (SW - 1))));
+        const int64_t m = mb + 32 * i + row, n = nb0 + PER * c;
+        if (m < mend && n < N) *(u32x4*)((TY*)y + m * N + n) = v;
+      }
+    } else {
+      for (int at = lane; at < 32 * 32 * NJ; at += 64) {
+        const int row = at / (32 * NJ), col = at % (32 * NJ);
+        const TY v = *(const TY*)(turn + row * CB + 16 * ((col / PER) ^ (row & (SW - 1))) + sizeof(TY) * (col % PER));
+        const int64_t m = mb + 32 * i + row, n = nb0 + col;
+        if (m < mend && n < N) ((TY*)y)[m * N + n] = v;
+      }
+    }
+  }
+}
+
+bool mx_gemm_fits(int64_t k) { return k % 128 == 0; }
+
+template <typename T, typename TY, bool GROUPED>
+static hipError_t mx_gemm_go(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                             const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts,
+                             hipStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
+  const hipError_t e = once_per_device(attr_done, [] {
+    return hipFuncSetAttribute((const void*)k_mx_gemm<T, TY, GROUPED>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)T::lds);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t tiles_m = GROUPED ? grouped_max_tiles(m, experts, T::BM) : (m + T::BM - 1) / T::BM;
+  const int64_t tiles_n = (n + T::BN - 1) / T::BN;
+  const int64_t grid = (tiles_m * tiles_n + 7) / 8 * 8;
+  k_mx_gemm<T, TY, GROUPED><<<dim3((unsigned)grid), T::NT, T::lds, st>>>(xq, xs, m, k, packed, scales, n, y, offsets,
+                                                                       experts, (uint32_t)tiles_m, (uint32_t)tiles_n);
+  return hipGetLastError();
+}
+
+#ifndef MX_CFG
+#define MX_CFG 256, 256, 2, 2, 2
+#endif
+template <typename TY>
+static hipError_t mx_gemm_pick(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                               const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts,
+                               hipStream_t st) {
+  typedef MxTile<MX_CFG> T;
+  if (offsets != nullptr) return mx_gemm_go<T, TY, true>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  return mx_gemm_go<T, TY, false>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+}
+
+hipError_t launch_mx_gemm(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                          const uint8_t* scales, int64_t n, void* y, int y_dtype, const int* offsets, int experts,
+                          hipStream_t st) {
+  if (y_dtype == W4_F32) return mx_gemm_pick<float>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  return mx_gemm_pick<__bf16>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+}
+
+}  // namespace w4
