@@ -37,6 +37,18 @@ __device__ __forceinline__ f32x16 mx_mfma(u32x4 a, u32x4 b, f32x16 c, uint32_t s
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
+// Orders R LDS reads among the M MFMAs that precede this call: at most 15 reads
+// of a wave can be outstanding, and one more would hold up the MFMAs behind it.
+template <int M, int R>
+__device__ __forceinline__ void interleave() {
+  if constexpr (M > 0 && R > 0) {
+    constexpr int per = (R + M - 1) / M;
+    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    interleave<M - 1, R - per>();
+  }
+}
+
 // Tile t of tiles_m x tiles_n in bands of 8 M tiles (the last may have fewer).
 __device__ __forceinline__ void band(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
   const uint32_t b = t / (8 * tiles_n), in = t - b * 8 * tiles_n;
@@ -187,24 +199,24 @@ __global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict_
   int fo[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) fo[j] = 16 * ((4 * h + j) ^ x);
-  // Fragments of quarter J of a K step, in two register sets: the reads of a
-  // quarter run under the previous quarter's MFMAs.
-  u32x4 av[2][MI], bv[2][NJ];
+  // Fragments of the four quarters of a K step.
+  u32x4 av[4][MI], bv[4][NJ];
   auto frag = [&](int stage, auto jc) {
     constexpr int J = decltype(jc)::value;
     const uint8_t* a = af + stage * T::STAGE + fo[J];
     const uint8_t* b = bf + stage * T::STAGE + fo[J];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) av[J & 1][i] = *(const u32x4*)(a + 32 * kStepBytes * i);
+    for (int i = 0; i < MI; ++i) av[J][i] = *(const u32x4*)(a + 32 * kStepBytes * i);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) bv[J & 1][j] = *(const u32x4*)(b + 32 * kStepBytes * j);
+    for (int j = 0; j < NJ; ++j) bv[J][j] = *(const u32x4*)(b + 32 * kStepBytes * j);
   };
-  auto mma = [&](auto jc, auto uc) {
+  // rows i0 .. i1 - 1 of the wave's block, quarter J of a step
+  auto mma = [&](auto jc, auto uc, int i0, int i1) {
     constexpr int J = decltype(jc)::value, U = decltype(uc)::value;
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = i0; i < i1; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mx_mfma<J>(bv[J & 1][j], av[J & 1][i], acc[i][j], sb[j][U], sa[i][U]);
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mx_mfma<J>(bv[J][j], av[J][i], acc[i][j], sb[j][U], sa[i][U]);
   };
   constexpr std::integral_constant<int, 0> c0{};
   constexpr std::integral_constant<int, 1> c1{};
@@ -218,16 +230,20 @@ __global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict_
   for (int i = 0; i < MI; ++i) na[i] = exchange(scale_mask(na[i], 0));
 #pragma unroll
   for (int j = 0; j < NJ; ++j) nb[j] = exchange(scale_mask(nb[j], 0));
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * (LA + LB)) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   frag(0, c0);
 
-  // One K step.  Before its last quarter every wave has read all of the
-  // step's stage into registers and waited for its own share of the next
-  // stage; behind the barrier the next stage is whole and this one is free.
-  // Nothing here is conditional on the accumulators' path: a branch around
-  // MFMAs would make the compiler move 256 accumulators where it joins.
+  // One K step, with two barriers.  Every wave reads all of the stage into
+  // registers under the MFMAs of the first quarter and a half; behind the
+  // first barrier the stage is free and the step S further on is loaded into
+  // it.  Before the last MFMAs each wave waits for its own share of the next
+  // stage, which the second barrier makes whole, and reads its first quarter.
+  // So a load has almost one and a half steps to arrive (with one barrier it
+  // had one, and the step took as long as the load).  Nothing here is
+  // conditional: a branch around MFMAs would make the compiler move 256
+  // accumulators where it joins.
   auto step = [&](int ks, auto u) {
     constexpr int U = decltype(u)::value;
     const int stage = ks % S;
@@ -238,27 +254,40 @@ __global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict_
       for (int j = 0; j < NJ; ++j) sb[j] = nb[j];
     }
     frag(stage, c1);
-    mma(c0, u);
-    __builtin_amdgcn_sched_barrier(0);
     frag(stage, c2);
-    mma(c1, u);
+    mma(c0, u, 0, MI);
+    interleave<MI * NJ, 2 * (MI + NJ)>();
     __builtin_amdgcn_sched_barrier(0);
     frag(stage, c3);
-    mma(c2, u);
+    mma(c1, u, 0, MI / 2);
+    interleave<MI * NJ / 2, MI + NJ>();
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    mma(c1, u, MI / 2, MI);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if constexpr (U == 3) {  // the scales have arrived; their exchange waits for no newer load here
+    if constexpr (U == 0) {
+      scales_issue(ks / 4 + 1);
+      __builtin_amdgcn_sched_barrier(0);  // before the stage's loads, which the second wait leaves outstanding
+    }
+    issue(ks + S, stage);
+    mma(c2, u, 0, MI);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (U == 3) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) na[i] = exchange(scale_mask(na[i], ks / 4 + 1));
 #pragma unroll
       for (int j = 0; j < NJ; ++j) nb[j] = exchange(scale_mask(nb[j], ks / 4 + 1));
     }
-    if constexpr (U == 0) scales_issue(ks / 4 + 1);
-    issue(ks + S, stage);
+    mma(c3, u, 0, MI / 2);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * (LA + LB)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     frag((ks + 1) % S, c0);
-    mma(c3, u);
+    mma(c3, u, MI / 2, MI);
+    interleave<MI * NJ / 2, MI + NJ>();
     __builtin_amdgcn_sched_barrier(0);
   };
   int ks = 0;
@@ -351,23 +380,53 @@ static hipError_t mx_gemm_go(const uint8_t* xq, const uint8_t* xs, int64_t m, in
   return hipGetLastError();
 }
 
-#ifndef MX_CFG
-#define MX_CFG 256, 256, 2, 2, 2
-#endif
-template <typename TY>
+// Workgroup tiles.  The first two have a CU to themselves (128 and 112 KB of
+// LDS), of the third two share one.
+typedef MxTile<256, 256, 2, 2, 2> MxLarge;
+typedef MxTile<256, 192, 2, 2, 2> MxNarrow;
+typedef MxTile<128, 128, 2, 2, 2> MxSmall;
+
+// Time of all tiles in rounds of a large tile a CU.  Measured, K = 4096 to
+// 16384: a round of narrow tiles takes 0.88 of a round of large ones ([11008,
+// 4096], 2048 rows: 58 us in two rounds against 66), a round of small ones
+// with two a CU 0.68, with one a CU 0.45 ([11008, 4096], 128 rows: 15 us
+// against 31).
+static double mx_rounds(int64_t tiles, int64_t slots, double each) {
+  return (double)((tiles + slots - 1) / slots) * each;
+}
+
+template <typename TY, bool GROUPED>
 static hipError_t mx_gemm_pick(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                                const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts,
                                hipStream_t st) {
-  typedef MxTile<MX_CFG> T;
-  if (offsets != nullptr) return mx_gemm_go<T, TY, true>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
-  return mx_gemm_go<T, TY, false>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  // by expert each one's last tile is half full on average
+  auto tiles = [&](int bm, int bn) {
+    const int64_t tm = GROUPED ? m / bm + ((experts < m ? experts : m) + 1) / 2 : (m + bm - 1) / bm;
+    return tm * ((n + bn - 1) / bn);
+  };
+  const int64_t small = tiles(128, 128);
+  const double large_t = mx_rounds(tiles(256, 256), 256, 1.0), narrow_t = mx_rounds(tiles(256, 192), 256, 0.88),
+               small_t = small <= 256 ? 0.45 : mx_rounds(small, 512, 0.68);
+  if (small_t <= large_t && small_t <= narrow_t)
+    return mx_gemm_go<MxSmall, TY, GROUPED>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  if (narrow_t < large_t)
+    return mx_gemm_go<MxNarrow, TY, GROUPED>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  return mx_gemm_go<MxLarge, TY, GROUPED>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+}
+
+template <typename TY>
+static hipError_t mx_gemm_form(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
+                               const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts,
+                               hipStream_t st) {
+  if (offsets != nullptr) return mx_gemm_pick<TY, true>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  return mx_gemm_pick<TY, false>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
 }
 
 hipError_t launch_mx_gemm(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                           const uint8_t* scales, int64_t n, void* y, int y_dtype, const int* offsets, int experts,
                           hipStream_t st) {
-  if (y_dtype == W4_F32) return mx_gemm_pick<float>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
-  return mx_gemm_pick<__bf16>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  if (y_dtype == W4_F32) return mx_gemm_form<float>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
+  return mx_gemm_form<__bf16>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
 }
 
 }  // namespace w4
