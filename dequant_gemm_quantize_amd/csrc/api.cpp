@@ -564,6 +564,10 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
+  if (x_dtype == W4_BF16 && t / experts > 16 && w4::w4a16_grouped_gemm_fits(k))
+    return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
+                                                    n, group_size, y, y_dtype, stream),
+                      fn);
   return hip_status(w4::launch_w4a16_grouped(x, x_dtype, t, k, offsets, (int)experts, packed, scales, zeros,
                                              sz_dtype, n, group_size, y, y_dtype, stream),
                     fn);

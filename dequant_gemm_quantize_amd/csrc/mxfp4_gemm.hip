@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "grouped.h"
+#include "lds_gemm.h"
 #include "w4_common.h"
 #include "w4_internal.h"
 
@@ -17,17 +18,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStepBytes = 128;  // a K step: 256 columns, one 128-byte line of a row
 
-// Raw buffer resource that answers reads past `bytes` with zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc_n(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-
-// 16 bytes a lane from the resource at the lane's offset to LDS at dst + 16
-// lane (dst the same in every lane), without passing through registers.
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
-}
-
 __device__ __forceinline__ i32x8 mx_operand(u32x4 v) {
   return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
@@ -36,28 +26,6 @@ template <int J>
 __device__ __forceinline__ f32x16 mx_mfma(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, J, (int)sa, J, (int)sb);
 }
-
-// Orders R LDS reads among the M MFMAs that precede this call: at most 15 reads
-// of a wave can be outstanding, and one more would hold up the MFMAs behind it.
-template <int M, int R>
-__device__ __forceinline__ void interleave() {
-  if constexpr (M > 0 && R > 0) {
-    constexpr int per = (R + M - 1) / M;
-    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    interleave<M - 1, R - per>();
-  }
-}
-
-// Tile t of tiles_m x tiles_n in bands of 8 M tiles (the last may have fewer).
-__device__ __forceinline__ void band(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
-  const uint32_t b = t / (8 * tiles_n), in = t - b * 8 * tiles_n;
-  const uint32_t width = tiles_m - 8 * b < 8 ? tiles_m - 8 * b : 8;
-  tn = in / width;
-  tm = 8 * b + in % width;
-}
-
-constexpr uint32_t kPastEnd = 0x80000000u;  // beyond every resource: their sizes stay below 2^31
 
 // Workgroup tile BM x BN of WR x WC waves, each 32 MI x 32 NJ outputs.
 template <int BM_, int BN_, int WR_, int WC_, int S_> struct MxTile {
@@ -307,57 +275,10 @@ __global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict_
 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
 
-  // ---- results.  Register e of acc[i][j] holds y row r, column 8 (e / 4) +
-  // 4 h + e % 4 of its 32 x 32 block (the weights are the first operand), so
-  // four registers are four consecutive columns.  Each wave turns 32 rows at
-  // a time around in its own part of LDS and stores them in whole rows of 16
-  // bytes a lane; stores of single elements took three times as long.  Slot
-  // c ^ (row % SW) of a row holds its 16-byte chunk c: no bank conflicts.
   __builtin_amdgcn_s_barrier();  // every wave is done with its fragments
-  constexpr int CB = 32 * NJ * (int)sizeof(TY);  // bytes of a row of the wave's block
-  constexpr int CH = CB / 16;                    // its chunks
-  constexpr int SW = (CH & -CH) < 16 ? (CH & -CH) : 16;
-  constexpr int PER = 16 / (int)sizeof(TY);      // elements of a chunk
-  static_assert(T::NW * 32 * CB <= (int)T::lds, "the waves' turning places fit in LDS");
-  uint8_t* turn = smx + w * 32 * CB;
-  const int64_t mb = m0 + 32 * MI * wm, nb0 = n0 + 32 * NJ * wn;
-  const bool wide = N % PER == 0;  // rows of y start at 16-byte addresses
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
-                    v3 = acc[i][j][4 * q + 3];
-        const int col = 32 * j + 8 * q + 4 * h;
-        uint8_t* dst = turn + r * CB + 16 * ((col / PER) ^ (r & (SW - 1)));
-        if constexpr (sizeof(TY) == 4) {
-          *(f32x4*)dst = f32x4{v0, v1, v2, v3};
-        } else {
-          u32x2 b;
-          b.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v0, (__bf16)v1});
-          b.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v2, (__bf16)v3});
-          *(u32x2*)(dst + 8 * h) = b;
-        }
-      }
-    if (wide) {
-#pragma unroll
-      for (int t = 0; t < 32 * CH / 64; ++t) {
-        const int at = 64 * t + lane, row = at / CH, c = at % CH;
-        const u32x4 v = *(const u32x4*)(turn + row * CB + 16 * (c ^ (row & (SW - 1))));
-        const int64_t m = mb + 32 * i + row, n = nb0 + PER * c;
-        if (m < mend && n < N) *(u32x4*)((TY*)y + m * N + n) = v;
-      }
-    } else {
-      for (int at = lane; at < 32 * 32 * NJ; at += 64) {
-        const int row = at / (32 * NJ), col = at % (32 * NJ);
-        const TY v = *(const TY*)(turn + row * CB + 16 * ((col / PER) ^ (row & (SW - 1))) + sizeof(TY) * (col % PER));
-        const int64_t m = mb + 32 * i + row, n = nb0 + col;
-        if (m < mend && n < N) ((TY*)y)[m * N + n] = v;
-      }
-    }
-  }
+  constexpr int TURN = turn_bytes<TY, NJ>();
+  static_assert(T::NW * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
+  turn_store<TY, MI, NJ>(smx + w * TURN, lane, acc, (TY*)y, N, m0 + 32 * MI * wm, mend, n0 + 32 * NJ * wn);
 }
 
 bool mx_gemm_fits(int64_t k) { return k % 128 == 0; }

@@ -125,6 +125,10 @@ hipError_t launch_mx_gemm(const uint8_t* xq, const uint8_t* xs, int64_t m, int64
 hipError_t launch_w4a16_grouped(const void* x, int x_dtype, int64_t t, int64_t k, const int* offsets,
                                 int experts, const uint8_t* packed, const void* scales, const void* zeros,
                                 int sz_dtype, int64_t n, int g, void* y, int y_dtype, hipStream_t st);
+bool w4a16_grouped_gemm_fits(int64_t k);
+hipError_t launch_w4a16_grouped_gemm(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
+                                     const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
+                                     int64_t n, int g, void* y, int y_dtype, hipStream_t st);
 // Limits of the products by expert: tile numbers stay below 2^31.
 constexpr int64_t kGroupedMaxRows = (int64_t)1 << 24;
 constexpr int64_t kGroupedMaxExperts = 65536;
