@@ -447,6 +447,9 @@ int w4a8_matmul_ws(const int8_t* xq, const float* x_scale, int64_t m, int64_t k,
                      group_size, y, y_dtype, workspace, workspace_bytes, stream);
 }
 
+#ifndef GROUPED_ROWS
+#define GROUPED_ROWS 16
+#endif
 // ---- microscaled 4-bit floating point and the products by expert ---------------
 
 // Block scales (one byte each): the pointer itself is 4-byte aligned.
@@ -508,7 +511,10 @@ static int mx_product(const char* fn, const uint8_t* xq, const uint8_t* xs, int6
                       const int32_t* offsets, int64_t experts, const uint8_t* packed, const uint8_t* scales,
                       int64_t n, void* y, int y_dtype, hipStream_t stream) {
   const int64_t rows = offsets != nullptr ? m / experts : m;
-  if (rows > 64 && w4::mx_gemm_fits(k))
+#ifndef MXR
+#define MXR 64
+#endif
+  if (rows > MXR && w4::mx_gemm_fits(k))
     return hip_status(w4::launch_mx_gemm(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
                       fn);
   return hip_status(w4::launch_mx_rows(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
@@ -564,12 +570,17 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
-  if (x_dtype == W4_BF16 && t / experts > 16 && w4::w4a16_grouped_gemm_fits(k))
+  // float32 x: multiply-adds; bf16 x: by the rows that an expert has on average
+  if (x_dtype == W4_F32)
+    return hip_status(w4::launch_w4a16_grouped_f32(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
+                                                   n, group_size, y, y_dtype, stream),
+                      fn);
+  if (t / experts > GROUPED_ROWS && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);
-  return hip_status(w4::launch_w4a16_grouped(x, x_dtype, t, k, offsets, (int)experts, packed, scales, zeros,
-                                             sz_dtype, n, group_size, y, y_dtype, stream),
+  return hip_status(w4::launch_w4a16_grouped_rows(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype, n,
+                                                  group_size, y, y_dtype, stream),
                     fn);
 }
 

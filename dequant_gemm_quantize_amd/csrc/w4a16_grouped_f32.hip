@@ -1,15 +1,12 @@
-// W4A16 product by expert (rows of x grouped by expert, group-wise INT4
-// weights of each expert):
+// W4A16 product by expert with float32 x (small layers and checks): rows of x
+// grouped by expert, group-wise INT4 weights of each expert,
 //   y[t, n] = sum over groups j of s[e, n, j] * sum_{k in j} x[t, k] (q[e, n, k] - zp[e, n, j])
-// for the expert e that owns row t.
+// for the expert e that owns row t, in float32 multiply-adds.
 //
-// k_w4a16_grouped_any: any shape, float32 or bf16 x, float32 multiply-adds.
-// A wave has 64 weight rows, one a lane, and 4 token rows, whose x is the
-// same address in every lane; each lane reads its row in 16-byte pieces of 32
+// A wave has 64 weight rows, one a lane, and 4 token rows, whose x is the same
+// address in every lane; each lane reads its row in 16-byte pieces of 32
 // codes, which lie in one group.  q - zp is an exact small integer, and the
 // group's scale multiplies the float32 sum of 32 columns.
-#include <type_traits>
-
 #include "grouped.h"
 #include "w4_common.h"
 #include "w4_internal.h"
@@ -18,18 +15,12 @@ namespace w4 {
 
 namespace {
 
-constexpr int kAnyGrid = 1 << 20;  // workgroups; more tiles than that loop
-
-template <typename TX>
-__device__ __forceinline__ float x_at(const TX* x, int i) {
-  if constexpr (sizeof(TX) == 4) return x[i];
-  else return bf16_bits_to_f32(x[i]);
-}
+constexpr int kF32Grid = 1 << 20;  // workgroups; more tiles than that loop
 
 }  // namespace
 
-template <typename TX, typename TS, typename TY>
-__global__ __launch_bounds__(256) void k_w4a16_grouped_any(const TX* __restrict__ x, int64_t T, int64_t K,
+template <typename TS, typename TY>
+__global__ __launch_bounds__(256) void k_w4a16_grouped_f32(const float* __restrict__ x, int64_t T, int64_t K,
                                                            const int* __restrict__ offsets, int experts,
                                                            const uint8_t* __restrict__ packed,
                                                            const void* __restrict__ scales,
@@ -47,7 +38,7 @@ __global__ __launch_bounds__(256) void k_w4a16_grouped_any(const TX* __restrict_
     if (r0 >= rend) continue;
     const int64_t row = (int64_t)gt.expert * N + (n < N ? n : N - 1);
     const u32x4* wp = (const u32x4*)(packed + row * (K / 2));
-    const TX* xp[4];
+    const float* xp[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) xp[i] = x + (r0 + i < rend ? r0 + i : rend - 1) * K;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -60,7 +51,7 @@ __global__ __launch_bounds__(256) void k_w4a16_grouped_any(const TX* __restrict_
       for (int j = 0; j < 32; ++j) {
         const float q = (float)((p[j >> 3] >> (4 * (j & 7))) & 15u) - z;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = fmaf(x_at(xp[i], (int)(32 * b) + j), q, sum[i]);
+        for (int i = 0; i < 4; ++i) sum[i] = fmaf(xp[i][32 * b + j], q, sum[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, sum[i], acc[i]);
@@ -76,35 +67,26 @@ __global__ __launch_bounds__(256) void k_w4a16_grouped_any(const TX* __restrict_
   }
 }
 
-template <typename TX, typename TS, typename TY>
-static hipError_t any_go(const void* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
+template <typename TS, typename TY>
+static hipError_t f32_go(const void* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
                          const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
   const int64_t tiles_n = (n + 63) / 64, tiles = grouped_max_tiles(t, experts, 16) * tiles_n;
-  const dim3 grid((unsigned)(tiles < kAnyGrid ? tiles : kAnyGrid));
-  k_w4a16_grouped_any<TX, TS, TY><<<grid, 256, 0, st>>>((const TX*)x, t, k, offsets, experts, packed, scales, zeros,
-                                                       n, g, (TY*)y, (uint32_t)tiles_n, tiles);
+  const dim3 grid((unsigned)(tiles < kF32Grid ? tiles : kF32Grid));
+  k_w4a16_grouped_f32<TS, TY><<<grid, 256, 0, st>>>((const float*)x, t, k, offsets, experts, packed, scales, zeros, n, g,
+                                                   (TY*)y, (uint32_t)tiles_n, tiles);
   return hipGetLastError();
 }
 
-template <typename TX>
-static hipError_t any_pick(const void* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
-                           const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y, int y_dtype,
-                           hipStream_t st) {
+hipError_t launch_w4a16_grouped_f32(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
+                                    const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
+                                    int64_t n, int g, void* y, int y_dtype, hipStream_t st) {
   if (sz_dtype == W4_F16) {
     if (y_dtype == W4_F32)
-      return any_go<TX, _Float16, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    return any_go<TX, _Float16, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+      return f32_go<_Float16, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return f32_go<_Float16, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
   }
-  if (y_dtype == W4_F32) return any_go<TX, float, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return any_go<TX, float, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-}
-
-hipError_t launch_w4a16_grouped(const void* x, int x_dtype, int64_t t, int64_t k, const int* offsets, int experts,
-                                const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype, int64_t n,
-                                int g, void* y, int y_dtype, hipStream_t st) {
-  if (x_dtype == W4_F32)
-    return any_pick<float>(x, t, k, offsets, experts, packed, scales, zeros, sz_dtype, n, g, y, y_dtype, st);
-  return any_pick<uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, sz_dtype, n, g, y, y_dtype, st);
+  if (y_dtype == W4_F32) return f32_go<float, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return f32_go<float, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 }  // namespace w4

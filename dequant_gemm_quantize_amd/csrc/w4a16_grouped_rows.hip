@@ -1,0 +1,319 @@
+// W4A16 product by expert for few rows an expert (decode), bf16 x:
+//   y[t, n] = sum over groups j of s (sum_{k in j} x (16 + q) - (16 + zp) sum_{k in j} x)
+// on v_mfma_f32_16x16x32_bf16 (16 token rows, 16 weight rows).  16 + q is an
+// exact bfloat16 whose mantissa bits 3..6 are the code: a shift and an and-or
+// make a pair of operands, codes i and i + 4 of a word (x is put into that
+// order once a slice).  The sums of x come from the same instruction against
+// ones.  Nothing is rounded below float32; 16 rather than 128 + q keeps the
+// part that cancels small.
+//
+// Bound by the weight bytes, and close behind by the vector unit that turns
+// codes into operands.  A workgroup goes through RB blocks of 16 weight rows of
+// one expert, all of K, for up to 16 token rows (one block a workgroup was
+// slower: starting the waves, about 13 cycles each on every XCD, then takes
+// longer than reading the weights).  Its waves have a 256-column slice of K each
+// (or take such slices in turn): a wave keeps x of its slice, and its sums, in
+// registers for all the blocks, and the codes and scales of the next blocks are
+// in flight while one is computed.  The waves add their sums through LDS at the
+// end.  Slices of 256 rather than 512 columns halve a wave's registers, so that
+// a CU holds 16 waves and not 8.
+//
+// The codes are loaded as 128-byte runs of a row and regrouped through the
+// wave's own 2 KB of LDS (row t's 16-byte piece c at slot c ^ ((t / 2) % 8),
+// free of bank conflicts; LDS operations of a wave complete in order).  G128
+// (groups of a multiple of 128): lane (l16, h) has piece 4 j + h of row l16, a
+// 32-column block of each 128 columns, and x's columns to match.  Otherwise a
+// group may end at any 32-column block, so an MFMA takes one block, of which
+// lane (l16, h) has 8 columns.
+#include <type_traits>
+
+#include "grouped.h"
+#include "lds_gemm.h"
+#include "w4_common.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kGRowsGrid = 1 << 20;  // workgroups; more tiles than that loop
+
+// mask and magic of the conversion, kept in registers (w4_common.h, NibConst)
+struct Nib16 {
+  uint32_t mask, magic;
+  __device__ static Nib16 make() {
+    Nib16 k{0x00780078u, 0x41804180u};
+    asm("" : "+v"(k.mask), "+v"(k.magic));
+    return k;
+  }
+};
+
+// 8 codes -> 16 + q as bf16 in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ bf16x8 codes16(uint32_t p, const Nib16& nk) {
+  u32x4 r;
+  r.x = ((p << 3) & nk.mask) | nk.magic;
+  r.y = ((p >> 1) & nk.mask) | nk.magic;
+  r.z = ((p >> 5) & nk.mask) | nk.magic;
+  r.w = ((p >> 9) & nk.mask) | nk.magic;
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// 8 consecutive bf16 into that order.
+__device__ __forceinline__ bf16x8 order_as_codes(u32x4 v) {
+  u32x4 r;
+  r.x = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);  // 0 4
+  r.y = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);  // 1 5
+  r.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);  // 2 6
+  r.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);  // 3 7
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// The value that each of the wave's four rows of 16 lanes holds, in every row.
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&out)[4]) {
+  const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // rows 0 1 0 1 and 2 3 2 3
+  const auto lo = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+  out[0] = lo[0], out[1] = lo[1], out[2] = hi[0], out[3] = hi[1];
+}
+
+template <typename TS>
+__device__ __forceinline__ float scale_value(uint32_t v) {
+  if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+  else return __uint_as_float(v);
+}
+
+}  // namespace
+
+// SL: 32-column blocks of a wave's slice, 16 or 8.
+template <typename TS, typename TY, bool G128, int SL, int RB>
+__global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a16_grouped_rows(
+    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
+    const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
+    int g, TY* __restrict__ y, uint32_t tiles_n, int64_t tiles) {
+  // [waves][16 tokens][16 RB rows] sums; before them 256 SL bytes a wave to regroup weights
+  extern __shared__ __attribute__((aligned(16))) float part[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6;
+  const int l16 = lane & 15, h = lane >> 4;
+  constexpr int RPL = 64 / SL, NC = 16 / RPL;  // rows a load covers, loads a block
+  const int lp = lane % SL, lr = lane / SL;    // the lane's piece and row of them
+  const uint32_t ng = (uint32_t)(K / g), half = (uint32_t)(K / 2), xrow = (uint32_t)(2 * K);
+  const int blocks32 = (int)(K / 32), slices = (blocks32 + SL - 1) / SL;
+  const uint32_t bpg = (uint32_t)g / 32;
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+  const Nib16 nk = Nib16::make();
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int NS = G128 ? SL / 4 : SL;  // scales of a row in a slice
+  constexpr int D = RB < (G128 ? 3 : 2) ? RB : (G128 ? 3 : 2);  // blocks whose codes are held at a time
+  constexpr int NL = 2 * NS / 4;    // loads of them, a scale or zero-point a lane
+  typedef typename std::conditional<sizeof(TS) == 2, uint16_t, uint32_t>::type Raw;
+  u32x4* place = (u32x4*)part + 16 * SL * w;
+
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    GroupTile gt;
+    if (!find_group_tile(offsets, experts, (int)T, 16, tiles_n, tile, lane, gt)) break;
+    const int64_t n0 = (int64_t)16 * RB * (gt.tile % tiles_n), r0 = gt.row0 + (int64_t)16 * (gt.tile / tiles_n);
+    const int tokens = (int)(gt.row0 + gt.rows - r0 < 16 ? gt.row0 + gt.rows - r0 : 16);
+    const int rows = (int)(N - n0 < 16 * RB ? N - n0 : 16 * RB);
+    const int64_t first = (int64_t)gt.expert * N + n0;
+    // weight rows past the end are past the resource and read as zero; their
+    // scales repeat the last row's
+    const __amdgpu_buffer_rsrc_t wr = buf_rsrc_n(uniform_ptr(packed + first * half), (uint32_t)rows * half);
+    const __amdgpu_buffer_rsrc_t xr = buf_rsrc_n(uniform_ptr(x + r0 * K), (uint32_t)tokens * xrow);
+    f32x4 acc[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[b] = zero;
+
+    for (int s = w; s < slices; s += nw) {
+      const int b0 = SL * s;                                   // the slice's first 32-column block
+      const int nb = blocks32 - b0 < SL ? blocks32 - b0 : SL;  // its blocks; those past K read x as zero
+      u32x4 cv[D][NC];
+      Raw sz[D][NL];
+      const uint32_t wo = (uint32_t)lr * half + 16u * lp + (uint32_t)s * (16 * SL);
+      // Scale or zero-point 4 i + h of the slice's 2 NS for row l16 (the scales
+      // first).  One value a lane, spread over the lanes afterwards: these
+      // gathers cost the address unit 64 lanes each whatever they fetch, and
+      // with one load for every value they took longer than the codes.
+      const Raw* sp[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int which = 4 * i + h, blk = (G128 ? 4 : 1) * (which % NS);
+        sp[i] = (const Raw*)(which < NS ? scales : zeros) + first * ng + (uint32_t)(b0 + (blk < nb ? blk : 0)) / bpg;
+      }
+      auto load = [&](int b) {
+        const int u = b % D;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          cv[u][i] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo + (uint32_t)(16 * b + RPL * i) * half, 0, 2));
+        const uint32_t row = 16 * b + l16 < rows ? 16 * b + l16 : rows - 1;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) sz[u][i] = sp[i][row * ng];
+      };
+#pragma unroll
+      for (int b = 0; b < D; ++b) load(b);
+      u32x4 xq[SL];  // G128: 8 q .. 8 q + 7 of block 4 j + h at 4 j + q; otherwise 8 h .. 8 h + 7 of block i
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        const int blk = G128 ? (i & ~3) + h : i;
+        const uint32_t col = 32u * (uint32_t)(b0 + blk) + (G128 ? 8u * (i & 3) : 8u * h);
+        const uint32_t off = blk < nb ? (uint32_t)l16 * xrow + 2u * col : kPastEnd;
+        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
+      }
+      // every load of the slice is on its way before anything waits for one
+      // (the compiler would sink the codes' loads to their use behind this)
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 xv[SL];
+#pragma unroll
+      for (int i = 0; i < SL; ++i) xv[i] = order_as_codes(xq[i]);
+      f32x4 xs[NS];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        xs[i] = zero;
+#pragma unroll
+        for (int q = 0; q < SL / NS; ++q)
+          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q], ones, xs[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int u = b % D;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int t = RPL * i + lr;
+          place[SL * t + (lp ^ (SL == 16 ? t : (t >> 1) & 7))] = cv[u][i];
+        }
+        __builtin_amdgcn_wave_barrier();
+        uint32_t words[SL];
+        const int sw = SL == 16 ? l16 : (l16 >> 1) & 7;
+        if constexpr (G128) {
+#pragma unroll
+          for (int j = 0; j < SL / 4; ++j) {
+            const u32x4 v = place[SL * l16 + ((4 * j + h) ^ sw)];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) words[4 * j + q] = v[q];
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < SL; ++c) words[c] = ((const uint32_t*)(place + SL * l16 + (c ^ sw)))[h];
+        }
+        __builtin_amdgcn_wave_barrier();
+        float val[2 * NS];  // scales, then zero-points
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          uint32_t v[4];
+          spread4(sz[u][i], v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) val[4 * i + k] = scale_value<TS>(v[k]);
+        }
+        f32x4 d[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) d[i] = zero;
+#pragma unroll
+        for (int q = 0; q < SL / NS; ++q)
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q], codes16(words[SL / NS * i + q], nk), d[i], 0,
+                                                           0, 0);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const float sc = val[i], nz = -sc * (16.0f + val[NS + i]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[b][r] = fmaf(sc, d[i][r], fmaf(nz, xs[i][r], acc[b][r]));
+        }
+        if (b + D < RB) {
+          load(b + D);
+          asm volatile("" ::: "memory");
+        }
+      }
+    }
+
+    // lane holds tokens 4 h + r (r = 0..3) of weight row 16 b + l16
+    __syncthreads();  // the regrouping places overlap the sums'
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (4 * h + r < tokens) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) part[((w * 16 + 4 * h + r) * RB + b) * 16 + l16] = acc[b][r];
+      }
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * RB * tokens; o += blockDim.x) {
+      float v = 0.0f;
+#pragma unroll 8
+      for (int i = 0; i < nw; ++i) v += part[i * 256 * RB + o];
+      const int64_t n = n0 + o % (16 * RB), m = r0 + o / (16 * RB);
+      if (n < N) {
+        if constexpr (sizeof(TY) == 4) y[m * N + n] = v;
+        else y[m * N + n] = (TY)f32_to_bf16_bits(v);
+      }
+    }
+    if (tile + gridDim.x < tiles) __syncthreads();  // the next tile writes part again
+  }
+}
+
+// At most `most` waves, each taking the same number of slices of sl blocks.
+static int grouped_rows_waves(int64_t k, int sl, int most) {
+  const int64_t slices = (k / 32 + sl - 1) / sl;
+  const int64_t per = (slices + most - 1) / most;
+  return (int)((slices + per - 1) / per);
+}
+
+template <typename TS, typename TY, bool G128, int SL, int RB>
+static hipError_t gr_rb(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
+                        const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
+                        hipStream_t st) {
+  const int64_t tiles_n = (n + 16 * RB - 1) / (16 * RB), tiles = grouped_max_tiles(t, experts, 16) * tiles_n;
+  const int nw = grouped_rows_waves(k, SL, 128 / SL);
+  const size_t sums = (size_t)nw * 1024 * RB, places = (size_t)nw * 256 * SL;
+  const dim3 grid((unsigned)(tiles < kGRowsGrid ? tiles : kGRowsGrid));
+  k_w4a16_grouped_rows<TS, TY, G128, SL, RB><<<grid, 64 * nw, sums > places ? sums : places, st>>>(
+      x, t, k, offsets, experts, packed, scales, zeros, n, g, (TY*)y, (uint32_t)tiles_n, tiles);
+  return hipGetLastError();
+}
+
+template <typename TS, typename TY, bool G128>
+static hipError_t gr_go(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
+                        const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
+                        hipStream_t st) {
+#ifdef GRB
+  constexpr int SL = G128 ? GSL : 8;
+  return gr_rb<TS, TY, G128, SL, GRB>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+#else
+  constexpr int SL = G128 ? 16 : 8;
+  switch (rows_per_group<G128 ? 6 : 2>(grouped_max_tiles(t, experts, 16), (n + 15) / 16)) {
+    case 1: return gr_rb<TS, TY, G128, SL, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    case 2: return gr_rb<TS, TY, G128, SL, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    case 4:
+      if constexpr (G128) return gr_rb<TS, TY, G128, SL, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    default:
+      if constexpr (G128) return gr_rb<TS, TY, G128, SL, 6>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  }
+  return hipErrorInvalidValue;
+#endif
+}
+
+template <typename TS, typename TY>
+static hipError_t gr_pick(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
+                          const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
+                          hipStream_t st) {
+  if (g % 128 == 0) return gr_go<TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gr_go<TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+}
+
+hipError_t launch_w4a16_grouped_rows(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
+                                     const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
+                                     int64_t n, int g, void* y, int y_dtype, hipStream_t st) {
+  const uint16_t* xb = (const uint16_t*)x;
+  if (sz_dtype == W4_F16) {
+    if (y_dtype == W4_F32)
+      return gr_pick<_Float16, float>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return gr_pick<_Float16, uint16_t>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  }
+  if (y_dtype == W4_F32)
+    return gr_pick<float, float>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gr_pick<float, uint16_t>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+}
+
+}  // namespace w4
