@@ -447,9 +447,6 @@ int w4a8_matmul_ws(const int8_t* xq, const float* x_scale, int64_t m, int64_t k,
                      group_size, y, y_dtype, workspace, workspace_bytes, stream);
 }
 
-#ifndef GROUPED_ROWS
-#define GROUPED_ROWS 16
-#endif
 // ---- microscaled 4-bit floating point and the products by expert ---------------
 
 // Block scales (one byte each): the pointer itself is 4-byte aligned.
@@ -506,15 +503,18 @@ int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64
   return hip_status(w4::launch_dequant_mxfp4(packed, scales, n, k, w_out, out_dtype, stream), fn);
 }
 
-// Kernel choice by the rows that one weight matrix has (on average, by expert).
+// Kernel choice.  By expert the many-row kernel takes over at 8 rows an expert
+// on average (64 rows of 8 experts [11008, 4096]: 43 against 44 us; 128 rows 43
+// against 65).  Dense, up to 32 rows go to the few-row kernel ([11008, 4096]:
+// 9.4 against 10.9 us at 16 rows, equal at 32); up to 128 rows the many-row
+// kernel's time goes with K alone while its tiles leave CUs idle, the few-row
+// kernel's with N * K, and N = 4608 is about where they meet (64 rows of
+// [11008, 4096]: 20 against 12 us, of [4096, 11008]: 19 against 24).
 static int mx_product(const char* fn, const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k,
                       const int32_t* offsets, int64_t experts, const uint8_t* packed, const uint8_t* scales,
                       int64_t n, void* y, int y_dtype, hipStream_t stream) {
-  const int64_t rows = offsets != nullptr ? m / experts : m;
-#ifndef MXR
-#define MXR 64
-#endif
-  if (rows > MXR && w4::mx_gemm_fits(k))
+  const bool many = offsets != nullptr ? m >= 8 * experts : m > 128 || (m > 32 && n > 4608);
+  if (many && w4::mx_gemm_fits(k))
     return hip_status(w4::launch_mx_gemm(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
                       fn);
   return hip_status(w4::launch_mx_rows(xq, xs, m, k, packed, scales, n, y, y_dtype, offsets, (int)experts, stream),
@@ -570,12 +570,16 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
-  // float32 x: multiply-adds; bf16 x: by the rows that an expert has on average
+  // float32 x: multiply-adds.  bf16 x: by the rows that an expert has on
+  // average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 85 us
+  // against 92, 192 rows 117 against 88; with groups that are no multiple of
+  // 128 its share of conversions is larger (256 rows of 16 experts [2048,
+  // 2048], groups of 32: 51 against 39 us).
   if (x_dtype == W4_F32)
     return hip_status(w4::launch_w4a16_grouped_f32(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                    n, group_size, y, y_dtype, stream),
                       fn);
-  if (t / experts > GROUPED_ROWS && w4::w4a16_grouped_gemm_fits(k))
+  if (t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);

@@ -320,9 +320,11 @@ template <typename TY, bool GROUPED>
 static hipError_t mx_gemm_pick(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                                const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts,
                                hipStream_t st) {
-  // by expert each one's last tile is half full on average
+  // by expert each one's last tile is half full on average, and each has one
+  const int64_t some = experts < m ? experts : m;
   auto tiles = [&](int bm, int bn) {
-    const int64_t tm = GROUPED ? m / bm + ((experts < m ? experts : m) + 1) / 2 : (m + bm - 1) / bm;
+    const int64_t half = m / bm + (some + 1) / 2;
+    const int64_t tm = !GROUPED ? (m + bm - 1) / bm : half > some ? half : some;
     return tm * ((n + bn - 1) / bn);
   };
   const int64_t small = tiles(128, 128);

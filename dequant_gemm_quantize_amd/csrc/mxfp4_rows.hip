@@ -222,9 +222,6 @@ template <typename TY, bool GROUPED, int MT>
 static void mx_rows_rb(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                        const uint8_t* scales, int64_t n, void* y, const int* offsets, int experts, hipStream_t st) {
   const int64_t tiles_m = GROUPED ? grouped_max_tiles(m, experts, 16 * MT) : (m + 16 * MT - 1) / (16 * MT);
-#ifdef RBSEL
-  return mx_rows_go<TY, GROUPED, MT, RBSEL>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
-#else
   switch (rows_per_group<MT == 4 ? 2 : MT == 2 ? 4 : 6>(tiles_m, (n + 15) / 16)) {
     case 1: return mx_rows_go<TY, GROUPED, MT, 1>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
     case 2: return mx_rows_go<TY, GROUPED, MT, 2>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
@@ -234,7 +231,6 @@ static void mx_rows_rb(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t 
     default:
       if constexpr (MT == 1) return mx_rows_go<TY, GROUPED, MT, 6>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
   }
-#endif
 }
 
 template <typename TY>

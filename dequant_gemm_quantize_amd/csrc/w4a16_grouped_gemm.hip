@@ -8,7 +8,7 @@
 // second the first's rounding error, and twice the MFMAs: with fp16 scales
 // (4 + 11 significant bits) the two hold the weight exactly.
 //
-// Workgroup tile BM rows x 256 columns, four waves, each all BM rows of 64
+// Workgroup tile BM rows x 128 NJ columns, four waves, each all BM rows of 32 NJ
 // columns: no two waves dequantize the same weight, and a wave's accumulators
 // (8 x 2 blocks at BM = 256) are reused against 64 KB of LDS reads a K step
 // of 64 columns, which is half of what LDS gives in the step's MFMA time.
@@ -29,9 +29,7 @@ namespace w4 {
 
 namespace {
 
-constexpr int GBN = 256;          // columns of a workgroup tile
 constexpr int GLine = 128;        // bytes of a row per stage: 64 bf16 or 256 codes
-constexpr int W_STAGE = GBN * GLine;
 
 template <typename TS> struct GScale;
 template <> struct GScale<_Float16> {
@@ -63,19 +61,19 @@ __device__ __forceinline__ void dequant_pairs(uint32_t p, float s, float b, u32x
   }
 }
 
-template <int BM> constexpr size_t gg_lds() { return 2 * (size_t)(BM * GLine + W_STAGE); }
+template <int BM, int NJ> constexpr size_t gg_lds() { return 2 * (size_t)(BM + 128 * NJ) * GLine; }
 
 }  // namespace
 
 // G128: g % 128 == 0, so two steps of a stage share a scale.
-template <int BM, typename TS, typename TY, bool G128>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
+template <int BM, int NJ, typename TS, typename TY, bool G128>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) void k_w4a16_grouped_gemm(
     const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
     const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
     int g, TY* __restrict__ y, uint32_t tiles_n) {
   constexpr bool SPLIT = sizeof(TY) == 4;
-  constexpr int MI = BM / 32, NJ = 2, LA = BM / 32, LW = GBN / 32;
-  constexpr int A_STAGE = BM * GLine;
+  constexpr int GBN = 128 * NJ, MI = BM / 32, LA = BM / 32, LW = GBN / 32;
+  constexpr int A_STAGE = BM * GLine, W_STAGE = GBN * GLine;
   extern __shared__ __attribute__((aligned(1024))) uint8_t sgg[];  // x stages, then weight stages
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -137,7 +135,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
   // scales of the lane's two weight rows for the four steps of a stage: step
   // u, half h has 32-column block 8 st + 2 u + h
   const int r = lane & 31, h = lane >> 5;
-  const int n_lane = 64 * w + r;
+  const int n_lane = 32 * NJ * w + r;
   const uint32_t bpg = (uint32_t)g / 32;
   constexpr int NS = G128 ? 2 : 4;
   TS sv[NJ][NS], zv[NJ][NS], snext[NJ][NS], znext[NJ][NS];
@@ -181,11 +179,15 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
     for (int i = 0; i < MI; ++i) xv[t & 1][i] = *(const u32x4*)(a + 32 * GLine * i);
   };
   // the step's codes: chunk 2 u + h of the weight line
-  u32x4 cv[NJ];
+  u32x4 cv[NJ], cnext[NJ];
   auto codes = [&](int st, int u) {
-    const uint8_t* b = sw + (st & 1) * W_STAGE + (64 * w + r) * GLine + 16 * ((2 * u + h) ^ swz);
+    const uint8_t* b = sw + (st & 1) * W_STAGE + (32 * NJ * w + r) * GLine + 16 * ((2 * u + h) ^ swz);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) cv[j] = *(const u32x4*)(b + 32 * GLine * j);
+    for (int j = 0; j < NJ; ++j) cnext[j] = *(const u32x4*)(b + 32 * GLine * j);
+  };
+  auto c_take = [&]() {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) cv[j] = cnext[j];
   };
   // weights of a slice, in two register sets; slice t of step u
   u32x4 whi[2][NJ], wlo[2][NJ];
@@ -230,18 +232,22 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
   w_issue(0);
   x_issue(0);
   x_issue(1);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LA) : "memory");  // all but step 1's x
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   s_take();
   codes(0, 0);
+  c_take();
   x_frag(0, c0);
   dequant(c0, c0);
 
   // One K step of 64 columns, four slices.  A slice's x reads and conversions
   // run under the MFMAs of the one before.  Before the last slice every wave
   // has read all of the step's x and waited for its share of the next step's;
-  // behind the barrier that is whole and this step's x stage is free.
+  // behind the barrier that is whole and this step's x stage is free.  The
+  // next step's codes are read a slice earlier still: their stage has been
+  // whole since the barrier of u = 1.  (More stages of x made no difference:
+  // a step waits for its conversions, not for memory.)
   auto step = [&](int ks, auto uc) {
     constexpr int u = decltype(uc)::value;
     x_frag(ks, c1);
@@ -249,6 +255,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
     mma(c0);
     mix();
     x_frag(ks, c2);
+    codes((ks + 1) / 4, (u + 1) & 3);
     dequant(c2, uc);
     mma(c1);
     mix();
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
     if constexpr (u == 1) s_issue(ks / 4 + 1);
     if constexpr (u == 3) s_take();
     x_issue(ks + 2);
-    codes((ks + 1) / 4, (u + 1) & 3);
+    c_take();
     x_frag(ks + 1, c0);
     dequant(c0, std::integral_constant<int, (u + 1) & 3>{});
     mma(c3);
@@ -286,46 +293,49 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_w4a16_grouped_gemm(
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
   __builtin_amdgcn_s_barrier();
   constexpr int TURN = turn_bytes<TY, NJ>();
-  static_assert(4 * TURN <= (int)gg_lds<BM>(), "the waves' turning places fit in LDS");
-  turn_store<TY, MI, NJ>(sgg + w * TURN, lane, acc, y, N, m0, mend, n0 + 64 * w);
+  static_assert(4 * TURN <= (int)gg_lds<BM, NJ>(), "the waves' turning places fit in LDS");
+  turn_store<TY, MI, NJ>(sgg + w * TURN, lane, acc, y, N, m0, mend, n0 + 32 * NJ * w);
 }
 
 // K % 64 == 0: whole steps; 256 rows of K bf16 stay below 2^31 bytes.
 bool w4a16_grouped_gemm_fits(int64_t k) { return k % 64 == 0 && k <= ((int64_t)1 << 21); }
 
-template <int BM, typename TS, typename TY, bool G128>
+template <int BM, int NJ, typename TS, typename TY, bool G128>
 static hipError_t gg_go(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
                         const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                         hipStream_t st) {
   static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
   const hipError_t e = once_per_device(attr_done, [] {
-    return hipFuncSetAttribute((const void*)k_w4a16_grouped_gemm<BM, TS, TY, G128>,
-                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)gg_lds<BM>());
+    return hipFuncSetAttribute((const void*)k_w4a16_grouped_gemm<BM, NJ, TS, TY, G128>,
+                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)gg_lds<BM, NJ>());
   });
   if (e != hipSuccess) return e;
-  const int64_t tiles_n = (n + GBN - 1) / GBN, grid = (grouped_max_tiles(t, experts, BM) * tiles_n + 7) / 8 * 8;
-  k_w4a16_grouped_gemm<BM, TS, TY, G128><<<dim3((unsigned)grid), 256, gg_lds<BM>(), st>>>(
+  const int64_t tiles_n = (n + 128 * NJ - 1) / (128 * NJ), grid = (grouped_max_tiles(t, experts, BM) * tiles_n + 7) / 8 * 8;
+  k_w4a16_grouped_gemm<BM, NJ, TS, TY, G128><<<dim3((unsigned)grid), 256, gg_lds<BM, NJ>(), st>>>(
       x, t, k, offsets, experts, packed, scales, zeros, n, g, (TY*)y, (uint32_t)tiles_n);
   return hipGetLastError();
+}
+
+template <typename TS, typename TY, bool G128>
+static hipError_t gg_tile(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
+                          const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
+                          hipStream_t st) {
+  // Experts [11008, 4096], 8 of them, us with 256 x 256 / 128 x 128 / 64 x 128
+  // tiles: 2048 rows 205 / 235 / 271, 1024 rows 198 / 136 / 162, 512 rows 180 /
+  // 112 / 100, 256 rows 179 / 99 / 74.
+  if (t > 192 * (int64_t)experts)
+    return gg_go<256, 2, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  if (t > 80 * (int64_t)experts)
+    return gg_go<128, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gg_go<64, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 template <typename TS, typename TY>
 static hipError_t gg_pick(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
                           const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                           hipStream_t st) {
-  const int64_t rows = t / experts;
-#ifdef GG_BM
-  constexpr int B = GG_BM;
-  if (g % 128 == 0) return gg_go<B, TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gg_go<B, TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-#else
-  if (rows > 160) {
-    if (g % 128 == 0) return gg_go<256, TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    return gg_go<256, TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  }
-  if (g % 128 == 0) return gg_go<64, TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gg_go<64, TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-#endif
+  if (g % 128 == 0) return gg_tile<TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gg_tile<TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 hipError_t launch_w4a16_grouped_gemm(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
