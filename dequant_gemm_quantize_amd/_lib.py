@@ -412,13 +412,31 @@ def w4a8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, s
 # ---------------------------------------------------------------------------
 # Microscaled 4-bit floating point and the products by expert
 # ---------------------------------------------------------------------------
-def _launch(dev: torch.device, fn, *args) -> None:
+# A product of one token takes less time than these wrappers can: what follows
+# asks each tensor as little as the checks need, looks for the words of an error
+# only when there is one, and takes the current stream's handle (an int) without
+# the Stream object around it (0.06 us against 1.06).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device(*ts: torch.Tensor) -> int:
+    """The index of the GPU that holds every one of the (dense) tensors."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if dev < 0 or t.get_device() != dev or not t.is_contiguous():
+            _gpu(*ts)  # raises, with the reason
+    return dev
+
+
+def _launch(dev: int, fn, *args) -> None:
     """Call fn with dev's current stream, on dev whichever device is current."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)))
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+            status = fn(*args, _raw_stream(dev))
+    if status != W4_OK:
+        _check(status)
 
 
 def _mx_blocks(k: int) -> int:
@@ -429,26 +447,27 @@ def _mx_blocks(k: int) -> int:
 
 def _check_mx(packed: torch.Tensor, scales: torch.Tensor, names: Tuple[str, str], lead: int) -> Tuple[int, ...]:
     """packed uint8 [..., K/2] and scales uint8 [..., K/32] of `lead` leading dimensions; returns (..., K)."""
-    if packed.dim() != lead + 1:
-        raise ValueError(f"{names[0]} must be a {lead + 1}-D tensor, got {packed.dim()} dimensions")
-    shape = tuple(int(d) for d in packed.shape)
+    shape = packed.shape
+    if len(shape) != lead + 1:
+        raise ValueError(f"{names[0]} must be a {lead + 1}-D tensor, got {len(shape)} dimensions")
     k = 2 * shape[-1]
-    _expect(packed, names[0], shape, (torch.uint8,))
-    _expect(scales, names[1], (*shape[:-1], _mx_blocks(k)), (torch.uint8,))
+    if packed.dtype is not torch.uint8:
+        _expect(packed, names[0], shape, (torch.uint8,))
+    if scales.dtype is not torch.uint8 or scales.shape != (*shape[:-1], _mx_blocks(k)):
+        _expect(scales, names[1], (*shape[:-1], _mx_blocks(k)), (torch.uint8,))
     return (*shape[:-1], k)
 
 
 Y_DTYPES = (torch.float32, torch.bfloat16)
 
 
-def _y_out(out: Optional[torch.Tensor], out_dtype: torch.dtype, shape, dev: torch.device) -> torch.Tensor:
+def _y_out(out: Optional[torch.Tensor], out_dtype: torch.dtype, shape, like: torch.Tensor) -> torch.Tensor:
+    """out (checked by the caller against the other tensors' device), or a new tensor beside `like`."""
     if out is None:
         if out_dtype not in Y_DTYPES:
             raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-        return torch.empty(shape, dtype=out_dtype, device=dev)
+        return like.new_empty(shape, dtype=out_dtype)
     _expect(out, "out", shape, Y_DTYPES)
-    if _gpu(out) != dev:
-        raise ValueError("all tensors must be on the same device")
     return out
 
 
@@ -461,12 +480,11 @@ def quantize_mxfp4(w: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tens
     if out is not None:
         _expect(out[0], "packed", (n, k // 2), (torch.uint8,))
         _expect(out[1], "scales", (n, nb), (torch.uint8,))
-        dev = _gpu(w, *out)
+        dev = _device(w, *out)
         packed, scales = out
     else:
-        dev = _gpu(w)
-        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((n, nb), dtype=torch.uint8, device=dev)
+        dev = _device(w)
+        packed, scales = w.new_empty((n, k // 2), dtype=torch.uint8), w.new_empty((n, nb), dtype=torch.uint8)
     _launch(dev, load().quantize_mxfp4, _ptr(w), _dtype_code(w.dtype), n, k, _ptr(packed), _ptr(scales))
     return packed, scales
 
@@ -477,12 +495,12 @@ def dequant_mxfp4(packed: torch.Tensor, scales: torch.Tensor, out_dtype: torch.d
     n, k = _check_mx(packed, scales, ("packed", "scales"), 1)
     if out is not None:
         _expect(out, "out", (n, k), tuple(_DT))
-        dev = _gpu(packed, scales, out)
+        dev = _device(packed, scales, out)
         w = out
     else:
         _dtype_code(out_dtype)
-        dev = _gpu(packed, scales)
-        w = torch.empty((n, k), dtype=out_dtype, device=dev)
+        dev = _device(packed, scales)
+        w = packed.new_empty((n, k), dtype=out_dtype)
     _launch(dev, load().dequant_mxfp4, _ptr(packed), _ptr(scales), n, k, _ptr(w), _dtype_code(w.dtype))
     return w
 
@@ -494,8 +512,8 @@ def mxfp4_matmul(xq: torch.Tensor, xs: torch.Tensor, packed: torch.Tensor, scale
     n, kw = _check_mx(packed, scales, ("packed", "scales"), 1)
     if kw != k:
         raise ValueError(f"packed has {kw} columns of codes, xq has K={k}")
-    dev = _gpu(xq, xs, packed, scales)
-    y = _y_out(out, out_dtype, (m, n), dev)
+    dev = _device(xq, xs, packed, scales) if out is None else _device(xq, xs, packed, scales, out)
+    y = _y_out(out, out_dtype, (m, n), xq)
     _launch(dev, load().mxfp4_matmul, _ptr(xq), _ptr(xs), m, k, _ptr(packed), _ptr(scales), n, _ptr(y),
             _dtype_code(y.dtype))
     return y
@@ -515,8 +533,8 @@ def mxfp4_grouped_matmul(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Tens
     if kw != k:
         raise ValueError(f"packed has {kw} columns of codes, xq has K={k}")
     _expect(offsets, "offsets", (e + 1,), (torch.int32,))
-    dev = _gpu(xq, xs, offsets, packed, scales)
-    y = _y_out(out, out_dtype, (t, n), dev)
+    dev = _device(xq, xs, offsets, packed, scales) if out is None else _device(xq, xs, offsets, packed, scales, out)
+    y = _y_out(out, out_dtype, (t, n), xq)
     _launch(dev, load().mxfp4_grouped_matmul, _ptr(xq), _ptr(xs), t, k, _ptr(offsets), e, _ptr(packed),
             _ptr(scales), n, _ptr(y), _dtype_code(y.dtype))
     return y
@@ -543,8 +561,8 @@ def w4a16_grouped_matmul(x: torch.Tensor, offsets: torch.Tensor, packed: torch.T
     _expect(scales, "scales", (e, n, ng), SZ_DTYPES)
     _expect(zeros, "zeros", (e, n, ng), (scales.dtype,))
     _expect(offsets, "offsets", (e + 1,), (torch.int32,))
-    dev = _gpu(x, offsets, packed, scales, zeros)
-    y = _y_out(out, out_dtype or x.dtype, (t, n), dev)
+    dev = _device(x, offsets, packed, scales, zeros) if out is None else _device(x, offsets, packed, scales, zeros, out)
+    y = _y_out(out, out_dtype or x.dtype, (t, n), x)
     _launch(dev, load().w4a16_grouped_matmul, _ptr(x), _dtype_code(x.dtype), t, k, _ptr(offsets), e, _ptr(packed),
             _ptr(scales), _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(y), _dtype_code(y.dtype))
     return y
