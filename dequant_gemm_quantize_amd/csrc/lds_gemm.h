@@ -39,6 +39,39 @@ __device__ __forceinline__ void band(uint32_t t, uint32_t tiles_m, uint32_t tile
 
 constexpr uint32_t kPastEnd = 0x80000000u;  // beyond every resource: their sizes stay below 2^31
 
+// Which tile of `total` a workgroup has.  Each XCD (workgroup number mod 8)
+// takes a contiguous eighth of the list, SLOTS tiles at a time (32 CUs times
+// the workgroups that one holds).  With SPLIT, tiles beyond the last whole round
+// of SLOTS are split into halves of half the rows when all the halves fit one
+// round, which then takes 0.6 of the time.  `half` is -1 (a whole tile), 0 or 1.
+// False: nothing to do.  A launch has xcd_grid(tiles) workgroups.
+template <uint32_t SLOTS, bool SPLIT>
+__device__ __forceinline__ bool xcd_tile(uint32_t total, uint32_t& tile, int& half) {
+  const uint32_t per = (total + 7) / 8, first = (blockIdx.x & 7) * per, j = blockIdx.x >> 3;
+  half = -1;
+  if (first >= total) return false;
+  const uint32_t mine = total - first < per ? total - first : per;
+  const uint32_t rest = mine % SLOTS, whole = mine - rest;
+  uint32_t at = j;
+  if (SPLIT && j >= whole && rest <= SLOTS / 2) {
+    at = whole + (j - whole) / 2;
+    half = (int)((j - whole) & 1);
+  }
+  tile = first + at;
+  return at < mine;
+}
+template <uint32_t SLOTS, bool SPLIT>
+inline int64_t xcd_grid(int64_t tiles) {
+  return (tiles + 7) / 8 * 8 + (SPLIT ? 8 * (SLOTS / 2) : 0);
+}
+
+// Rounds of tiles, a round of halves taking `part` of one.
+template <uint32_t SLOTS>
+inline double xcd_rounds(int64_t tiles, double part) {
+  const int64_t mine = (tiles + 7) / 8, rest = mine % SLOTS;
+  return (double)(mine / SLOTS) + (rest == 0 ? 0.0 : rest <= SLOTS / 2 ? part : 1.0);
+}
+
 // Turns a wave's 32 x 32 blocks around in LDS and stores them to y.
 //
 // Register e of acc[i][j] holds y row r = lane % 32 of block row i, column

@@ -35,52 +35,24 @@ template <int BM_, int BN_, int WR_, int WC_, int S_> struct MxTile {
   static constexpr int LA = BM / (8 * NW), LB = BN / (8 * NW);  // 1 KB loads per wave and step
   static constexpr int A_STAGE = BM * kStepBytes, B_STAGE = BN * kStepBytes, STAGE = A_STAGE + B_STAGE;
   static constexpr size_t lds = (size_t)S * STAGE;
+  typedef MxTile<BM / 2, BN, WR, WC, S> Half;
+  static constexpr uint32_t SLOTS = 2 * lds <= 163840 ? 64 : 32;  // workgroups an XCD holds (160 KB of LDS a CU)
+  // Halves of small tiles cost more than they give: with few rows the second
+  // one is often empty and the weights are read twice (256 rows of 8 experts
+  // [11008, 4096] 46 us without, 51 with).
+  static constexpr bool SPLIT = BM == 256;
 };
 
 }  // namespace
 
-template <typename T, typename TY, bool GROUPED>
-__global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
-                                                      int64_t M, int64_t K, const uint8_t* __restrict__ packed,
-                                                      const uint8_t* __restrict__ scales, int64_t N,
-                                                      void* __restrict__ y, const int* __restrict__ offsets,
-                                                      int experts, uint32_t tiles_m, uint32_t tiles_n) {
+// One tile: rows m0 .. min(m0 + BM, mend) - 1 of y, columns from n0.
+template <typename T, typename TY>
+__device__ __forceinline__ void mx_tile(uint8_t* smx, int lane, int w, const uint8_t* __restrict__ xq,
+                                        const uint8_t* __restrict__ xs, int64_t K, const uint8_t* __restrict__ wp,
+                                        const uint8_t* __restrict__ sp, int64_t N, TY* __restrict__ y, int64_t m0,
+                                        int64_t mend, int64_t n0) {
   constexpr int MI = T::MI, NJ = T::NJ, LA = T::LA, LB = T::LB, S = T::S;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smx[];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / T::WC, wn = w % T::WC;
-
-  // ---- tile: each XCD (workgroup number mod 8) takes a contiguous eighth of
-  // the list, which goes through bands of 8 M tiles, in a band N tile by N
-  // tile: the 32 tiles that an XCD has at a time read 8 + 4 operand tiles
-  int64_t m0, mend, n0;
-  const uint8_t* wp = packed;
-  const uint8_t* sp = scales;
-  {
-    uint32_t total = tiles_m * tiles_n;
-    if constexpr (GROUPED) total = (uint32_t)grouped_tiles(offsets, experts, (int)M, T::BM, lane) * tiles_n;
-    const uint32_t per = (total + 7) / 8, t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || t >= total) return;
-    if constexpr (GROUPED) {
-      GroupTile g;
-      if (!find_group_tile(offsets, experts, (int)M, T::BM, tiles_n, t, lane, g)) return;
-      const uint32_t own = (uint32_t)(g.rows + T::BM - 1) / T::BM;
-      uint32_t tm, tn;
-      band(g.tile, own, tiles_n, tm, tn);
-      m0 = g.row0 + (int64_t)T::BM * tm;
-      n0 = (int64_t)T::BN * tn;
-      mend = g.row0 + g.rows;
-      wp += (int64_t)g.expert * N * (K / 2);
-      sp += (int64_t)g.expert * N * (K / 32);
-    } else {
-      uint32_t tm, tn;
-      band(t, tiles_m, tiles_n, tm, tn);
-      m0 = (int64_t)T::BM * tm;
-      n0 = (int64_t)T::BN * tn;
-      mend = M;
-    }
-  }
   const uint32_t half = (uint32_t)(K / 2), kb = (uint32_t)(K / 32);
   const int mrows = (int)(mend - m0 < T::BM ? mend - m0 : T::BM);
   const int nrows = (int)(N - n0 < T::BN ? N - n0 : T::BN);
@@ -274,11 +246,63 @@ __global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict_
   }
 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
-
   __builtin_amdgcn_s_barrier();  // every wave is done with its fragments
+  asm volatile("" ::: "memory");
   constexpr int TURN = turn_bytes<TY, NJ>();
   static_assert(T::NW * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
-  turn_store<TY, MI, NJ>(smx + w * TURN, lane, acc, (TY*)y, N, m0 + 32 * MI * wm, mend, n0 + 32 * NJ * wn);
+  turn_store<TY, MI, NJ>(smx + w * TURN, lane, acc, y, N, m0 + 32 * MI * wm, mend, n0 + 32 * NJ * wn);
+}
+
+template <typename T, typename TY, bool GROUPED>
+__global__ __launch_bounds__(T::NT, 1) void k_mx_gemm(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
+                                                      int64_t M, int64_t K, const uint8_t* __restrict__ packed,
+                                                      const uint8_t* __restrict__ scales, int64_t N,
+                                                      void* __restrict__ y, const int* __restrict__ offsets,
+                                                      int experts, uint32_t tiles_m, uint32_t tiles_n) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smx[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // ---- tile: the list goes through bands of 8 M tiles, in a band N tile by N
+  // tile: the 32 tiles that an XCD has at a time read 8 + 4 operand tiles
+  int64_t m0, mend, n0;
+  const uint8_t* wp = packed;
+  const uint8_t* sp = scales;
+  uint32_t t;
+  int half;
+  {
+    uint32_t total = tiles_m * tiles_n;
+    if constexpr (GROUPED) total = (uint32_t)grouped_tiles(offsets, experts, (int)M, T::BM, lane) * tiles_n;
+    if (!xcd_tile<T::SLOTS, T::SPLIT>(total, t, half)) return;
+    if constexpr (GROUPED) {
+      GroupTile g;
+      if (!find_group_tile(offsets, experts, (int)M, T::BM, tiles_n, t, lane, g)) return;
+      const uint32_t own = (uint32_t)(g.rows + T::BM - 1) / T::BM;
+      uint32_t tm, tn;
+      band(g.tile, own, tiles_n, tm, tn);
+      m0 = g.row0 + (int64_t)T::BM * tm;
+      n0 = (int64_t)T::BN * tn;
+      mend = g.row0 + g.rows;
+      wp += (int64_t)g.expert * N * (K / 2);
+      sp += (int64_t)g.expert * N * (K / 32);
+    } else {
+      uint32_t tm, tn;
+      band(t, tiles_m, tiles_n, tm, tn);
+      m0 = (int64_t)T::BM * tm;
+      n0 = (int64_t)T::BN * tn;
+      mend = M;
+    }
+  }
+  if (half == 0 && mend > m0 + T::BM / 2) mend = m0 + T::BM / 2;
+  if (half == 1) {
+    m0 += T::BM / 2;
+    if (m0 >= mend) return;
+  }
+  // half a tile, or one with rows in its upper half only, takes half the time
+  if (half >= 0 || mend - m0 <= T::BM / 2)
+    mx_tile<typename T::Half, TY>(smx, lane, w, xq, xs, K, wp, sp, N, (TY*)y, m0, mend, n0);
+  else
+    mx_tile<T, TY>(smx, lane, w, xq, xs, K, wp, sp, N, (TY*)y, m0, mend, n0);
 }
 
 bool mx_gemm_fits(int64_t k) { return k % 128 == 0; }
@@ -295,7 +319,7 @@ static hipError_t mx_gemm_go(const uint8_t* xq, const uint8_t* xs, int64_t m, in
   if (e != hipSuccess) return e;
   const int64_t tiles_m = GROUPED ? grouped_max_tiles(m, experts, T::BM) : (m + T::BM - 1) / T::BM;
   const int64_t tiles_n = (n + T::BN - 1) / T::BN;
-  const int64_t grid = (tiles_m * tiles_n + 7) / 8 * 8;
+  const int64_t grid = xcd_grid<T::SLOTS, T::SPLIT>(tiles_m * tiles_n);
   k_mx_gemm<T, TY, GROUPED><<<dim3((unsigned)grid), T::NT, T::lds, st>>>(xq, xs, m, k, packed, scales, n, y, offsets,
                                                                        experts, (uint32_t)tiles_m, (uint32_t)tiles_n);
   return hipGetLastError();
@@ -308,13 +332,9 @@ typedef MxTile<256, 192, 2, 2, 2> MxNarrow;
 typedef MxTile<128, 128, 2, 2, 2> MxSmall;
 
 // Time of all tiles in rounds of a large tile a CU.  Measured, K = 4096 to
-// 16384: a round of narrow tiles takes 0.88 of a round of large ones ([11008,
-// 4096], 2048 rows: 58 us in two rounds against 66), a round of small ones
-// with two a CU 0.68, with one a CU 0.45 ([11008, 4096], 128 rows: 15 us
-// against 31).
-static double mx_rounds(int64_t tiles, int64_t slots, double each) {
-  return (double)((tiles + slots - 1) / slots) * each;
-}
+// 16384: a round of narrow tiles takes 0.88 of a round of large ones, a round of
+// halves of either about 0.6 of it, a round of small ones with two a CU 0.68,
+// with one a CU 0.45 ([11008, 4096], 128 rows: 15 us against 31).
 
 template <typename TY, bool GROUPED>
 static hipError_t mx_gemm_pick(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
@@ -328,8 +348,8 @@ static hipError_t mx_gemm_pick(const uint8_t* xq, const uint8_t* xs, int64_t m, 
     return tm * ((n + bn - 1) / bn);
   };
   const int64_t small = tiles(128, 128);
-  const double large_t = mx_rounds(tiles(256, 256), 256, 1.0), narrow_t = mx_rounds(tiles(256, 192), 256, 0.88),
-               small_t = small <= 256 ? 0.45 : mx_rounds(small, 512, 0.68);
+  const double large_t = xcd_rounds<32>(tiles(256, 256), 0.6), narrow_t = 0.88 * xcd_rounds<32>(tiles(256, 192), 0.6),
+               small_t = small <= 256 ? 0.45 : 0.68 * (double)((small + 511) / 512);
   if (small_t <= large_t && small_t <= narrow_t)
     return mx_gemm_go<MxSmall, TY, GROUPED>(xq, xs, m, k, packed, scales, n, y, offsets, experts, st);
   if (narrow_t < large_t)

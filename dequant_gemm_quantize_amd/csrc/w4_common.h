@@ -101,21 +101,14 @@ struct NibConst {
 };
 
 // ---- 16-row operands of packed 4-bit data ------------------------------------
-// A wave's slice of 16 weight rows x 256 bytes (512 codes).  It is loaded as
-// 256-byte runs of one row per 16 lanes (memory serves long runs better:
-// 64-byte pieces of 16 rows took 8.4 us against 7.1 on [11008, 4096]), lane
-// (l16, h) with 16-byte piece l16 of rows 4 j + h, and regrouped through the
-// wave's own 4 KB of LDS into pieces 4 j + h of row l16.  Row t's piece c is at
-// slot c ^ t, free of bank conflicts both ways.  LDS operations of a wave
-// complete in order, so the place is used again without a wait.
-__device__ __forceinline__ void load_runs(const uint8_t* base, int64_t row_bytes, int rows, int lane, u32x4 (&v)[4]) {
-  const int l16 = lane & 15, h = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int t = 4 * j + h < rows ? 4 * j + h : rows - 1;  // rows past the end repeat the last one
-    v[j] = ldg_nt((const u32x4*)(base + t * row_bytes + 16 * l16));
-  }
-}
+// A wave's slice of 16 weight rows x 256 bytes (512 codes), loaded as 256-byte
+// runs of one row per 16 lanes: lane (l16, h) has 16-byte piece l16 of rows
+// 4 j + h.  It is regrouped through the wave's own 4 KB of LDS into pieces 4 j + h of
+// row l16.  (Memory serves long runs better: with the pieces loaded where they
+// are needed, 64 bytes of 16 rows at a time, one row of x times [11008, 4096]
+// took 8.4 us against 8.0.)  Row t's piece c is at slot c ^ t, free of bank
+// conflicts both ways.  LDS operations of a wave complete in order, so the
+// place is used again without a wait.
 __device__ __forceinline__ void regroup_runs(u32x4* place, int lane, u32x4 (&v)[4]) {
   const int l16 = lane & 15, h = lane >> 4;
 #pragma unroll

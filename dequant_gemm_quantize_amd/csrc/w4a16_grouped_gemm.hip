@@ -65,35 +65,17 @@ template <int BM, int NJ> constexpr size_t gg_lds() { return 2 * (size_t)(BM + 1
 
 }  // namespace
 
-// G128: g % 128 == 0, so two steps of a stage share a scale.
+// One tile: rows m0 .. min(m0 + BM, mend) - 1 of y, columns from n0, for the
+// expert whose first weight row is ebase.  G128: g % 128 == 0, so two steps of
+// a stage share a scale.
 template <int BM, int NJ, typename TS, typename TY, bool G128>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) void k_w4a16_grouped_gemm(
-    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
-    const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
-    int g, TY* __restrict__ y, uint32_t tiles_n) {
+__device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uint16_t* __restrict__ x, int64_t K,
+                                        const uint8_t* __restrict__ packed, const void* __restrict__ scales,
+                                        const void* __restrict__ zeros, int64_t N, int g, TY* __restrict__ y, int64_t m0,
+                                        int64_t mend, int64_t n0, int64_t ebase) {
   constexpr bool SPLIT = sizeof(TY) == 4;
   constexpr int GBN = 128 * NJ, MI = BM / 32, LA = BM / 32, LW = GBN / 32;
   constexpr int A_STAGE = BM * GLine, W_STAGE = GBN * GLine;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t sgg[];  // x stages, then weight stages
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  // each XCD takes a contiguous eighth of the list of tiles (mxfp4_gemm.hip)
-  int64_t m0, mend, n0;
-  int64_t ebase;  // the expert's first weight row
-  {
-    const uint32_t total = (uint32_t)grouped_tiles(offsets, experts, (int)T, BM, lane) * tiles_n;
-    const uint32_t per = (total + 7) / 8, t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || t >= total) return;
-    GroupTile gt;
-    if (!find_group_tile(offsets, experts, (int)T, BM, tiles_n, t, lane, gt)) return;
-    uint32_t tm, tn;
-    band(gt.tile, (uint32_t)(gt.rows + BM - 1) / BM, tiles_n, tm, tn);
-    m0 = gt.row0 + (int64_t)BM * tm;
-    n0 = (int64_t)GBN * tn;
-    mend = gt.row0 + gt.rows;
-    ebase = (int64_t)gt.expert * N;
-  }
   const uint32_t xrow = (uint32_t)(2 * K), wrow = (uint32_t)(K / 2), ng = (uint32_t)(K / g);
   const uint32_t mrows = (uint32_t)(mend - m0 < BM ? mend - m0 : BM);
   const uint32_t nrows = (uint32_t)(N - n0 < GBN ? N - n0 : GBN);
@@ -292,9 +274,50 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) v
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
   __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   constexpr int TURN = turn_bytes<TY, NJ>();
   static_assert(4 * TURN <= (int)gg_lds<BM, NJ>(), "the waves' turning places fit in LDS");
   turn_store<TY, MI, NJ>(sgg + w * TURN, lane, acc, y, N, m0, mend, n0 + 32 * NJ * w);
+}
+
+template <int BM, int NJ, typename TS, typename TY, bool G128>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) void k_w4a16_grouped_gemm(
+    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
+    const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
+    int g, TY* __restrict__ y, uint32_t tiles_n) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sgg[];  // x stages, then weight stages
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  int64_t m0, mend, n0;
+  int64_t ebase;  // the expert's first weight row
+  int half;
+  {
+    const uint32_t total = (uint32_t)grouped_tiles(offsets, experts, (int)T, BM, lane) * tiles_n;
+    uint32_t t;
+    if (!xcd_tile<32, BM == 256>(total, t, half)) return;
+    GroupTile gt;
+    if (!find_group_tile(offsets, experts, (int)T, BM, tiles_n, t, lane, gt)) return;
+    uint32_t tm, tn;
+    band(gt.tile, (uint32_t)(gt.rows + BM - 1) / BM, tiles_n, tm, tn);
+    m0 = gt.row0 + (int64_t)BM * tm;
+    n0 = (int64_t)128 * NJ * tn;
+    mend = gt.row0 + gt.rows;
+    ebase = (int64_t)gt.expert * N;
+  }
+  if (half == 0 && mend > m0 + BM / 2) mend = m0 + BM / 2;
+  if (half == 1) {
+    m0 += BM / 2;
+    if (m0 >= mend) return;
+  }
+  // half a tile, or one with rows in its upper half only, takes half the time
+  if constexpr (BM > 64) {
+    if (half >= 0 || mend - m0 <= BM / 2) {
+      gg_tile<BM / 2, NJ, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
+      return;
+    }
+  }
+  gg_tile<BM, NJ, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
 }
 
 // K % 64 == 0: whole steps; 256 rows of K bf16 stay below 2^31 bytes.
@@ -310,14 +333,15 @@ static hipError_t gg_go(const uint16_t* x, int64_t t, int64_t k, const int* offs
                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)gg_lds<BM, NJ>());
   });
   if (e != hipSuccess) return e;
-  const int64_t tiles_n = (n + 128 * NJ - 1) / (128 * NJ), grid = (grouped_max_tiles(t, experts, BM) * tiles_n + 7) / 8 * 8;
+  const int64_t tiles_n = (n + 128 * NJ - 1) / (128 * NJ);
+  const int64_t grid = xcd_grid<32, BM == 256>(grouped_max_tiles(t, experts, BM) * tiles_n);
   k_w4a16_grouped_gemm<BM, NJ, TS, TY, G128><<<dim3((unsigned)grid), 256, gg_lds<BM, NJ>(), st>>>(
       x, t, k, offsets, experts, packed, scales, zeros, n, g, (TY*)y, (uint32_t)tiles_n);
   return hipGetLastError();
 }
 
 template <typename TS, typename TY, bool G128>
-static hipError_t gg_tile(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
+static hipError_t gg_size(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
                           const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                           hipStream_t st) {
   // Experts [11008, 4096], 8 of them, us with 256 x 256 / 128 x 128 / 64 x 128
@@ -334,8 +358,8 @@ template <typename TS, typename TY>
 static hipError_t gg_pick(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
                           const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                           hipStream_t st) {
-  if (g % 128 == 0) return gg_tile<TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gg_tile<TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  if (g % 128 == 0) return gg_size<TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gg_size<TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 hipError_t launch_w4a16_grouped_gemm(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
