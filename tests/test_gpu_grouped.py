@@ -38,10 +38,12 @@ SPLITS = {
     "wide": ([70, 0, 129, 33, 1, 256], 1, 30),
     "large": ([300, 257, 0, 511, 65], 0, 9),
 }
+# with these the tiles fill several rounds of the chip
+MANY = {"two": ([600, 500], 0, 3), "uneven": ([1000, 1, 129, 0, 700, 256], 2, 0), "dozen": ([100] * 7 + [0, 130, 260], 0, 0)}
 
 
 def offsets_of(split):
-    sizes, before, behind = SPLITS[split]
+    sizes, before, behind = {**SPLITS, **MANY}[split]
     off = np.concatenate([[0], np.cumsum(sizes)]) + before
     return off.astype(np.int32), int(off[-1]) + behind
 
@@ -109,29 +111,50 @@ def test_w4a16_exact(w4, split, n, k, g, xd, sz, out):
     assert torch.equal(c.tensor.cpu(), torch.from_numpy(want).to(dtype_of(out)))
 
 
+# whole tiles, halves and both, of every size
+@pytest.mark.parametrize("n,k", [(1400, 256), (5001, 128), (8000, 384), (14000, 128)])
+@pytest.mark.parametrize("split", sorted(MANY))
+def test_mxfp4_exact_many_tiles(w4, split, n, k):
+    test_mxfp4_exact(w4, split, n, k, "f32")
+
+
+@pytest.mark.parametrize("n,k,g", [(1400, 192, 64), (7168, 128, 128), (14001, 128, 32)])
+@pytest.mark.parametrize("split", sorted(MANY))
+def test_w4a16_exact_many_tiles(w4, split, n, k, g):
+    test_w4a16_exact(w4, split, n, k, g, "bf16", "f16", "bf16")
+
+
+@pytest.mark.parametrize("sz", ["f16", "f32"])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("split,n,k,g", [("few", 500, 4096, 128), ("padded", 260, 2048, 64), ("large", 300, 2048, 128),
                                          ("wide", 200, 1120, 32)])
-def test_w4a16_real(w4, split, n, k, g, out):
+def test_w4a16_real(w4, split, n, k, g, out, sz):
     off, t = offsets_of(split)
     e = len(off) - 1
     rng = np.random.default_rng(n + k)
     xt = to_dev(rng.normal(0, 1, (t, k)).astype(np.float32), "f32").to(torch.bfloat16)
     wt = to_dev(rng.normal(0, 0.02, (e * n, k)).astype(np.float32), "f32")
-    p, s, z = w4.quantize_pack_int4(wt, g)
+    p, s, z = w4.quantize_pack_int4(wt, g, torch.float16 if sz == "f16" else torch.float32)
     ng = k // g
     y = w4.w4a16_grouped_matmul(xt, to_dev32(off), p.view(e, n, k // 2), s.view(e, n, ng), z.view(e, n, ng), g,
                                 out=torch.zeros((t, n), dtype=dtype_of(out), device="cuda"))
     w = O.dequant_f64(to_host(p), to_host(s), to_host(z), g).reshape(e, n, k)
     x = xt.double().cpu().numpy()
-    ref, _ = MX.grouped(x, w, off, np.zeros((t, n)))
-    # The library multiplies x by 16 + q and takes (16 + zp) times the group's
-    # sum of x off again, so its sums are of terms up to |x| (16 + 15) s,
-    # twice, not |x w|: additions and the scale's rounding are off by 2^-23 of
-    # those sums.
+    ref, xw = MX.grouped(x, w, off, np.zeros((t, n)))
+    # Few rows an expert: the library multiplies x by 16 + q and takes
+    # (16 + zp) times the group's sum of x off again, so its sums are of terms
+    # up to |x| (16 + 15) s, twice, not |x w|: additions and the scale's
+    # rounding are off by 2^-23 of those sums.
     s64 = np.repeat(to_host(s).astype(np.float64).reshape(e, n, ng), g, -1)
     _, mag = MX.grouped(x, 62 * s64, off, np.zeros((t, n)))
-    assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, k + 2 * ng, out)).all()
+    # Many rows an expert: the weight is rounded to bf16, off by 2^-8 |w| at
+    # most, for bf16 results; for float32 ones what that rounding lacks is
+    # rounded in turn and added, which leaves 2^-8 2^-8 |w|, with float32
+    # scales too.  The weight itself, fma(q, s, -zp s), is off by two float32
+    # roundings of values up to 15 s: with x, 2^-23 of terms that mag has.
+    # Each adds its part of sum |x w| to the result's error before its rounding.
+    lost = xw * (2.0 ** -16 if out == "f32" else 2.0 ** -8 * (1 + 2.0 ** -8))
+    assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, k + 2 * ng, out) + lost).all()
 
 
 
@@ -159,14 +182,17 @@ def test_experts_layer(w4, fmt, split):
             q = w4.quantize_mxfp4(xin)
             xv = MX.values(to_host(q[0]), to_host(q[1]))
             ref, mag = MX.grouped(xv, wd, off, np.zeros(tuple(y.shape)))
+            lost = 0.0
         else:
             xv = xin.double().cpu().numpy()
-            ref, _ = MX.grouped(xv, wd, off, np.zeros(tuple(y.shape)))
+            ref, xw = MX.grouped(xv, wd, off, np.zeros(tuple(y.shape)))
             s64 = np.repeat(layer.scales.double().cpu().numpy(), layer.group_size, -1)
             _, mag = MX.grouped(xv, 62 * s64, off, np.zeros(tuple(y.shape)))
             # dequantize() rounds the weight to float32 once
             mag = mag * 1.01
-        assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, 2 * k, fin)).all()
+            # with many rows an expert the product rounds the weight too (test_w4a16_real)
+            lost = xw * (2.0 ** -16 if fin == "f32" else 2.0 ** -8 * (1 + 2.0 ** -8))
+        assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, 2 * k, fin) + lost).all()
 
 
 @pytest.mark.parametrize("fmt", ["int4", "mxfp4"])

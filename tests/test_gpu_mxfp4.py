@@ -129,6 +129,15 @@ def test_matmul_exact(w4, m, n, k, out):
     assert torch.equal(c.tensor.cpu(), want)
 
 
+# Many tiles: 256 x 256 and 256 x 192 ones, whole, in halves and both, with
+# and without a last half step of K, rows of y that start anywhere.
+@pytest.mark.parametrize("m,n,k", [(2000, 8190, 384), (1500, 4100, 256), (1530, 2999, 640), (2048, 4352, 128),
+                                   (1100, 13000, 256), (4200, 4501, 128)])
+def test_matmul_exact_many_tiles(w4, m, n, k):
+    test_matmul_exact(w4, m, n, k, "f32")
+    test_matmul_exact(w4, m, n, k, "bf16")
+
+
 def bound(y, mag, k, out):
     err = k * 2.0 ** -23 * mag
     return err if out == "f32" else err * (1 + 2.0 ** -8) + 2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(y)
