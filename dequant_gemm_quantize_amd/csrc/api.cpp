@@ -570,21 +570,17 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
-  // float32 x: multiply-adds.  bf16 x: by the rows that an expert has on
+  // float32 x goes to the few-row kernel, bf16 x by the rows that an expert has on
   // average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 85 us
   // against 92, 192 rows 117 against 88; with groups that are no multiple of
   // 128 its share of conversions is larger (256 rows of 16 experts [2048,
   // 2048], groups of 32: 51 against 39 us).
-  if (x_dtype == W4_F32)
-    return hip_status(w4::launch_w4a16_grouped_f32(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
-                                                   n, group_size, y, y_dtype, stream),
-                      fn);
-  if (t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
+  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);
-  return hip_status(w4::launch_w4a16_grouped_rows(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype, n,
-                                                  group_size, y, y_dtype, stream),
+  return hip_status(w4::launch_w4a16_grouped_rows(x, x_dtype, t, k, offsets, (int)experts, packed, scales, zeros,
+                                                  sz_dtype, n, group_size, y, y_dtype, stream),
                     fn);
 }
 

@@ -121,11 +121,8 @@ bool mx_gemm_fits(int64_t k);
 hipError_t launch_mx_gemm(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                           const uint8_t* scales, int64_t n, void* y, int y_dtype, const int* offsets,
                           int experts, hipStream_t st);
-// W4A16 by expert: float32 x, bf16 x with few rows an expert, and with many.
-hipError_t launch_w4a16_grouped_f32(const void* x, int64_t t, int64_t k, const int* offsets,
-                                int experts, const uint8_t* packed, const void* scales, const void* zeros,
-                                int sz_dtype, int64_t n, int g, void* y, int y_dtype, hipStream_t st);
-hipError_t launch_w4a16_grouped_rows(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
+// W4A16 by expert: few rows an expert or float32 x, and many rows.
+hipError_t launch_w4a16_grouped_rows(const void* x, int x_dtype, int64_t t, int64_t k, const int* offsets, int experts,
                                      const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
                                      int64_t n, int g, void* y, int y_dtype, hipStream_t st);
 bool w4a16_grouped_gemm_fits(int64_t k);

@@ -346,10 +346,12 @@ static hipError_t gg_size(const uint16_t* x, int64_t t, int64_t k, const int* of
                           hipStream_t st) {
   // Experts [11008, 4096], 8 of them, us with 256 x 256 / 128 x 128 / 64 x 128
   // tiles: 2048 rows 205 / 235 / 271, 1024 rows 198 / 136 / 162, 512 rows 180 /
-  // 112 / 100, 256 rows 179 / 99 / 74.
+  // 112 / 100, 256 rows 179 / 99 / 74.  (A launch has fewer than 2^32 threads,
+  // which the smallest tiles of the largest calls could exceed.)
   if (t > 192 * (int64_t)experts)
     return gg_go<256, 2, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  if (t > 80 * (int64_t)experts)
+  const bool too_many = grouped_max_tiles(t, experts, 64) * ((n + 127) / 128) >= (1 << 24) - 8;
+  if (t > 80 * (int64_t)experts || too_many)
     return gg_go<128, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
   return gg_go<64, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }

@@ -1,11 +1,13 @@
-// W4A16 product by expert for few rows an expert (decode), bf16 x:
+// W4A16 product by expert for few rows an expert (decode), bf16 x, and for any
+// number of rows, float32 x:
 //   y[t, n] = sum over groups j of s (sum_{k in j} x (16 + q) - (16 + zp) sum_{k in j} x)
 // on v_mfma_f32_16x16x32_bf16 (16 token rows, 16 weight rows).  16 + q is an
 // exact bfloat16 whose mantissa bits 3..6 are the code: a shift and an and-or
 // make a pair of operands, codes i and i + 4 of a word (x is put into that
 // order once a slice).  The sums of x come from the same instruction against
 // ones.  Nothing is rounded below float32; 16 rather than 128 + q keeps the
-// part that cancels small.
+// part that cancels small.  float32 x is the sum of three bf16 values (8 bits of
+// its 24 each), which take three MFMAs to a pair of codes converted once.
 //
 // Bound by the weight bytes, and close behind by the vector unit that turns
 // codes into operands.  A workgroup goes through RB blocks of 16 weight rows of
@@ -16,7 +18,9 @@
 // and its sums, in registers for all the blocks, and the codes and scales of
 // the next two blocks are in flight while one is computed.  The waves add
 // their sums through LDS at the end.  Two rows of two experts [11008, 4096]:
-// 16.4 us (2.8 TB/s); 16 rows of 64 experts [2048, 2048] 11.4 us.
+// 16.2 us (2.8 TB/s); 16 rows of 64 experts [2048, 2048] 11.5 us; float32 x
+// 18.7 and 16.9 us (multiply-adds of the vector unit, a weight row a lane, took
+// 129 and 83).
 //
 // The codes are loaded as 256-byte runs of a row (128 without G128) and
 // regrouped through the wave's own place in LDS, row t's 16-byte piece c at slot
@@ -68,6 +72,24 @@ __device__ __forceinline__ bf16x8 order_as_codes(u32x4 v) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// 8 consecutive float32 as hi + mid + lo, each bf16 in that order: the upper
+// halves of the words, of what they lack, and of what that lacks, which is exact.
+__device__ __forceinline__ void split_as_codes(u32x4 v0, u32x4 v1, bf16x8 (&out)[3]) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = __builtin_amdgcn_perm(v1[i], v0[i], 0x07060302u);
+      if (p < 2) {
+        v0[i] = __float_as_uint(__uint_as_float(v0[i]) - __uint_as_float(v0[i] & 0xffff0000u));
+        v1[i] = __float_as_uint(__uint_as_float(v1[i]) - __uint_as_float(v1[i] & 0xffff0000u));
+      }
+    }
+    out[p] = __builtin_bit_cast(bf16x8, r);
+  }
+}
+
 // The value that each of the wave's four rows of 16 lanes holds, in every row.
 __device__ __forceinline__ void spread4(uint32_t v, uint32_t (&out)[4]) {
   const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // rows 0 1 0 1 and 2 3 2 3
@@ -84,10 +106,13 @@ __device__ __forceinline__ float scale_value(uint32_t v) {
 
 }  // namespace
 
+// Most waves of a workgroup: 16 where the registers allow it.
+constexpr int gr_waves(size_t x_bytes, int sl) { return sl == 8 && x_bytes == 2 ? 16 : 8; }
+
 // SL: 32-column blocks of a wave's slice, 16 or 8.
-template <typename TS, typename TY, bool G128, int SL, int RB>
-__global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a16_grouped_rows(
-    const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
+template <typename TX, typename TS, typename TY, bool G128, int SL, int RB>
+__global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX), SL) / 4) void k_w4a16_grouped_rows(
+    const TX* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
     const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
     int g, TY* __restrict__ y, uint32_t tiles_n, int64_t tiles) {
   // [waves][16 tokens][16 RB rows] sums; before them 256 SL bytes a wave to regroup weights
@@ -98,7 +123,7 @@ __global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a
   const int l16 = lane & 15, h = lane >> 4;
   constexpr int RPL = 64 / SL, NC = 16 / RPL;  // rows a load covers, loads a block
   const int lp = lane % SL, lr = lane / SL;    // the lane's piece and row of them
-  const uint32_t ng = (uint32_t)(K / g), half = (uint32_t)(K / 2), xrow = (uint32_t)(2 * K);
+  const uint32_t ng = (uint32_t)(K / g), half = (uint32_t)(K / 2), xrow = (uint32_t)(sizeof(TX) * K);
   const int blocks32 = (int)(K / 32), slices = (blocks32 + SL - 1) / SL;
   const uint32_t bpg = (uint32_t)g / 32;
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
@@ -106,6 +131,7 @@ __global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   constexpr int NS = G128 ? SL / 4 : SL;  // scales of a row in a slice
   constexpr int D = RB < (G128 ? 3 : 2) ? RB : (G128 ? 3 : 2);  // blocks whose codes are held at a time
+  constexpr int NX = sizeof(TX) == 4 ? 3 : 1, WX = sizeof(TX) / 2;  // bf16 parts of x; 16-byte loads of 8 columns
   constexpr int NL = 2 * NS / 4;    // loads of them, a scale or zero-point a lane
   typedef typename std::conditional<sizeof(TS) == 2, uint16_t, uint32_t>::type Raw;
   u32x4* place = (u32x4*)part + 16 * SL * w;
@@ -153,28 +179,35 @@ __global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a
       };
 #pragma unroll
       for (int b = 0; b < D; ++b) load(b);
-      u32x4 xq[SL];  // G128: 8 q .. 8 q + 7 of block 4 j + h at 4 j + q; otherwise 8 h .. 8 h + 7 of block i
+      // G128: columns 8 q .. 8 q + 7 of block 4 j + h at 4 j + q; otherwise 8 h .. 8 h + 7 of block i
+      u32x4 xq[SL][WX];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         const int blk = G128 ? (i & ~3) + h : i;
         const uint32_t col = 32u * (uint32_t)(b0 + blk) + (G128 ? 8u * (i & 3) : 8u * h);
-        const uint32_t off = blk < nb ? (uint32_t)l16 * xrow + 2u * col : kPastEnd;
-        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
+        const uint32_t off = blk < nb ? (uint32_t)l16 * xrow + (uint32_t)sizeof(TX) * col : kPastEnd;
+#pragma unroll
+        for (int j = 0; j < WX; ++j)
+          xq[i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off + 16 * j, 0, 0));
       }
       // every load of the slice is on its way before anything waits for one
       // (the compiler would sink the codes' loads to their use behind this)
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      bf16x8 xv[SL];
+      bf16x8 xv[SL][NX];
 #pragma unroll
-      for (int i = 0; i < SL; ++i) xv[i] = order_as_codes(xq[i]);
+      for (int i = 0; i < SL; ++i)
+        if constexpr (NX == 1) xv[i][0] = order_as_codes(xq[i][0]);
+        else split_as_codes(xq[i][0], xq[i][1], xv[i]);
       f32x4 xs[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         xs[i] = zero;
 #pragma unroll
         for (int q = 0; q < SL / NS; ++q)
-          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q], ones, xs[i], 0, 0, 0);
+#pragma unroll
+          for (int p = 0; p < NX; ++p)
+            xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q][p], ones, xs[i], 0, 0, 0);
       }
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
@@ -214,9 +247,12 @@ __global__ __launch_bounds__(SL == 16 ? 512 : 1024, SL == 16 ? 2 : 4) void k_w4a
 #pragma unroll
         for (int q = 0; q < SL / NS; ++q)
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
-            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q], codes16(words[SL / NS * i + q], nk), d[i], 0,
-                                                           0, 0);
+          for (int i = 0; i < NS; ++i) {
+            const bf16x8 c = codes16(words[SL / NS * i + q], nk);
+#pragma unroll
+            for (int p = 0; p < NX; ++p)
+              d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q][p], c, d[i], 0, 0, 0);
+          }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const float sc = val[i], nz = -sc * (16.0f + val[NS + i]);
@@ -260,58 +296,57 @@ static int grouped_rows_waves(int64_t k, int sl, int most) {
   return (int)((slices + per - 1) / per);
 }
 
-template <typename TS, typename TY, bool G128, int SL, int RB>
-static hipError_t gr_rb(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
-                        const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
-                        hipStream_t st) {
+template <typename TX, typename TS, typename TY, bool G128, int SL, int RB>
+static hipError_t gr_rb(const TX* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
+                        const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
   const int64_t tiles_n = (n + 16 * RB - 1) / (16 * RB), tiles = grouped_max_tiles(t, experts, 16) * tiles_n;
-  const int nw = grouped_rows_waves(k, SL, 128 / SL);
+  const int nw = grouped_rows_waves(k, SL, gr_waves(sizeof(TX), SL));
   const size_t sums = (size_t)nw * 1024 * RB, places = (size_t)nw * 256 * SL;
   const dim3 grid((unsigned)(tiles < kGRowsGrid ? tiles : kGRowsGrid));
-  k_w4a16_grouped_rows<TS, TY, G128, SL, RB><<<grid, 64 * nw, sums > places ? sums : places, st>>>(
+  k_w4a16_grouped_rows<TX, TS, TY, G128, SL, RB><<<grid, 64 * nw, sums > places ? sums : places, st>>>(
       x, t, k, offsets, experts, packed, scales, zeros, n, g, (TY*)y, (uint32_t)tiles_n, tiles);
   return hipGetLastError();
 }
 
-template <typename TS, typename TY, bool G128>
-static hipError_t gr_go(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
-                        const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
-                        hipStream_t st) {
+template <typename TX, typename TS, typename TY>
+static hipError_t gr_pick(const void* xv, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
+                          const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
+  const TX* x = (const TX*)xv;
   // Groups that end at any block keep a scale for each: one block of rows a
   // workgroup, of 256-column slices, is what fits the registers (16 rows of 64
   // experts [2048, 2048], groups of 32: 22 us against 30 with two).
-  if constexpr (!G128) {
-    return gr_rb<TS, TY, false, 8, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  } else {
-    switch (rows_per_group<6>(grouped_max_tiles(t, experts, 16), (n + 15) / 16)) {
-      case 1: return gr_rb<TS, TY, true, 16, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-      case 2: return gr_rb<TS, TY, true, 16, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-      case 4: return gr_rb<TS, TY, true, 16, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-      default: return gr_rb<TS, TY, true, 16, 6>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    }
+  if (g % 128 != 0)
+    return gr_rb<TX, TS, TY, false, 8, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  // The three parts of float32 x take the registers of twice the columns.
+  constexpr int SL = sizeof(TX) == 2 ? 16 : 8;
+  switch (rows_per_group<6>(grouped_max_tiles(t, experts, 16), (n + 15) / 16)) {
+    case 1: return gr_rb<TX, TS, TY, true, SL, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    case 2: return gr_rb<TX, TS, TY, true, SL, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    case 4: return gr_rb<TX, TS, TY, true, SL, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    default: return gr_rb<TX, TS, TY, true, SL, 6>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
   }
 }
 
-template <typename TS, typename TY>
-static hipError_t gr_pick(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
-                          const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
-                          hipStream_t st) {
-  if (g % 128 == 0) return gr_go<TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gr_go<TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-}
-
-hipError_t launch_w4a16_grouped_rows(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
-                                     const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
-                                     int64_t n, int g, void* y, int y_dtype, hipStream_t st) {
-  const uint16_t* xb = (const uint16_t*)x;
+template <typename TX>
+static hipError_t gr_types(const void* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
+                           const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y, int y_dtype,
+                           hipStream_t st) {
   if (sz_dtype == W4_F16) {
     if (y_dtype == W4_F32)
-      return gr_pick<_Float16, float>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    return gr_pick<_Float16, uint16_t>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+      return gr_pick<TX, _Float16, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return gr_pick<TX, _Float16, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
   }
   if (y_dtype == W4_F32)
-    return gr_pick<float, float>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gr_pick<float, uint16_t>(xb, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return gr_pick<TX, float, float>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gr_pick<TX, float, uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+}
+
+hipError_t launch_w4a16_grouped_rows(const void* x, int x_dtype, int64_t t, int64_t k, const int* offsets, int experts,
+                                     const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
+                                     int64_t n, int g, void* y, int y_dtype, hipStream_t st) {
+  if (x_dtype == W4_F32)
+    return gr_types<float>(x, t, k, offsets, experts, packed, scales, zeros, sz_dtype, n, g, y, y_dtype, st);
+  return gr_types<uint16_t>(x, t, k, offsets, experts, packed, scales, zeros, sz_dtype, n, g, y, y_dtype, st);
 }
 
 }  // namespace w4

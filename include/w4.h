@@ -352,8 +352,9 @@ int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64
 /*
  * mxfp4_matmul -- y [M, N] = dequant(xq) . dequant(W)^T with both operands in
  * MXFP4: xq [M, K/2] and xs [M, K/32] from quantize_mxfp4 of the activations,
- * packed and scales those of the weights.  Products are exact; sums are
- * float32 and rounded once to y_dtype (W4_BF16 or W4_F32).  Deterministic.
+ * packed and scales those of the weights.  Products are exact in
+ * float32 (below 2^-149 they vanish); sums are float32 and rounded once to
+ * y_dtype (W4_BF16 or W4_F32).  Deterministic.
  */
 int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, const uint8_t* packed,
                  const uint8_t* scales, int64_t n, void* y, int y_dtype, hipStream_t stream);
@@ -381,7 +382,8 @@ int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, con
  *   rounded once to bf16, as in w4a16_matmul, for W4_BF16 y, and to the sum of
  *   two bf16 values (exact with W4_F16 scales and whole zero-points) for
  *   W4_F32 y; otherwise a code and its zero-point multiply x exactly and a
- *   group's sum takes its scale.  Deterministic.
+ *   group's sum takes its scale.  Deterministic.  A row of x that holds an
+ *   infinity may give NaN.
  */
 int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_t k, const int32_t* offsets,
                          int64_t experts, const uint8_t* packed, const uint8_t* scales, int64_t n, void* y,

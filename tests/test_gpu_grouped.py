@@ -111,6 +111,16 @@ def test_w4a16_exact(w4, split, n, k, g, xd, sz, out):
     assert torch.equal(c.tensor.cpu(), torch.from_numpy(want).to(dtype_of(out)))
 
 
+# few rows and many weight rows: workgroups of 1, 2, 4 and 6 blocks of 16 weight rows
+@pytest.mark.parametrize("n,k,g", [(4001, 512, 128), (8001, 640, 128), (11001, 1152, 384), (17003, 4480, 128),
+                                   (9001, 544, 32)])
+@pytest.mark.parametrize("split", ["one", "few"])
+def test_exact_many_weight_rows(w4, split, n, k, g):
+    test_mxfp4_exact(w4, split, n, k, "f32")
+    test_w4a16_exact(w4, split, n, k, g, "bf16", "f16", "bf16")
+    test_w4a16_exact(w4, split, n, k, g, "f32", "f32", "f32")
+
+
 # whole tiles, halves and both, of every size
 @pytest.mark.parametrize("n,k", [(1400, 256), (5001, 128), (8000, 384), (14000, 128)])
 @pytest.mark.parametrize("split", sorted(MANY))
@@ -156,6 +166,27 @@ def test_w4a16_real(w4, split, n, k, g, out, sz):
     lost = xw * (2.0 ** -16 if out == "f32" else 2.0 ** -8 * (1 + 2.0 ** -8))
     assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, k + 2 * ng, out) + lost).all()
 
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("split,n,k,g", [("few", 500, 4096, 128), ("padded", 260, 2048, 64), ("wide", 200, 1120, 32),
+                                         ("one", 9000, 1280, 256)])
+def test_w4a16_real_float32_x(w4, split, n, k, g, out):
+    """float32 x, of which the library adds three parts: 3 K additions in place of K in test_w4a16_real's bound,
+    and no rounded weight.  Values from 2^-60 to 2^60 side by side in different rows."""
+    off, t = offsets_of(split)
+    e, ng = len(off) - 1, k // g
+    rng = np.random.default_rng(n + k)
+    x = (rng.normal(0, 1, (t, k)) * np.ldexp(1.0, rng.integers(-60, 61, (t, 1)))).astype(np.float32)
+    p, s, z = w4.quantize_pack_int4(to_dev(rng.normal(0, 0.02, (e * n, k)).astype(np.float32), "f32"), g)
+    y = w4.w4a16_grouped_matmul(to_dev(x, "f32"), to_dev32(off), p.view(e, n, k // 2), s.view(e, n, ng),
+                                z.view(e, n, ng), g, out=torch.zeros((t, n), dtype=dtype_of(out), device="cuda"))
+    w = O.dequant_f64(to_host(p), to_host(s), to_host(z), g).reshape(e, n, k)
+    x = x.astype(np.float64)
+    ref, _ = MX.grouped(x, w, off, np.zeros((t, n)))
+    s64 = np.repeat(to_host(s).astype(np.float64).reshape(e, n, ng), g, -1)
+    _, mag = MX.grouped(x, 62 * s64, off, np.zeros((t, n)))
+    assert (np.abs(y_as_f64(y) - ref) <= bound(ref, mag, 3 * k + 2 * ng, out)).all()
 
 
 @pytest.mark.parametrize("fmt", ["int4", "mxfp4"])

@@ -138,6 +138,15 @@ def test_matmul_exact_many_tiles(w4, m, n, k):
     test_matmul_exact(w4, m, n, k, "bf16")
 
 
+# Few rows and many weight rows: workgroups of 1, 2, 4 and 6 blocks of 16 weight
+# rows, whole slices of K and a partial one, one or two slices a wave.
+@pytest.mark.parametrize("m,n,k", [(1, 8001, 544), (16, 11001, 512), (3, 20003, 96), (9, 17000, 1056), (20, 8001, 544),
+                                   (32, 11001, 512), (40, 4600, 1024), (130, 4600, 160), (2, 700, 8736)])
+def test_matmul_exact_many_weight_rows(w4, m, n, k):
+    test_matmul_exact(w4, m, n, k, "f32")
+    test_matmul_exact(w4, m, n, k, "bf16")
+
+
 def bound(y, mag, k, out):
     err = k * 2.0 ** -23 * mag
     return err if out == "f32" else err * (1 + 2.0 ** -8) + 2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(y)
