@@ -202,12 +202,16 @@ __global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX),
       f32x4 xs[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
+        f32x4 low = zero;
         xs[i] = zero;
 #pragma unroll
-        for (int q = 0; q < SL / NS; ++q)
+        for (int q = 0; q < SL / NS; ++q) {
+          const bf16x8(&v)[NX] = xv[SL / NS * i + q];
+          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], ones, xs[i], 0, 0, 0);
 #pragma unroll
-          for (int p = 0; p < NX; ++p)
-            xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q][p], ones, xs[i], 0, 0, 0);
+          for (int p = 1; p < NX; ++p) low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[p], ones, low, 0, 0, 0);
+        }
+        if constexpr (NX > 1) xs[i] += low;
       }
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
@@ -241,20 +245,24 @@ __global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX),
 #pragma unroll
           for (int k = 0; k < 4; ++k) val[4 * i + k] = scale_value<TS>(v[k]);
         }
-        f32x4 d[NS];
+        // the lower parts' sums are small and rounded finely; added once, they
+        // cost the upper part's one rounding
+        f32x4 d[NS], low[NS];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) d[i] = zero;
+        for (int i = 0; i < NS; ++i) d[i] = low[i] = zero;
 #pragma unroll
         for (int q = 0; q < SL / NS; ++q)
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
             const bf16x8 c = codes16(words[SL / NS * i + q], nk);
+            const bf16x8(&v)[NX] = xv[SL / NS * i + q];
+            d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], c, d[i], 0, 0, 0);
 #pragma unroll
-            for (int p = 0; p < NX; ++p)
-              d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[SL / NS * i + q][p], c, d[i], 0, 0, 0);
+            for (int p = 1; p < NX; ++p) low[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[p], c, low[i], 0, 0, 0);
           }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
+          if constexpr (NX > 1) d[i] += low[i];
           const float sc = val[i], nz = -sc * (16.0f + val[NS + i]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[b][r] = fmaf(sc, d[i][r], fmaf(nz, xs[i][r], acc[b][r]));
