@@ -43,7 +43,8 @@ constexpr uint32_t kPastEnd = 0x80000000u;  // beyond every resource: their size
 // takes a contiguous eighth of the list, SLOTS tiles at a time (32 CUs times
 // the workgroups that one holds).  With SPLIT, tiles beyond the last whole round
 // of SLOTS are split into halves of half the rows when all the halves fit one
-// round, which then takes 0.6 of the time.  `half` is -1 (a whole tile), 0 or 1.
+// round, which then takes 0.6 of the time (2048 x 4096 x 11008 in MXFP4 63 us
+// without, 58 with; INT4 by expert 4096 rows 411 and 381).  `half` is -1 (a whole tile), 0 or 1.
 // False: nothing to do.  A launch has xcd_grid(tiles) workgroups.
 template <uint32_t SLOTS, bool SPLIT>
 __device__ __forceinline__ bool xcd_tile(uint32_t total, uint32_t& tile, int& half) {

@@ -3,6 +3,20 @@
 // on v_mfma_scale_f32_32x32x64_f8f6f4: lane (r = lane % 32, h = lane / 32) holds
 // 16 bytes (one block of 32 columns) of row r of each operand and that
 // block's scale byte, so the scales cost no instruction of their own.
+//
+// Bound by three things that lie close together.  The operands of an FP4 MFMA
+// (2 KB, 32 cycles) take LDS twice as long as a CU's four MFMAs if each is read
+// for one alone, so a wave has a large block of outputs (128 x 128 of the
+// workgroup's 256 x 256, 256 accumulators a lane): LDS is then busy half of the
+// MFMAs' time.  The matrix cores on real data are held back by power (a loop
+// of nothing but these MFMAs reaches 6.6 - 7.2 PFLOP/s on random codes and over
+// 9 on zeros).  And the tiles come from L2, 64 KB a K step and CU, which takes
+// about a step's time and has to be asked for one and a half steps ahead.  y
+// is a third of the bytes at K = 4096.
+// Measured: 512 x 28672 x 8192 65 us of kernel time (3.7 PFLOP/s), 2048 x
+// 11008 x 4096 55 us (3.4), 4096 x 8192 x 8192 130 us (4.2); 4096 rows by
+// expert, 8 of [11008, 4096], 132 us (2.8: the experts' last tiles).  Matrix
+// cores are busy a third of that time.
 #include <type_traits>
 
 #include "grouped.h"

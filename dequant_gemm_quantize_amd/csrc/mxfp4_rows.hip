@@ -8,9 +8,16 @@
 // rows, all of K, for up to 16 MT token rows.  Its waves have a 512-column slice
 // of K each (or take such slices in turn), keep x of it in registers for all
 // the blocks, and add their sums through LDS at the end.  The weights of the
-// next two blocks are in flight while one is computed.  One block a workgroup
+// next block are in flight while one is computed.  One block a workgroup
 // was slower: the launch then has so many waves that starting them (about 13
 // cycles a wave on each XCD) takes longer than reading the weights.
+//
+// Measured: one row times [11008, 4096] 7.4 us (3.2 TB/s), [28672, 8192] 26.2 us
+// (4.8 TB/s), [8192, 28672] 23.3 us (5.4 TB/s), 16 rows of 64 experts [2048,
+// 2048] 8.8 us of which the bytes of the experts with rows take 6.2.  More token
+// rows cost time of their own, since every workgroup reads x of its slices
+// (64 rows times [4096, 11008] 19 us against 6.6 for one).  16 waves in place of 8
+// where a workgroup has one block: 7.2 us against 6.6 for [4096, 11008].
 //
 // Any K that is a multiple of 32: the last, partial slice is loaded block by
 // block, and blocks past K count as zero.
@@ -48,7 +55,9 @@ __global__ __launch_bounds__(512, 2) void k_mx_rows(const uint8_t* __restrict__ 
   const int l16 = lane & 15, h = lane >> 4;
   const int64_t kb = K / 32, half = K / 2;
   const int full = (int)(K / kMxSlice), slices = (int)((K + kMxSlice - 1) / kMxSlice);
-  constexpr int D = RB < 3 ? RB : 3;  // blocks whose weights are held at a time
+  // blocks whose weights are held at a time (three or four were slower: one row
+  // times [28672, 8192] 26.2, 27.2 and 28.4 us)
+  constexpr int D = RB < 2 ? 1 : 2;
 
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     int64_t r0, rend, n0;  // token rows r0 .. rend - 1 at most 16 MT of them, weight rows from n0

@@ -18,6 +18,12 @@
 // 64 rows into bf16 operands.  Lane (r, h) of an operand holds row r; of the
 // step's 64 columns it has the 32 that its half h reads as one 16-byte piece
 // of codes, the same permutation of K on both operands.
+//
+// Bound by the wave's own instructions: 4.9 vector instructions an MFMA leave
+// the matrix cores busy 48% of the time, at one wave a SIMD, and no other order
+// of conversions and MFMAs did better (372 - 381 us all).  4096 rows of 8
+// experts [11008, 4096] 380 us (0.97 PFLOP/s); a large bf16 product of the
+// library reaches 1.53.  1024 rows 139 us.
 #include <type_traits>
 
 #include "grouped.h"

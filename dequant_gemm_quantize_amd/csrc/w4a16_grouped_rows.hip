@@ -16,10 +16,10 @@
 // longer than reading the weights).  Its waves have a slice of K each, 512
 // columns with G128 (or take such slices in turn): a wave keeps x of its slice,
 // and its sums, in registers for all the blocks, and the codes and scales of
-// the next two blocks are in flight while one is computed.  The waves add
+// the next block are in flight while one is computed.  The waves add
 // their sums through LDS at the end.  Two rows of two experts [11008, 4096]:
-// 16.2 us (2.8 TB/s); 16 rows of 64 experts [2048, 2048] 11.5 us; float32 x
-// 18.7 and 16.9 us (multiply-adds of the vector unit, a weight row a lane, took
+// 14.6 us (3.1 TB/s); 16 rows of 64 experts [2048, 2048] 11.6 us; float32 x
+// 17.6 and 16.9 us (multiply-adds of the vector unit, a weight row a lane, took
 // 129 and 83).
 //
 // The codes are loaded as 256-byte runs of a row (128 without G128) and
@@ -130,7 +130,9 @@ __global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX),
   const Nib16 nk = Nib16::make();
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   constexpr int NS = G128 ? SL / 4 : SL;  // scales of a row in a slice
-  constexpr int D = RB < (G128 ? 3 : 2) ? RB : (G128 ? 3 : 2);  // blocks whose codes are held at a time
+  // blocks whose codes are held at a time (with three the sums of six blocks
+  // left no registers: 16.5 us against 14.6 for two rows of [11008, 4096])
+  constexpr int D = RB < 2 ? 1 : 2;
   constexpr int NX = sizeof(TX) == 4 ? 3 : 1, WX = sizeof(TX) / 2;  // bf16 parts of x; 16-byte loads of 8 columns
   constexpr int NL = 2 * NS / 4;    // loads of them, a scale or zero-point a lane
   typedef typename std::conditional<sizeof(TS) == 2, uint16_t, uint32_t>::type Raw;

@@ -284,3 +284,32 @@ def test_offsets_out_of_order_stay_in_bounds(w4, fmt, cuts):
     layer(torch.randn((t, k), device="cuda"), to_dev32(np.array(cuts)), out=c.tensor)
     c.check()
     assert torch.isfinite(c.tensor).all()
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("fmt", ["int4", "mxfp4"])
+def test_last_expert_of_many_gigabytes(w4, fmt, rows):
+    """Codes of 5 GB: the last expert's rows equal the same call with that expert alone, and the dense product.
+    x is -1, 0 or 1 and weights are multiples of 2^-3 up to 15: sums below 2^19, exact in any order."""
+    e, n, k, g = 20, 16384, 32768, 128
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    packed = torch.randint(0, 256, (e, n, k // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    off = torch.full((e + 1,), 0, dtype=torch.int32, device="cuda")
+    off[e] = rows
+    alone = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    x = torch.randint(-1, 2, (rows, k), device="cuda", generator=gen).to(torch.bfloat16)
+    if fmt == "mxfp4":
+        scales = torch.randint(126, 129, (e, n, k // 32), dtype=torch.uint8, device="cuda", generator=gen)
+        xq = w4.quantize_mxfp4(x)
+        y = w4.mxfp4_grouped_matmul(*xq, off, packed, scales)
+        want = w4.mxfp4_grouped_matmul(*xq, alone, packed[-1:], scales[-1:])
+        dense = w4.mxfp4_matmul(*xq, packed[-1], scales[-1])
+    else:
+        scales = torch.randint(0, 4, (e, n, k // g), device="cuda", generator=gen)
+        scales = (0.125 * 2.0 ** scales).to(torch.float16)
+        zeros = torch.randint(0, 16, (e, n, k // g), device="cuda", generator=gen).to(torch.float16)
+        y = w4.w4a16_grouped_matmul(x, off, packed, scales, zeros, g)
+        want = w4.w4a16_grouped_matmul(x, alone, packed[-1:], scales[-1:], zeros[-1:], g)
+        dense = w4.w4a16_matmul(x, packed[-1], scales[-1], zeros[-1], g)
+    assert torch.equal(y, want) and torch.equal(y, dense)
+    assert y.float().abs().max() > 0
