@@ -12,7 +12,7 @@
 // columns: no two waves dequantize the same weight, and a wave's accumulators
 // (8 x 2 blocks at BM = 256) are reused against 64 KB of LDS reads a K step
 // of 64 columns, which is half of what LDS gives in the step's MFMA time.
-// x goes from memory to LDS directly, two stages of 64 columns (128-byte
+// x goes from memory to LDS directly, S stages of 64 columns (128-byte
 // lines); the packed weights the same way, two stages of 256 columns (again
 // 128-byte lines), and from there to registers, where each wave turns its own
 // 64 rows into bf16 operands.  Lane (r, h) of an operand holds row r; of the
@@ -22,8 +22,8 @@
 // Bound by the wave's own instructions: 4.9 vector instructions an MFMA leave
 // the matrix cores busy 48% of the time, at one wave a SIMD, and no other order
 // of conversions and MFMAs did better (372 - 381 us all).  4096 rows of 8
-// experts [11008, 4096] 380 us (0.97 PFLOP/s); a large bf16 product of the
-// library reaches 1.53.  1024 rows 139 us.
+// experts [11008, 4096] 375 us (0.98 PFLOP/s); a large bf16 product of the
+// library reaches 1.53.  1024 rows 137 us.
 #include <type_traits>
 
 #include "grouped.h"
@@ -67,14 +67,14 @@ __device__ __forceinline__ void dequant_pairs(uint32_t p, float s, float b, u32x
   }
 }
 
-template <int BM, int NJ> constexpr size_t gg_lds() { return 2 * (size_t)(BM + 128 * NJ) * GLine; }
+template <int BM, int NJ, int S> constexpr size_t gg_lds() { return (size_t)(S * BM + 2 * 128 * NJ) * GLine; }
 
 }  // namespace
 
 // One tile: rows m0 .. min(m0 + BM, mend) - 1 of y, columns from n0, for the
-// expert whose first weight row is ebase.  G128: g % 128 == 0, so two steps of
+// expert whose first weight row is ebase.  S: stages of x.  G128: g % 128 == 0, so two steps of
 // a stage share a scale.
-template <int BM, int NJ, typename TS, typename TY, bool G128>
+template <int BM, int NJ, int S, typename TS, typename TY, bool G128>
 __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uint16_t* __restrict__ x, int64_t K,
                                         const uint8_t* __restrict__ packed, const void* __restrict__ scales,
                                         const void* __restrict__ zeros, int64_t N, int g, TY* __restrict__ y, int64_t m0,
@@ -107,12 +107,12 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
     wo[i] = (uint32_t)row * wrow + 16u * (slot ^ ((row >> 1) & 7));
   }
   const int nks = (int)(K / 64);
-  uint8_t* sw = sgg + 2 * A_STAGE;
+  uint8_t* sw = sgg + S * A_STAGE;
   // steps and stages past the last lie outside the resources
   auto x_issue = [&](int ks) {
     const uint32_t o = ks < nks ? (uint32_t)ks * GLine : kPastEnd;
 #pragma unroll
-    for (int i = 0; i < LA; ++i) load_lds(xr, sgg + (ks & 1) * A_STAGE + 1024 * (w * LA + i), xo[i] + o);
+    for (int i = 0; i < LA; ++i) load_lds(xr, sgg + ks % S * A_STAGE + 1024 * (w * LA + i), xo[i] + o);
   };
   auto w_issue = [&](int st) {
     const uint32_t o = 4 * st < nks ? (uint32_t)st * GLine : kPastEnd;
@@ -162,7 +162,7 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
   u32x4 xv[2][MI];
   auto x_frag = [&](int ks, auto tc) {
     constexpr int t = decltype(tc)::value;
-    const uint8_t* a = sgg + (ks & 1) * A_STAGE + fo[t];
+    const uint8_t* a = sgg + ks % S * A_STAGE + fo[t];
 #pragma unroll
     for (int i = 0; i < MI; ++i) xv[t & 1][i] = *(const u32x4*)(a + 32 * GLine * i);
   };
@@ -218,9 +218,9 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
 
   s_issue(0);
   w_issue(0);
-  x_issue(0);
-  x_issue(1);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LA) : "memory");  // all but step 1's x
+#pragma unroll
+  for (int p = 0; p < S; ++p) x_issue(p);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * LA) : "memory");  // all but the x of the steps behind the first
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   s_take();
@@ -234,8 +234,13 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
   // has read all of the step's x and waited for its share of the next step's;
   // behind the barrier that is whole and this step's x stage is free.  The
   // next step's codes are read a slice earlier still: their stage has been
-  // whole since the barrier of u = 1.  (More stages of x made no difference:
-  // a step waits for its conversions, not for memory.)
+  // whole since the barrier of u = 2.  The wait leaves the x of S - 2 further
+  // steps on its way, and behind the barrier of u = 0 also the weights issued
+  // there (they are older than what the other waits leave).  A step of 64-row
+  // tiles is too short for a load: four stages there took 777 rows of 16
+  // experts [2050, 2048], bf16 y, from 39 to 35 us.  Larger tiles wait for their
+  // conversions, and more stages would cost the second workgroup of a CU
+  // (1024 rows of 8 experts [11008, 4096]: two stages 135 us, three 143, four 162).
   auto step = [&](int ks, auto uc) {
     constexpr int u = decltype(uc)::value;
     x_frag(ks, c1);
@@ -251,13 +256,13 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
     dequant(c3, uc);
     mma(c2);
     mix();
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * LA + (u == 1 && S > 2 ? LW : 0)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if constexpr (u == 0) w_issue(ks / 4 + 1);
     if constexpr (u == 1) s_issue(ks / 4 + 1);
     if constexpr (u == 3) s_take();
-    x_issue(ks + 2);
+    x_issue(ks + S);
     c_take();
     x_frag(ks + 1, c0);
     dequant(c0, std::integral_constant<int, (u + 1) & 3>{});
@@ -282,12 +287,14 @@ __device__ __forceinline__ void gg_tile(uint8_t* sgg, int lane, int w, const uin
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   constexpr int TURN = turn_bytes<TY, NJ>();
-  static_assert(4 * TURN <= (int)gg_lds<BM, NJ>(), "the waves' turning places fit in LDS");
+  static_assert(4 * TURN <= (int)gg_lds<BM, NJ, S>(), "the waves' turning places fit in LDS");
   turn_store<TY, MI, NJ>(sgg + w * TURN, lane, acc, y, N, m0, mend, n0 + 32 * NJ * w);
 }
 
-template <int BM, int NJ, typename TS, typename TY, bool G128>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) void k_w4a16_grouped_gemm(
+// (LDS holds two workgroups of 64-row tiles; registers for three were 4%
+// faster than the compiler's larger use of them.)
+template <int BM, int NJ, int S, typename TS, typename TY, bool G128>
+__global__ __launch_bounds__(256, BM == 256 ? 1 : BM == 64 ? 3 : 2) void k_w4a16_grouped_gemm(
     const uint16_t* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
     const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
     int g, TY* __restrict__ y, uint32_t tiles_n) {
@@ -319,29 +326,29 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : NJ == 1 && BM == 64 ? 3 : 2) v
   // half a tile, or one with rows in its upper half only, takes half the time
   if constexpr (BM > 64) {
     if (half >= 0 || mend - m0 <= BM / 2) {
-      gg_tile<BM / 2, NJ, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
+      gg_tile<BM / 2, NJ, S, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
       return;
     }
   }
-  gg_tile<BM, NJ, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
+  gg_tile<BM, NJ, S, TS, TY, G128>(sgg, lane, w, x, K, packed, scales, zeros, N, g, y, m0, mend, n0, ebase);
 }
 
 // K % 64 == 0: whole steps; 256 rows of K bf16 stay below 2^31 bytes.
 bool w4a16_grouped_gemm_fits(int64_t k) { return k % 64 == 0 && k <= ((int64_t)1 << 21); }
 
-template <int BM, int NJ, typename TS, typename TY, bool G128>
+template <int BM, int NJ, int S, typename TS, typename TY, bool G128>
 static hipError_t gg_go(const uint16_t* x, int64_t t, int64_t k, const int* offsets, int experts,
                         const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                         hipStream_t st) {
   static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
   const hipError_t e = once_per_device(attr_done, [] {
-    return hipFuncSetAttribute((const void*)k_w4a16_grouped_gemm<BM, NJ, TS, TY, G128>,
-                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)gg_lds<BM, NJ>());
+    return hipFuncSetAttribute((const void*)k_w4a16_grouped_gemm<BM, NJ, S, TS, TY, G128>,
+                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)gg_lds<BM, NJ, S>());
   });
   if (e != hipSuccess) return e;
   const int64_t tiles_n = (n + 128 * NJ - 1) / (128 * NJ);
   const int64_t grid = xcd_grid<32, BM == 256>(grouped_max_tiles(t, experts, BM) * tiles_n);
-  k_w4a16_grouped_gemm<BM, NJ, TS, TY, G128><<<dim3((unsigned)grid), 256, gg_lds<BM, NJ>(), st>>>(
+  k_w4a16_grouped_gemm<BM, NJ, S, TS, TY, G128><<<dim3((unsigned)grid), 256, gg_lds<BM, NJ, S>(), st>>>(
       x, t, k, offsets, experts, packed, scales, zeros, n, g, (TY*)y, (uint32_t)tiles_n);
   return hipGetLastError();
 }
@@ -351,15 +358,15 @@ static hipError_t gg_size(const uint16_t* x, int64_t t, int64_t k, const int* of
                           const uint8_t* packed, const void* scales, const void* zeros, int64_t n, int g, void* y,
                           hipStream_t st) {
   // Experts [11008, 4096], 8 of them, us with 256 x 256 / 128 x 128 / 64 x 128
-  // tiles: 2048 rows 205 / 235 / 271, 1024 rows 198 / 136 / 162, 512 rows 180 /
-  // 112 / 100, 256 rows 179 / 99 / 74.  (A launch has fewer than 2^32 threads,
+  // tiles (each with two stages of x): 2048 rows 205 / 235 / 271, 1024 rows 198 /
+  // 136 / 162, 512 rows 180 / 112 / 100, 256 rows 179 / 99 / 74.  (A launch has fewer than 2^32 threads,
   // which the smallest tiles of the largest calls could exceed.)
   if (t > 192 * (int64_t)experts)
-    return gg_go<256, 2, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return gg_go<256, 2, 2, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
   const bool too_many = grouped_max_tiles(t, experts, 64) * ((n + 127) / 128) >= (1 << 24) - 8;
   if (t > 80 * (int64_t)experts || too_many)
-    return gg_go<128, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  return gg_go<64, 1, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    return gg_go<128, 1, 2, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gg_go<64, 1, 4, TS, TY, G128>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 template <typename TS, typename TY>
