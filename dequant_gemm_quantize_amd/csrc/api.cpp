@@ -504,12 +504,12 @@ int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64
 }
 
 // Kernel choice.  By expert the many-row kernel takes over at 8 rows an expert
-// on average (64 rows of 8 experts [11008, 4096]: 43 against 44 us; 128 rows 43
-// against 65).  Dense, up to 32 rows go to the few-row kernel ([11008, 4096]:
+// on average (64 rows of 8 experts [11008, 4096]: 42.5 against 41.6 us; 96 rows
+// 42 against 61).  Dense, up to 32 rows go to the few-row kernel ([11008, 4096]:
 // 9.4 against 10.9 us at 16 rows, equal at 32); up to 128 rows the many-row
 // kernel's time goes with K alone while its tiles leave CUs idle, the few-row
 // kernel's with N * K, and N = 4608 is about where they meet (64 rows of
-// [11008, 4096]: 20 against 12 us, of [4096, 11008]: 19 against 24).
+// [11008, 4096]: 20 against 10.5 us, of [4096, 11008]: 19 against 24).
 static int mx_product(const char* fn, const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k,
                       const int32_t* offsets, int64_t experts, const uint8_t* packed, const uint8_t* scales,
                       int64_t n, void* y, int y_dtype, hipStream_t stream) {
@@ -570,12 +570,14 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "scales", scales));
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
-  // float32 x goes to the few-row kernel, bf16 x by the rows that an expert has on
-  // average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 85 us
-  // against 92, 192 rows 117 against 88; with groups that are no multiple of
-  // 128 its share of conversions is larger (256 rows of 16 experts [2048,
-  // 2048], groups of 32: 51 against 39 us).
-  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
+  // float32 x goes to the few-row kernel, bf16 x by the rows that an expert has
+  // on average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 78 us
+  // against 77, 192 rows 108 against 77.  With groups that are no multiple of
+  // 128 its share of conversions is larger: groups of 64, 32 rows of the same
+  // 149 against 98, 64 rows of 16 experts [2048, 2048] 25.8 against 22.7; but
+  // 16 rows there 17.5 against 21.3, and 16 rows of 8 experts [4096, 11008] 83
+  // against 106.
+  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 3) * experts && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);

@@ -35,6 +35,7 @@ SPLITS = {
     "empty": ([0, 0, 0], 0, 5),
     "padded": ([3, 0, 17, 16, 40], 4, 7),
     "many": ([1 if i % 3 == 0 else 0 for i in range(150)], 0, 2),
+    "skewed": ([0] * 15 + [37] + [0] * 5, 1, 2),
     "wide": ([70, 0, 129, 33, 1, 256], 1, 30),
     "large": ([300, 257, 0, 511, 65], 0, 9),
 }
