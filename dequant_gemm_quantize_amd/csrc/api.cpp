@@ -573,11 +573,9 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   // float32 x goes to the few-row kernel, bf16 x by the rows that an expert has
   // on average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 78 us
   // against 77, 192 rows 108 against 77.  With groups that are no multiple of
-  // 128 its share of conversions is larger: groups of 64, 32 rows of the same
-  // 149 against 98, 64 rows of 16 experts [2048, 2048] 25.8 against 22.7; but
-  // 16 rows there 17.5 against 21.3, and 16 rows of 8 experts [4096, 11008] 83
-  // against 106.
-  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 3) * experts && w4::w4a16_grouped_gemm_fits(k))
+  // 128 its share of conversions is larger: groups of 64, 64 rows of the same 88
+  // against 98, 128 rows of 16 experts [2048, 2048] 25 against 23.5.
+  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);

@@ -20,7 +20,7 @@
 // their sums through LDS at the end.  Two rows of two experts [11008, 4096]:
 // 14.6 us (3.1 TB/s); 16 rows of 64 experts [2048, 2048] 11.6 us; float32 x
 // 17.6 and 16.9 us (multiply-adds of the vector unit, a weight row a lane, took
-// 129 and 83).
+// 129 and 83).  Groups of 32, 16 rows of 64 experts: 17.3 us.
 //
 // The codes are loaded as 256-byte runs of a row (128 without G128) and
 // regrouped through the wave's own place in LDS, row t's 16-byte piece c at slot
@@ -106,12 +106,9 @@ __device__ __forceinline__ float scale_value(uint32_t v) {
 
 }  // namespace
 
-// Most waves of a workgroup: 16 where the registers allow it.
-constexpr int gr_waves(size_t x_bytes, int sl) { return sl == 8 && x_bytes == 2 ? 16 : 8; }
-
 // SL: 32-column blocks of a wave's slice, 16 or 8.
 template <typename TX, typename TS, typename TY, bool G128, int SL, int RB>
-__global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX), SL) / 4) void k_w4a16_grouped_rows(
+__global__ __launch_bounds__(512, 2) void k_w4a16_grouped_rows(
     const TX* __restrict__ x, int64_t T, int64_t K, const int* __restrict__ offsets, int experts,
     const uint8_t* __restrict__ packed, const void* __restrict__ scales, const void* __restrict__ zeros, int64_t N,
     int g, TY* __restrict__ y, uint32_t tiles_n, int64_t tiles) {
@@ -299,10 +296,10 @@ __global__ __launch_bounds__(64 * gr_waves(sizeof(TX), SL), gr_waves(sizeof(TX),
   }
 }
 
-// At most `most` waves, each taking the same number of slices of sl blocks.
-static int grouped_rows_waves(int64_t k, int sl, int most) {
+// At most 8 waves, each taking the same number of slices of sl blocks.
+static int grouped_rows_waves(int64_t k, int sl) {
   const int64_t slices = (k / 32 + sl - 1) / sl;
-  const int64_t per = (slices + most - 1) / most;
+  const int64_t per = (slices + 7) / 8;
   return (int)((slices + per - 1) / per);
 }
 
@@ -310,7 +307,7 @@ template <typename TX, typename TS, typename TY, bool G128, int SL, int RB>
 static hipError_t gr_rb(const TX* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
                         const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
   const int64_t tiles_n = (n + 16 * RB - 1) / (16 * RB), tiles = grouped_max_tiles(t, experts, 16) * tiles_n;
-  const int nw = grouped_rows_waves(k, SL, gr_waves(sizeof(TX), SL));
+  const int nw = grouped_rows_waves(k, SL);
   const size_t sums = (size_t)nw * 1024 * RB, places = (size_t)nw * 256 * SL;
   const dim3 grid((unsigned)(tiles < kGRowsGrid ? tiles : kGRowsGrid));
   k_w4a16_grouped_rows<TX, TS, TY, G128, SL, RB><<<grid, 64 * nw, sums > places ? sums : places, st>>>(
@@ -318,23 +315,33 @@ static hipError_t gr_rb(const TX* x, int64_t t, int64_t k, const int* offsets, i
   return hipGetLastError();
 }
 
+template <typename TX, typename TS, typename TY, bool G128>
+static hipError_t gr_size(const TX* x, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
+                          const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
+  // The three parts of float32 x take the registers of twice the columns, and
+  // so do the scales and sums of groups that end at any block, which leave none
+  // for six blocks of rows, and with float32 x for one only (four: 8 rows of 8
+  // experts [11008, 4096] 155 us against 131).  (Groups of 64: one block a workgroup and 16 waves
+  // took 8 rows of 8 experts [11008, 4096] 100 us, one and 8 waves 61, up to
+  // four 56; groups of 32, 16 rows of 64 experts [2048, 2048] 22 and 17.)
+  constexpr int SL = G128 && sizeof(TX) == 2 ? 16 : 8, MAX = G128 ? 6 : sizeof(TX) == 2 ? 4 : 1;
+  if constexpr (MAX > 1) {
+    switch (rows_per_group<MAX>(grouped_max_tiles(t, experts, 16), (n + 15) / 16)) {
+      case 1: break;
+      case 2: return gr_rb<TX, TS, TY, G128, SL, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+      case 4: return gr_rb<TX, TS, TY, G128, SL, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+      default: return gr_rb<TX, TS, TY, G128, SL, MAX>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+    }
+  }
+  return gr_rb<TX, TS, TY, G128, SL, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+}
+
 template <typename TX, typename TS, typename TY>
 static hipError_t gr_pick(const void* xv, int64_t t, int64_t k, const int* offsets, int experts, const uint8_t* packed,
                           const void* scales, const void* zeros, int64_t n, int g, void* y, hipStream_t st) {
   const TX* x = (const TX*)xv;
-  // Groups that end at any block keep a scale for each: one block of rows a
-  // workgroup, of 256-column slices, is what fits the registers (16 rows of 64
-  // experts [2048, 2048], groups of 32: 22 us against 30 with two).
-  if (g % 128 != 0)
-    return gr_rb<TX, TS, TY, false, 8, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  // The three parts of float32 x take the registers of twice the columns.
-  constexpr int SL = sizeof(TX) == 2 ? 16 : 8;
-  switch (rows_per_group<6>(grouped_max_tiles(t, experts, 16), (n + 15) / 16)) {
-    case 1: return gr_rb<TX, TS, TY, true, SL, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    case 2: return gr_rb<TX, TS, TY, true, SL, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    case 4: return gr_rb<TX, TS, TY, true, SL, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-    default: return gr_rb<TX, TS, TY, true, SL, 6>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-  }
+  if (g % 128 == 0) return gr_size<TX, TS, TY, true>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+  return gr_size<TX, TS, TY, false>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
 }
 
 template <typename TX>

@@ -114,7 +114,7 @@ def test_w4a16_exact(w4, split, n, k, g, xd, sz, out):
 
 # few rows and many weight rows: workgroups of 1, 2, 4 and 6 blocks of 16 weight rows
 @pytest.mark.parametrize("n,k,g", [(4001, 512, 128), (8001, 640, 128), (11001, 1152, 384), (17003, 4480, 128),
-                                   (9001, 544, 32)])
+                                   (9001, 544, 32), (4001, 2240, 64), (8001, 416, 32), (11001, 960, 64)])
 @pytest.mark.parametrize("split", ["one", "few"])
 def test_exact_many_weight_rows(w4, split, n, k, g):
     test_mxfp4_exact(w4, split, n, k, "f32")
