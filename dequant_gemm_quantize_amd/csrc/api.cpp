@@ -571,11 +571,11 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
   W4_TRY(check_ptr(fn, "zeros", zeros));
   W4_TRY(check_ptr(fn, "y", y));
   // float32 x goes to the few-row kernel, bf16 x by the rows that an expert has
-  // on average: 128 rows of 8 experts [11008, 4096] take the few-row kernel 78 us
-  // against 77, 192 rows 108 against 77.  With groups that are no multiple of
-  // 128 its share of conversions is larger: groups of 64, 64 rows of the same 88
-  // against 98, 128 rows of 16 experts [2048, 2048] 25 against 23.5.
-  if (x_dtype == W4_BF16 && t > (group_size % 128 == 0 ? 16 : 8) * experts && w4::w4a16_grouped_gemm_fits(k))
+  // on average.  us of the few-row kernel against the other, groups of 128, 64
+  // and 32: 72 rows of 8 experts [11008, 4096] 56 / 61, 88 / 85, 90 / 121; 104 rows
+  // 69 / 60, 102 / 85, 103 / 118; 136 rows 82 / 63, 128 / 90, 127 / 127; 512 rows of 64
+  // experts [2048, 2048] 43 / 57, 74 / 65, 74 / 88; 1100 rows 59 / 59, 106 / 71, 106 / 104.
+  if (x_dtype == W4_BF16 && t > (group_size % 128 == 64 ? 8 : 16) * experts && w4::w4a16_grouped_gemm_fits(k))
     return hip_status(w4::launch_w4a16_grouped_gemm(x, t, k, offsets, (int)experts, packed, scales, zeros, sz_dtype,
                                                     n, group_size, y, y_dtype, stream),
                       fn);

@@ -44,7 +44,7 @@ constexpr uint32_t kPastEnd = 0x80000000u;  // beyond every resource: their size
 // the workgroups that one holds).  With SPLIT, tiles beyond the last whole round
 // of SLOTS are split into halves of half the rows when all the halves fit one
 // round, which then takes 0.6 of the time (2048 x 4096 x 11008 in MXFP4 63 us
-// without, 58 with; INT4 by expert 4096 rows 411 and 381).  `half` is -1 (a whole tile), 0 or 1.
+// without, 58 with).  `half` is -1 (a whole tile), 0 or 1.
 // False: nothing to do.  A launch has xcd_grid(tiles) workgroups.
 template <uint32_t SLOTS, bool SPLIT>
 __device__ __forceinline__ bool xcd_tile(uint32_t total, uint32_t& tile, int& half) {
@@ -75,9 +75,10 @@ inline double xcd_rounds(int64_t tiles, double part) {
 
 // Turns a wave's 32 x 32 blocks around in LDS and stores them to y.
 //
-// Register e of acc[i][j] holds y row r = lane % 32 of block row i, column
-// 8 (e / 4) + 4 (lane / 32) + e % 4 of block column j (the weights are the
-// MFMA's first operand), so four registers are four consecutive columns.  32
+// WFIRST: register e of acc[i][j] holds y row r = lane % 32 of block row i,
+// column 8 (e / 4) + 4 (lane / 32) + e % 4 of block column j (the weights are
+// the MFMA's first operand), so four registers are four consecutive columns.
+// Otherwise the other way round (x is the first operand).  32
 // rows at a time go to `turn` (turn_bytes of the wave's own) and leave it in
 // whole rows, 16 bytes a lane: stores of single elements made the MXFP4
 // product of 2048 x 11008 x 4096 take 84 us against 73.  Slot c ^ (row % SW)
@@ -88,7 +89,7 @@ constexpr int turn_bytes() {
   return 32 * 32 * NJ * (int)sizeof(TY);
 }
 
-template <typename TY, int MI, int NJ>
+template <typename TY, int MI, int NJ, bool WFIRST = true>
 __device__ __forceinline__ void turn_store(uint8_t* turn, int lane, const f32x16 (&acc)[MI][NJ], TY* y, int64_t N,
                                            int64_t mb, int64_t mend, int64_t nb) {
   constexpr int CB = 32 * NJ * (int)sizeof(TY);  // bytes of a row of the block
@@ -100,23 +101,37 @@ __device__ __forceinline__ void turn_store(uint8_t* turn, int lane, const f32x16
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     if (mb + 32 * i >= mend) break;  // the same in every lane
+    if constexpr (WFIRST) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
-                    v3 = acc[i][j][4 * q + 3];
-        const int col = 32 * j + 8 * q + 4 * h;
-        uint8_t* dst = turn + r * CB + 16 * ((col / PER) ^ (r & (SW - 1)));
-        if constexpr (sizeof(TY) == 4) {
-          *(f32x4*)dst = f32x4{v0, v1, v2, v3};
-        } else {
-          u32x2 b;
-          b.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v0, (__bf16)v1});
-          b.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v2, (__bf16)v3});
-          *(u32x2*)(dst + 8 * h) = b;
+        for (int q = 0; q < 4; ++q) {
+          const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2],
+                      v3 = acc[i][j][4 * q + 3];
+          const int col = 32 * j + 8 * q + 4 * h;
+          uint8_t* dst = turn + r * CB + 16 * ((col / PER) ^ (r & (SW - 1)));
+          if constexpr (sizeof(TY) == 4) {
+            *(f32x4*)dst = f32x4{v0, v1, v2, v3};
+          } else {
+            u32x2 b;
+            b.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v0, (__bf16)v1});
+            b.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v2, (__bf16)v3});
+            *(u32x2*)(dst + 8 * h) = b;
+          }
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int row = 8 * (e >> 2) + 4 * h + (e & 3);
+        uint8_t* dst = turn + row * CB + sizeof(TY) * (r % PER);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          uint8_t* at = dst + 16 * (((32 * j + r) / PER) ^ (row & (SW - 1)));
+          if constexpr (sizeof(TY) == 4) *(float*)at = acc[i][j][e];
+          else *(uint16_t*)at = (uint16_t)f32_to_bf16_bits(acc[i][j][e]);
         }
       }
+    }
     if (wide) {
 #pragma unroll
       for (int t = 0; t < 32 * CH / 64; ++t) {

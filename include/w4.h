@@ -378,12 +378,10 @@ int mxfp4_matmul(const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k, con
  *   as mxfp4_matmul.
  * w4a16_grouped_matmul -- packed [E, N, K/2], scales and zeros [E, N, K/g] in
  *   the INT4 format, x [T, K] W4_BF16 or W4_F32, y W4_BF16 or W4_F32.  Sums
- *   are float32.  With W4_BF16 x and many rows an expert each weight is
- *   rounded once to bf16, as in w4a16_matmul, for W4_BF16 y, and to the sum of
- *   two bf16 values (exact with W4_F16 scales and whole zero-points) for
- *   W4_F32 y; otherwise a code and its zero-point multiply x exactly and a
- *   group's sum takes its scale.  Deterministic.  A row of x that holds an
- *   infinity may give NaN.
+ *   are float32 and no weight is rounded: codes multiply x exactly, a group's
+ *   sum takes its scale, and the zero-point's part is taken off.  Deterministic.
+ *   A row of x that holds an infinity may give NaN, and so may one with finite
+ *   values whose |x|, summed over a group and times 31, leave float32's range.
  */
 int mxfp4_grouped_matmul(const uint8_t* xq, const uint8_t* xs, int64_t t, int64_t k, const int32_t* offsets,
                          int64_t experts, const uint8_t* packed, const uint8_t* scales, int64_t n, void* y,
