@@ -83,7 +83,9 @@ inline double xcd_rounds(int64_t tiles, double part) {
 // whole rows, 16 bytes a lane: stores of single elements made the MXFP4
 // product of 2048 x 11008 x 4096 take 84 us against 73.  Slot c ^ (row % SW)
 // of a row holds its 16-byte chunk c, which keeps the reads, and the stores
-// but for one conflict in four, apart in the banks.
+// but for one conflict in four, apart in the banks.  The LDS operations of a
+// wave complete in order; the wave barriers (no instruction) keep the compiler,
+// which looks at one lane alone, from changing that order.
 template <typename TY, int NJ>
 constexpr int turn_bytes() {
   return 32 * 32 * NJ * (int)sizeof(TY);
@@ -132,6 +134,7 @@ __device__ __forceinline__ void turn_store(uint8_t* turn, int lane, const f32x16
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();
     if (wide) {
 #pragma unroll
       for (int t = 0; t < 32 * CH / 64; ++t) {
@@ -148,6 +151,7 @@ __device__ __forceinline__ void turn_store(uint8_t* turn, int lane, const f32x16
         if (m < mend && n < N) y[m * N + n] = v;
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 

@@ -8,9 +8,9 @@
 // own with one column a unit, s zp times the unit's sum of x, each the sum of
 // three bf16 values (8 of the 9 products, the ninth below 2^-32): one MFMA for
 // two units.  The sums of x come from an MFMA against ones, 16 rows a wave.
-// (Weights rounded to bf16 before the product took 375 us where this takes
-// 440 - 460, and tripled the error against 64 bits that the rounding of bf16 y
-// leaves; as the sum of two bf16 values they took 650.)
+// (Weights rounded to bf16 before the product took 390 us where this takes
+// 455, and left an error against 64 bits of 2.3e-3 where the rounding of bf16 y
+// alone leaves 1.7e-3; as the sum of two bf16 values they took 650.)
 //
 // Workgroup tile 128 x 128 or 64 x 128 of four waves, each all the rows of 32
 // columns: a lane holds one weight row, so its scale and zero-point are one
