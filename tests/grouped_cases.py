@@ -75,3 +75,43 @@ def allowance_f32(x, s, g, off):
     mag = MX.grouped(np.abs(x).astype(np.float64), np.repeat(s, g, -1).astype(np.float64), off,
                      np.zeros((x.shape[0], s.shape[1])))[0]
     return 2.0 ** -24 * (31 + 31 + 3 * 30) * mag
+
+
+def wide_x(rng, t, e, n, k, g):
+    """float32 x of two columns, whole numbers of 17 bits whose bits 16, 8 and 0 are set: each bf16 part, of 8 bits from
+    its highest on, leaves something for the next.  The scale is 1/2, so every product and sum, with 16 + code too, is a
+    multiple of 1/2 below 2^22 (2 2^17 31 / 2): exact in float32 in any order."""
+    values = np.array([1 << 16 | a << 9 | 1 << 8 | b << 1 | 1 for a in range(0, 128, 9) for b in range(0, 128, 11)])
+    x = sparse(rng, t, k, 2, values.astype(np.float32))
+    code = rng.integers(0, 16, (e, n, k)).astype(np.uint8)
+    s = np.full((e, n, k // g), 0.5, np.float32)
+    z = rng.integers(0, 16, (e, n, k // g)).astype(np.float32)
+    return x, code, s, z
+
+
+def parts(x):
+    """float32 x as hi + mid + lo, each the upper half of what is left."""
+    out = []
+    left = np.ascontiguousarray(x, np.float32)
+    for _ in range(3):
+        p = (left.view(np.uint32) & 0xFFFF0000).astype(np.uint32).view(np.float32)
+        out.append(p)
+        left = left - p
+    assert not left.any()
+    return out
+
+
+def real_float_x(rng, t, e, n, k):
+    x = rng.normal(0, 1, (t, k)).astype(np.float32)
+    return x, rng.normal(0, 0.02, (e * n, k)).astype(np.float32)
+
+
+def allowance_real(x, s, g, off):
+    """How far a float32 result of normal data may be off, growing with the root of the additions.  A matrix instruction
+    adds 32 products at a time or more and a group's sum is added once, for codes and zero-points each: K / 32 + 2 K / g
+    roundings, independent and of half a step of a partial sum each.  Partial sums are of terms up to 31 |x| s of any
+    sign, root of the sum of their squares; 8 covers the largest of many outputs and the order inside an instruction."""
+    k = x.shape[1]
+    sq = MX.grouped(x.astype(np.float64) ** 2, (31 * np.repeat(s, g, -1).astype(np.float64)) ** 2, off,
+                    np.zeros((x.shape[0], s.shape[1])))[0]
+    return 8 * 2.0 ** -24 * np.sqrt(k / 32 + 2 * k / g) * np.sqrt(sq)

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import oracle.mxfp4_oracle as MX
+import oracle.w4_oracle as O
 import tests.grouped_cases as GC
 from tests.gpu_util import Canary, to_dev, y_as_f64
 
@@ -73,3 +74,33 @@ def test_rows_beside_others(w4, g):
     near = (many != alone).double().mean().item()
     # half a step of bf16 is 2^-9 |y|; the float32 sums differ by about 2^-20 of it, so ties split in far below 2% of cases
     assert near <= 0.02
+
+
+@pytest.mark.parametrize("sz", ["f16", "f32"])
+@pytest.mark.parametrize("n,k,g", GC.SHAPES + [(100, 672, 96), (9001, 256, 128)])
+@pytest.mark.parametrize("split", sorted(GC.SPLITS))
+def test_wide_float32_x_exact(w4, split, n, k, g, sz):
+    """float32 x whose middle and lower bf16 parts count."""
+    off, t = GC.offsets_of(split)
+    x, code, s, z = GC.wide_x(np.random.default_rng(n + k + g + t), t, len(off) - 1, n, k, g)
+    y = product(w4, x, code, s, z, g, off, "f32", xd="f32", sz=sz)
+    want = torch.from_numpy(GC.exact(x, GC.weights(code, s, z, g), off, t, n, -7.0)).to(torch.float32)
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("xd", ["f32", "bf16"])
+@pytest.mark.parametrize("split,n,k,g", [("few", 500, 4096, 128), ("some", 260, 2048, 64), ("many", 200, 1120, 32),
+                                         ("many", 300, 2048, 128), ("most", 130, 1024, 32), ("most", 200, 1280, 256)])
+def test_real_data_to_float32(w4, split, n, k, g, xd):
+    """Normal data, float32 y, against 64 bits with a bound that grows with the root of K."""
+    off, t = GC.offsets_of(split)
+    e, ng = len(off) - 1, k // g
+    x, wf = GC.real_float_x(np.random.default_rng(n + k), t, e, n, k)
+    x = GC.bf16(x) if xd == "bf16" else x
+    xt = to_dev(x, "f32").to(torch.bfloat16 if xd == "bf16" else torch.float32)
+    p, s, z = w4.quantize_pack_int4(to_dev(wf, "f32"), g)
+    y = w4.w4a16_grouped_matmul(xt, torch.from_numpy(off).cuda(), p.view(e, n, k // 2), s.view(e, n, ng), z.view(e, n, ng), g,
+                                out=torch.zeros((t, n), dtype=torch.float32, device="cuda"))
+    sh = s.float().cpu().numpy().reshape(e, n, ng)
+    w = O.dequant_f64(p.cpu().numpy(), s.cpu().numpy(), z.cpu().numpy(), g).reshape(e, n, k)
+    assert (np.abs(y_as_f64(y) - GC.exact(x, w, off, t, n)) <= GC.allowance_real(x, sh, g, off)).all()

@@ -63,3 +63,44 @@ def test_float_scales_pass_in_float32(n, k, g):
 def test_bf16_rounds_to_the_nearest():
     a = np.array([1.0, 1.0 + 2.0 ** -8, 1.0 + 3 * 2.0 ** -8, 1.0 + 2.0 ** -9, -1.0 - 2.0 ** -8 - 2.0 ** -20], np.float32)
     assert GC.bf16(a).tolist() == [1.0, 1.0, 1.0 + 2.0 ** -6, 1.0, -1.0 - 2.0 ** -7]
+
+
+@pytest.mark.parametrize("n,k,g", GC.SHAPES)
+def test_wide_x_tells_a_missing_part(n, k, g):
+    off, t, x, s, w = case(GC.wide_x, "some", n, k, g)
+    hi, mid, lo = GC.parts(x)
+    used = x != 0
+    assert lo[used].all() and mid[used].all()
+    want = GC.exact(x, w, off, t, n)
+    assert np.abs(want).max() < 2.0 ** 23 and np.array_equal(2 * want, np.rint(2 * want))
+    own = (GC.exact(np.ones_like(x), np.ones_like(w), off, t, n) > 0) & (want != 0)
+    for model in (hi, hi + mid, hi + lo, GC.bf16(x)):
+        assert (GC.exact(model, w, off, t, n) != want)[own].mean() > 0.9
+
+
+@pytest.mark.parametrize("k,g", [(4096, 128), (2048, 64), (1120, 32), (1280, 256)])
+def test_real_bound_tells_bf16_x(k, g):
+    """On normal data the bound that grows with the root of K passes float32 arithmetic and refuses x or weights of bf16,
+    and zeros."""
+    off, t, n = np.array([0, 16], np.int32), 16, 60
+    rng = np.random.default_rng(k)
+    x, wf = GC.real_float_x(rng, t, 1, n, k)
+    b = wf.reshape(n, -1, g)
+    s = ((b.max(-1) - b.min(-1)) / 15).astype(np.float16).astype(np.float32)
+    z = np.clip(np.rint(-b.min(-1) / s), 0, 15).astype(np.float32)
+    code = np.clip(np.rint(b / s[..., None] + z[..., None]), 0, 15).astype(np.uint8).reshape(1, n, k)
+    w = GC.weights(code, s[None], z[None], g)
+    want, allowed = GC.exact(x, w, off, t, n), GC.allowance_real(x, s[None], g, off)
+    for model_x, model_w in ((GC.bf16(x), w), (GC.parts(x)[0], w), (x, rounded(w)), (0 * x, w)):
+        assert (np.abs(GC.exact(model_x, model_w, off, t, n) - want) > allowed).mean() > 0.8
+    xb, cb = x.reshape(t, -1, g), code.reshape(n, -1, g).astype(np.float32)
+    for bias in (np.float32(0), np.float32(16)):  # group by group in float32
+        y = np.zeros((t, n), np.float32)
+        for j in range(k // g):
+            d = np.zeros((t, n), np.float32)
+            xs = np.zeros(t, np.float32)
+            for i in range(0, g, 32):
+                d += (xb[:, j, i:i + 32].astype(np.float64) @ (bias + cb[:, j, i:i + 32]).T.astype(np.float64)).astype(np.float32)
+                xs += xb[:, j, i:i + 32].astype(np.float64).sum(1).astype(np.float32)
+            y += s[:, j] * d - s[:, j] * (bias + z[:, j]) * xs[:, None]
+        assert (np.abs(y - want) <= allowed).all()
