@@ -107,7 +107,7 @@ def _gpu(*ts: torch.Tensor) -> torch.device:
     return dev
 
 
-def _stream(dev: torch.device) -> int:
+def _stream(dev) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -415,8 +415,9 @@ def w4a8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, s
 # A product of one token takes less time than these wrappers can: what follows
 # asks each tensor as little as the checks need, looks for the words of an error
 # only when there is one, and takes the current stream's handle (an int) without
-# the Stream object around it (0.06 us against 1.06).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the Stream object around it (0.06 us against 1.06) where torch has that query,
+# a private name.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
 
 
 def _device(*ts: torch.Tensor) -> int:
