@@ -127,8 +127,18 @@ def _float_weight(w: torch.Tensor) -> torch.Tensor:
     return (w if w.dtype in (torch.bfloat16, torch.float32) else w.to(torch.float32)).contiguous()
 
 
-def _mx_activations(x2: torch.Tensor):
-    return _lib.quantize_mxfp4(x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.to(torch.float32))
+def _activations(x2: torch.Tensor) -> torch.Tensor:
+    """Activations as the kernels take them: fp16 ones in float32, which holds them."""
+    return x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.to(torch.float32)
+
+
+def _result_dtype(x: torch.Tensor, out_dtype: Optional[torch.dtype]) -> torch.dtype:
+    return out_dtype or (x.dtype if x.is_floating_point() else torch.float32)
+
+
+def _product_dtype(dt: torch.dtype) -> torch.dtype:
+    """The type of y to ask a product for where the layer's result is of type dt (the products give fp32 and bf16)."""
+    return torch.bfloat16 if dt == torch.bfloat16 else torch.float32
 
 
 class MXFP4Linear(torch.nn.Module):
@@ -137,8 +147,8 @@ class MXFP4Linear(torch.nn.Module):
     scales [N, K/32], x quantized in forward, the product on the matrix
     cores' 4-bit inputs.
 
-    forward(x): x [..., in_features] on the weight's GPU; returns
-    [..., out_features] in ``out_dtype`` (default bf16)."""
+    forward(x): x [..., in_features] in bf16, fp32 or fp16 on the weight's
+    GPU; returns [..., out_features] in ``out_dtype`` (default: x's dtype)."""
 
     def __init__(self, in_features: int, out_features: int, out_dtype: Optional[torch.dtype] = None, device=None):
         super().__init__()
@@ -167,8 +177,9 @@ class MXFP4Linear(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.shape[-1] != self.in_features:
             raise ValueError(f"x has {x.shape[-1]} features, the layer takes {self.in_features}")
-        xq, xs = _mx_activations(x.reshape(-1, self.in_features).contiguous())
-        y = _lib.mxfp4_matmul(xq, xs, self.packed, self.scales, out_dtype=self.out_dtype or torch.bfloat16)
+        xq, xs = _lib.quantize_mxfp4(_activations(x.reshape(-1, self.in_features).contiguous()))
+        dt = _result_dtype(x, self.out_dtype)
+        y = _lib.mxfp4_matmul(xq, xs, self.packed, self.scales, out_dtype=_product_dtype(dt)).to(dt)
         return y.reshape(*x.shape[:-1], self.out_features)
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
@@ -184,10 +195,11 @@ class QuantizedExperts(torch.nn.Module):
     mixture of experts, in the INT4 format (``fmt="int4"``: W4A16 product) or
     in MXFP4 (``fmt="mxfp4"``: activations quantized in forward).
 
-    forward(x, offsets): x [T, in_features] with its rows sorted by expert;
-    offsets int32 [experts + 1] on the GPU, expert e owning rows offsets[e] ..
-    offsets[e+1]-1.  Rows that no expert owns are not written (pass ``out`` to
-    choose what they hold)."""
+    forward(x, offsets): x [T, in_features] in bf16, fp32 or fp16 with its rows
+    sorted by expert; offsets int32 [experts + 1] on the GPU, expert e owning
+    rows offsets[e] .. offsets[e+1]-1; returns [T, out_features] in
+    ``out_dtype`` (default: x's dtype), or ``out`` (fp32 or bf16).  Rows that no
+    expert owns are not written (pass ``out`` to choose what they hold)."""
 
     def __init__(self, experts: int, in_features: int, out_features: int, fmt: str = "int4", group_size: int = 128,
                  scale_dtype: torch.dtype = torch.float16, out_dtype: Optional[torch.dtype] = None, device=None):
@@ -230,13 +242,16 @@ class QuantizedExperts(torch.nn.Module):
         return layer
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        x = x.contiguous()
+        dt = _result_dtype(x, self.out_dtype)
+        ask = _product_dtype(dt)
+        x = _activations(x.contiguous())
         if self.fmt == "mxfp4":
-            xq, xs = _mx_activations(x)
-            return _lib.mxfp4_grouped_matmul(xq, xs, offsets, self.packed, self.scales,
-                                             out_dtype=self.out_dtype or torch.bfloat16, out=out)
-        return _lib.w4a16_grouped_matmul(x, offsets, self.packed, self.scales, self.zeros, self.group_size,
-                                         out_dtype=self.out_dtype, out=out)
+            xq, xs = _lib.quantize_mxfp4(x)
+            y = _lib.mxfp4_grouped_matmul(xq, xs, offsets, self.packed, self.scales, out_dtype=ask, out=out)
+        else:
+            y = _lib.w4a16_grouped_matmul(x, offsets, self.packed, self.scales, self.zeros, self.group_size,
+                                          out_dtype=ask, out=out)
+        return y if out is not None else y.to(dt)
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The dense weights [experts, out, in], for inspection."""
