@@ -330,7 +330,8 @@ static hipError_t gr_size(const TX* x, int64_t t, int64_t k, const int* offsets,
       case 1: break;
       case 2: return gr_rb<TX, TS, TY, G128, SL, 2>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
       case 4: return gr_rb<TX, TS, TY, G128, SL, 4>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
-      default: return gr_rb<TX, TS, TY, G128, SL, MAX>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
+      default:
+        if constexpr (MAX == 6) return gr_rb<TX, TS, TY, G128, SL, 6>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
     }
   }
   return gr_rb<TX, TS, TY, G128, SL, 1>(x, t, k, offsets, experts, packed, scales, zeros, n, g, y, st);
