@@ -509,7 +509,10 @@ int dequant_mxfp4(const uint8_t* packed, const uint8_t* scales, int64_t n, int64
 // 9.4 against 10.9 us at 16 rows, equal at 32); up to 128 rows the many-row
 // kernel's time goes with K alone while its tiles leave CUs idle, the few-row
 // kernel's with N * K, and N = 4608 is about where they meet (64 rows of
-// [11008, 4096]: 20 against 10.5 us, of [4096, 11008]: 19 against 24).
+// [11008, 4096]: 20 against 10.5 us, of [4096, 11008]: 19 against 20.5, of [8192,
+// 2048] 9.5 against 6.5, of [4608, 8192] 17.6 against 16.4).  Of 11 shapes of K
+// 2048 .. 13824 at 24 to 200 rows the choice costs most at 40 rows of [5120, 13824]
+// (35 us where the few-row kernel takes 21) and 128 of [4608, 8192] (32 against 20).
 static int mx_product(const char* fn, const uint8_t* xq, const uint8_t* xs, int64_t m, int64_t k,
                       const int32_t* offsets, int64_t experts, const uint8_t* packed, const uint8_t* scales,
                       int64_t n, void* y, int y_dtype, hipStream_t stream) {

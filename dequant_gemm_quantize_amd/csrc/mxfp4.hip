@@ -12,7 +12,8 @@
 //
 // Both kernels stream: nothing is read twice, and each lane's 8 elements are
 // one or two 16-byte accesses.  Bound by the bytes: bf16 [28672, 8192] there and
-// back takes 201 us, 5.3 TB/s (a copy of 1 GiB reaches 5.1).
+// back takes 201 us, 5.9 TB/s with the codes and scales written and read again,
+// some of them from cache (a copy of 1 GiB reaches 5.1 - 5.2).
 #include "w4_common.h"
 #include "w4_internal.h"
 

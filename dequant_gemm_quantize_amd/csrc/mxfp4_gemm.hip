@@ -13,10 +13,10 @@
 // 9 on zeros).  And the tiles come from L2, 64 KB a K step and CU, which takes
 // about a step's time and has to be asked for one and a half steps ahead.  y
 // is a third of the bytes at K = 4096.
-// Measured: 512 x 28672 x 8192 65 us of kernel time (3.7 PFLOP/s), 2048 x
-// 11008 x 4096 55 us (3.4), 4096 x 8192 x 8192 130 us (4.2); 4096 rows by
-// expert, 8 of [11008, 4096], 132 us (2.8: the experts' last tiles).  Matrix
-// cores are busy a third of that time.
+// Measured, kernel time: 512 x 28672 x 8192 64 us (3.7 PFLOP/s), 2048 x 11008 x
+// 4096 57 us (3.2); 4096 rows by expert, 8 of [11008, 4096], 130 us (2.8: the
+// experts' last tiles); 4096 x 8192 x 8192 136 us a call in a replayed graph (4.1).
+// Matrix cores are busy a third of that time.
 #include <type_traits>
 
 #include "grouped.h"

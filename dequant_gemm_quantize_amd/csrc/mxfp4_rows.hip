@@ -12,9 +12,11 @@
 // was slower: the launch then has so many waves that starting them (about 13
 // cycles a wave on each XCD) takes longer than reading the weights.
 //
-// Measured: one row times [11008, 4096] 7.4 us (3.2 TB/s), [28672, 8192] 26.2 us
-// (4.8 TB/s), [8192, 28672] 23.3 us (5.4 TB/s), 16 rows of 64 experts [2048,
-// 2048] 8.8 us of which the bytes of the experts with rows take 6.2.  More token
+// Measured (a call's share of a replayed graph of calls, weights rotated; the
+// kernel alone takes 1 - 2 us less): one row times [11008, 4096] 7.4 - 8.0 us (3.1
+// TB/s), [28672, 8192] 26.2 us (4.8 TB/s), [8192, 28672] 23.3 us (5.4 TB/s), 16 rows
+// of 64 experts [2048, 2048] 8.9 us of which the bytes of the experts with rows
+// take 6.2.  More token
 // rows cost time of their own, since every workgroup reads x of its slices
 // (64 rows times [4096, 11008] 19 us against 6.6 for one).  16 waves in place of 8
 // where a workgroup has one block: 7.2 us against 6.6 for [4096, 11008].

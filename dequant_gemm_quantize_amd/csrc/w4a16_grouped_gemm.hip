@@ -8,8 +8,8 @@
 // own with one column a unit, s zp times the unit's sum of x, each the sum of
 // three bf16 values (8 of the 9 products, the ninth below 2^-32): one MFMA for
 // two units.  The sums of x come from an MFMA against ones, 16 rows a wave.
-// (Weights rounded to bf16 before the product took 390 us where this takes
-// 455, and left an error against 64 bits of 2.3e-3 where the rounding of bf16 y
+// (Weights rounded to bf16 before the product took 390 us where this takes 440
+// to 465, and left an error against 64 bits of 2.3e-3 where the rounding of bf16 y
 // alone leaves 1.7e-3; as the sum of two bf16 values they took 650.)
 //
 // Workgroup tile 128 x 128 or 64 x 128 of four waves, each all the rows of 32
@@ -21,11 +21,12 @@
 // (again 128-byte lines), and from there to registers, where a wave turns its
 // own 32 rows into operands.
 //
-// Bound by the vector instructions (5 an MFMA with units of 128 columns, 8 and
-// 12 with units of 64 and 32) and the matrix cores, each busy about half of
-// the time.  Experts [11008, 4096], 8 of them, bf16 y, fp16 scales: 4096 rows
-// 455 us (0.81 PFLOP/s; a large bf16 product of the library reaches 1.53), with
-// groups of 64 537, of 32 695; 1200 rows 175 / 214 / 297, 256 rows 70 / 88 / 125.
+// Bound by the matrix cores and the vector instructions (6 an MFMA with units
+// of 128 columns, more with shorter ones), which are busy half of the time each
+// and wait for each other.  Experts [11008, 4096], 8 of them, bf16 y, fp16 scales:
+// 4096 rows 440 - 465 us (0.8 PFLOP/s; a large bf16 product of the library reaches
+// 1.53), with groups of 64 540, of 32 715; 1200 rows 176 / 219 / 306, 256 rows 71 /
+// 97 / 136.
 #include <type_traits>
 
 #include "grouped.h"

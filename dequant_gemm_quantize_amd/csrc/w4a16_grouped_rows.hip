@@ -17,10 +17,11 @@
 // columns with G128 (or take such slices in turn): a wave keeps x of its slice,
 // and its sums, in registers for all the blocks, and the codes and scales of
 // the next block are in flight while one is computed.  The waves add
-// their sums through LDS at the end.  Two rows of two experts [11008, 4096]:
-// 14.6 us (3.1 TB/s); 16 rows of 64 experts [2048, 2048] 11.6 us; float32 x
-// 17.6 and 16.9 us (multiply-adds of the vector unit, a weight row a lane, took
-// 129 and 83).  Groups of 32, 16 rows of 64 experts: 17.3 us.
+// their sums through LDS at the end.  A call's share of a replayed graph of
+// calls, weights rotated: two rows of two experts [11008, 4096] 14.6 us (3.1 TB/s; the
+// kernel alone 13.6), 16 rows of 64 experts [2048, 2048] 11.1 us; float32 x 17.8
+// and 15.7 us (multiply-adds of the vector unit, a weight row a lane, took 129
+// and 83).  Groups of 32, 16 rows of 64 experts: 17.4 us.
 //
 // The codes are loaded as 256-byte runs of a row (128 without G128) and
 // regrouped through the wave's own place in LDS, row t's 16-byte piece c at slot

@@ -8,6 +8,7 @@ Every numeric step runs in the HIP kernels behind libw4.so: quantization at
 construction (asymmetric, symmetric, symmetric with a percentile or MSE
 calibrated scale, or GPTQ with calibration activations), the product in forward (W4A16, or W4A8 with per-token
 INT8 activations).  This module only reshapes tensors and keeps the buffers.
+The layers are for inference: no gradient flows through their results.
 """
 from __future__ import annotations
 
