@@ -48,6 +48,17 @@ SIGNATURES = [
     ("mxfp4_matmul", _I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _I, _VP]),
     ("mxfp4_grouped_matmul", _I, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I, _VP]),
     ("w4a16_grouped_matmul", _I, [_VP, _I, _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP]),
+    ("quantize_checkpoint_int8", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP]),
+    ("dequant_checkpoint_int8", _I, [_VP, _VP, _I64, _I64, _VP, _I, _VP]),
+    ("w4a16_lora_matmul", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP, _VP,
+                               _VP, _I64, _VP, _VP, _I, _VP]),
+    ("w4a16_matmul_t_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I32, _I, _I, _I]),
+    ("w4a16_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP, ctypes.c_size_t, _VP]),
+    ("w4a16_lora_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP,
+                                 _VP, _VP, _I64, _VP, _VP, _I, _VP, ctypes.c_size_t, _VP]),
+    ("lora_grads_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I32]),
+    ("lora_grads", _I, [_VP, _VP, _I64, _I64, _VP, _I, _I64, _VP, _VP, _VP, _VP, _I64, _I64, _I32, _VP, _VP, _VP,
+                        ctypes.c_size_t, _VP]),
     ("w4_status_string", ctypes.c_char_p, [_I]),
     ("w4_last_error", ctypes.c_char_p, []),
     ("w4_version", ctypes.c_char_p, []),
@@ -567,6 +578,216 @@ def w4a16_grouped_matmul(x: torch.Tensor, offsets: torch.Tensor, packed: torch.T
     _launch(dev, load().w4a16_grouped_matmul, _ptr(x), _dtype_code(x.dtype), t, k, _ptr(offsets), e, _ptr(packed),
             _ptr(scales), _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(y), _dtype_code(y.dtype))
     return y
+
+
+# ---------------------------------------------------------------------------
+# Activation checkpoints in 8 bits, the transposed product, low-rank adapters
+# ---------------------------------------------------------------------------
+CHECKPOINT_BLOCK = 128  # columns of a block of the 8-bit checkpoint
+
+
+def _checkpoint_blocks(k: int) -> int:
+    if k <= 0 or k % 32:
+        raise ValueError(f"K = {k} is not a positive multiple of 32")
+    return -(-k // CHECKPOINT_BLOCK)
+
+
+def quantize_checkpoint_int8(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """x [M, K] (fp32 or bf16) -> (xq int8 [M, K], xs float32 [M, ceil(K/128)]), a scale for each 128 columns of a row."""
+    m, k = _matrix(x, "x")
+    if x.dtype not in Y_DTYPES:
+        raise ValueError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
+    nb = _checkpoint_blocks(k)
+    if out is not None:
+        xq, xs = out
+        _expect(xq, "xq", (m, k), (torch.int8,))
+        _expect(xs, "xs", (m, nb), (torch.float32,))
+        dev = _device(x, xq, xs)
+    else:
+        dev = _device(x)
+        xq, xs = x.new_empty((m, k), dtype=torch.int8), x.new_empty((m, nb), dtype=torch.float32)
+    _launch(dev, load().quantize_checkpoint_int8, _ptr(x), _dtype_code(x.dtype), m, k, _ptr(xq), _ptr(xs))
+    return xq, xs
+
+
+def _check_checkpoint(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
+    m, k = _matrix(xq, "xq")
+    _expect(xq, "xq", (m, k), (torch.int8,))
+    _expect(xs, "xs", (m, _checkpoint_blocks(k)), (torch.float32,))
+    return m, k
+
+
+def dequant_checkpoint_int8(xq: torch.Tensor, xs: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                            out: Optional[torch.Tensor] = None):
+    """(xq, xs) -> the values [M, K] in out_dtype (fp32, fp16 or bf16)."""
+    m, k = _check_checkpoint(xq, xs)
+    if out is not None:
+        _expect(out, "out", (m, k), tuple(_DT))
+        dev = _device(xq, xs, out)
+    else:
+        _dtype_code(out_dtype)
+        dev = _device(xq, xs)
+        out = xq.new_empty((m, k), dtype=out_dtype)
+    _launch(dev, load().dequant_checkpoint_int8, _ptr(xq), _ptr(xs), m, k, _ptr(out), _dtype_code(out.dtype))
+    return out
+
+
+def _check_segments(offsets: torch.Tensor, adapters: torch.Tensor) -> int:
+    """offsets int32 [S + 1] and adapters int32 [S]; returns S."""
+    if adapters.dim() != 1:
+        raise ValueError(f"adapters must be a 1-D tensor, got {adapters.dim()} dimensions")
+    s = adapters.shape[0]
+    if adapters.dtype is not torch.int32 or offsets.dtype is not torch.int32 or offsets.shape != (s + 1,):
+        _expect(adapters, "adapters", (s,), (torch.int32,))
+        _expect(offsets, "offsets", (s + 1,), (torch.int32,))
+    return s
+
+
+def _check_lora(a, b, scaling, offsets, adapters, k: int, n: int) -> Tuple[int, int, int]:
+    """a [L, R, K] and b [L, N, R] of one dtype, scaling float32 [L], and the segments; returns (L, R, S)."""
+    if a.dim() != 3:
+        raise ValueError(f"a must be a 3-D tensor, got {a.dim()} dimensions")
+    count, rank = a.shape[0], a.shape[1]
+    if a.shape != (count, rank, k) or a.dtype not in Y_DTYPES:
+        _expect(a, "a", (count, rank, k), Y_DTYPES)
+    if b.shape != (count, n, rank) or b.dtype is not a.dtype:
+        _expect(b, "b", (count, n, rank), (a.dtype,))
+    if scaling.shape != (count,) or scaling.dtype is not torch.float32:
+        _expect(scaling, "scaling", (count,), (torch.float32,))
+    return count, rank, _check_segments(offsets, adapters)
+
+
+def _int4_product(x, name: str, packed, scales, zeros, group_size: int, transposed: bool) -> Tuple[int, int, int]:
+    """x [M, K] (or dy [M, N]) against an INT4 weight; returns (M, K, N)."""
+    m, d = _matrix(x, name)
+    if x.dtype not in Y_DTYPES:
+        raise ValueError(f"{name} has dtype {x.dtype}, expected float32 or bfloat16")
+    k = 2 * _matrix(packed, "packed")[1]
+    n = _check_weights(packed, scales, zeros, k, group_size)
+    if d != (n if transposed else k):
+        raise ValueError(f"{name} has {d} columns, the weight [N, K] is [{n}, {k}]")
+    return m, k, n
+
+
+def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                      group_size: int, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor,
+                      offsets: torch.Tensor, adapters: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
+                      out: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None):
+    """y [M, N] = x . dequant(W)^T + u . B^T with u = scaling x . A^T of each row's adapter.
+
+    a [L, R, K] and b [L, N, R] (both bf16 or both fp32, R a multiple of 8 up
+    to 256), scaling float32 [L]; offsets int32 [S + 1], rising, and adapters
+    int32 [S] on the GPU (never read on the host): rows offsets[s] ..
+    offsets[s+1]-1 have adapter adapters[s], none if that is no number of 0 .. L-1.
+    u: a float32 [M, R] tensor that takes u (rows of no adapter are left as they
+    were).  out_dtype defaults to x's dtype."""
+    m, k, n = _int4_product(x, "x", packed, scales, zeros, group_size, False)
+    count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
+    given = tuple(t for t in (out, u) if t is not None)
+    dev = _device(x, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
+    y = _y_out(out, out_dtype or x.dtype, (m, n), x)
+    if u is None:
+        u = x.new_empty((m, rank), dtype=torch.float32)
+    elif u.shape != (m, rank) or u.dtype is not torch.float32:
+        _expect(u, "u", (m, rank), (torch.float32,))
+    _launch(dev, load().w4a16_lora_matmul, _ptr(x), _dtype_code(x.dtype), m, k, _ptr(packed), _ptr(scales),
+            _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
+            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(u), _ptr(y), _dtype_code(y.dtype))
+    return y
+
+
+def w4a16_matmul_t_workspace_size(m: int, k: int, n: int, group_size: int, dy_dtype: torch.dtype = torch.bfloat16,
+                                  sz_dtype: torch.dtype = torch.float16,
+                                  dx_dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that w4a16_matmul_t and w4a16_lora_matmul_t need for this shape."""
+    return int(load().w4a16_matmul_t_workspace_size(m, k, n, group_size, _dtype_code(dy_dtype), _dtype_code(sz_dtype),
+                                                    _dtype_code(dx_dtype)))
+
+
+def _t_workspace(dy, m, k, n, group_size, scales, dx) -> Optional[torch.Tensor]:
+    nbytes = load().w4a16_matmul_t_workspace_size(m, k, n, group_size, _dtype_code(dy.dtype),
+                                                  _dtype_code(scales.dtype), _dtype_code(dx.dtype))
+    return dy.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+
+
+def w4a16_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int,
+                   out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None):
+    """dx [M, K] = dy [M, N] . dequant(W): the gradient of w4a16_matmul with respect to x.
+
+    dy bf16 or fp32; out_dtype defaults to dy's dtype.  The workspace comes from torch."""
+    m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
+    dev = _device(dy, packed, scales, zeros) if out is None else _device(dy, packed, scales, zeros, out)
+    dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
+    ws = _t_workspace(dy, m, k, n, group_size, scales, dx)
+    _launch(dev, load().w4a16_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales), _ptr(zeros),
+            _dtype_code(scales.dtype), n, group_size, _ptr(dx), _dtype_code(dx.dtype),
+            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    return dx
+
+
+def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                        group_size: int, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor,
+                        offsets: torch.Tensor, adapters: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
+                        out: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+    """dx [M, K] = dy . dequant(W) + v . A with v = scaling dy . B of each row's
+    adapter: the gradient of w4a16_lora_matmul with respect to x.
+
+    Arguments as there; v: a float32 [M, R] tensor that takes v (rows of no
+    adapter are left as they were).  out_dtype defaults to dy's dtype."""
+    m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
+    count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
+    given = tuple(t for t in (out, v) if t is not None)
+    dev = _device(dy, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
+    dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
+    if v is None:
+        v = dy.new_empty((m, rank), dtype=torch.float32)
+    elif v.shape != (m, rank) or v.dtype is not torch.float32:
+        _expect(v, "v", (m, rank), (torch.float32,))
+    ws = _t_workspace(dy, m, k, n, group_size, scales, dx)
+    _launch(dev, load().w4a16_lora_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales),
+            _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
+            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(v), _ptr(dx), _dtype_code(dx.dtype),
+            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    return dx
+
+
+def lora_grads_workspace_size(m: int, k: int, n: int, adapters: int, rank: int) -> int:
+    """Bytes of workspace that lora_grads needs for this shape (0: none)."""
+    return int(load().lora_grads_workspace_size(m, k, n, adapters, rank))
+
+
+def lora_grads(xq: torch.Tensor, xs: torch.Tensor, dy: torch.Tensor, u: torch.Tensor, v: torch.Tensor,
+               offsets: torch.Tensor, adapters: torch.Tensor, num_adapters: int,
+               out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """(da [L, R, K], db [L, N, R]), float32: the gradients of num_adapters = L adapters.
+
+    xq, xs: x's checkpoint from quantize_checkpoint_int8; dy [M, N] bf16 or
+    fp32; u and v from w4a16_lora_matmul and w4a16_lora_matmul_t.  An adapter
+    without rows gets zeros; rows of no adapter are not read."""
+    m, k = _check_checkpoint(xq, xs)
+    n = _matrix(dy, "dy")[1]
+    _expect(dy, "dy", (m, n), Y_DTYPES)
+    rank = _matrix(u, "u")[1]
+    _expect(u, "u", (m, rank), (torch.float32,))
+    _expect(v, "v", (m, rank), (torch.float32,))
+    s = _check_segments(offsets, adapters)
+    if num_adapters < 0:
+        raise ValueError(f"num_adapters = {num_adapters} < 0")
+    shapes = (num_adapters, rank, k), (num_adapters, n, rank)
+    if out is not None:
+        da, db = out
+        _expect(da, "da", shapes[0], (torch.float32,))
+        _expect(db, "db", shapes[1], (torch.float32,))
+        dev = _device(xq, xs, dy, u, v, offsets, adapters, da, db)
+    else:
+        dev = _device(xq, xs, dy, u, v, offsets, adapters)
+        da, db = u.new_empty(shapes[0]), u.new_empty(shapes[1])
+    nbytes = load().lora_grads_workspace_size(m, k, n, num_adapters, rank)
+    ws = u.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+    _launch(dev, load().lora_grads, _ptr(xq), _ptr(xs), m, k, _ptr(dy), _dtype_code(dy.dtype), n, _ptr(u), _ptr(v),
+            _ptr(offsets), _ptr(adapters), s, num_adapters, rank, _ptr(da), _ptr(db),
+            None if ws is None else _ptr(ws), nbytes)
+    return da, db
 
 
 def version() -> str:

@@ -587,4 +587,228 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
                     fn);
 }
 
+// ---------------------------------------------------------------------------
+// Activation checkpoints in 8 bits, the transposed product, low-rank adapters
+// ---------------------------------------------------------------------------
+static int check_checkpoint(const char* fn, int64_t m, int64_t k) {
+  if (m < 0 || m > w4::kLoraMaxRows)
+    return fail(W4_EINVAL, "%s: m = %lld must lie in 0 .. %lld", fn, (long long)m, (long long)w4::kLoraMaxRows);
+  if (k <= 0 || k % 32 != 0 || k > kMaxK)
+    return fail(W4_EINVAL, "%s: k = %lld must be a positive multiple of 32, at most %lld", fn, (long long)k,
+                (long long)kMaxK);
+  if (m > kMaxElems / k) return fail(W4_EINVAL, "%s: m * k is too large", fn);
+  return W4_OK;
+}
+
+int quantize_checkpoint_int8(const void* x, int x_dtype, int64_t m, int64_t k, int8_t* xq, float* xs,
+                             hipStream_t stream) {
+  static const char* fn = "quantize_checkpoint_int8";
+  W4_TRY(check_checkpoint(fn, m, k));
+  if (x_dtype != W4_F32 && x_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: x dtype %d must be W4_F32 or W4_BF16", fn, x_dtype);
+  if (m == 0) return ok();
+  W4_TRY(check_ptr(fn, "x", x));
+  W4_TRY(check_ptr(fn, "xq", xq));
+  W4_TRY(check_ptr4(fn, "xs", xs));
+  return hip_status(w4::launch_quantize_checkpoint(x, x_dtype, m, k, xq, xs, stream), fn);
+}
+
+int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_t k, void* out, int out_dtype,
+                            hipStream_t stream) {
+  static const char* fn = "dequant_checkpoint_int8";
+  W4_TRY(check_checkpoint(fn, m, k));
+  if (out_dtype != W4_F32 && out_dtype != W4_F16 && out_dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: out dtype %d must be W4_F32, W4_F16 or W4_BF16", fn, out_dtype);
+  if (m == 0) return ok();
+  W4_TRY(check_ptr(fn, "xq", xq));
+  W4_TRY(check_ptr4(fn, "xs", xs));
+  W4_TRY(check_ptr(fn, "out", out));
+  return hip_status(w4::launch_dequant_checkpoint(xq, xs, m, k, out, out_dtype, stream), fn);
+}
+
+// Shapes of the adapters: [L, R, K] and [L, N, R].
+static int check_adapters(const char* fn, int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank,
+                          int64_t segments) {
+  if (m > w4::kLoraMaxRows)
+    return fail(W4_EINVAL, "%s: m = %lld is too large (at most %lld)", fn, (long long)m, (long long)w4::kLoraMaxRows);
+  if (adapters < 0 || adapters > w4::kLoraMaxAdapters)
+    return fail(W4_EINVAL, "%s: adapters = %lld must lie in 0 .. %lld", fn, (long long)adapters,
+                (long long)w4::kLoraMaxAdapters);
+  if (segments < 0 || segments > w4::kLoraMaxSegments)
+    return fail(W4_EINVAL, "%s: segments = %lld must lie in 0 .. %lld", fn, (long long)segments,
+                (long long)w4::kLoraMaxSegments);
+  if (rank <= 0 || rank % 8 != 0 || rank > w4::kLoraMaxRank)
+    return fail(W4_EINVAL, "%s: rank = %d must be a multiple of 8 in 8 .. %d", fn, (int)rank, w4::kLoraMaxRank);
+  const int64_t most = kMaxElems / (rank * (adapters > 0 ? adapters : 1));
+  if (k > most || n > most) return fail(W4_EINVAL, "%s: adapters * rank * columns is too large", fn);
+  return W4_OK;
+}
+
+static int check_x(const char* fn, const char* name, int dtype) {
+  if (dtype != W4_F32 && dtype != W4_BF16)
+    return fail(W4_EINVAL, "%s: %s dtype %d must be W4_F32 or W4_BF16", fn, name, dtype);
+  return W4_OK;
+}
+
+// Pointers of the adapters' arguments, where there is any adapter.
+static int check_adapter_ptrs(const char* fn, const void* a, const void* b, const float* scaling,
+                              const int32_t* offsets, const int32_t* which, const char* low_name, const float* low) {
+  W4_TRY(check_ptr(fn, "a", a));
+  W4_TRY(check_ptr(fn, "b", b));
+  W4_TRY(check_ptr4(fn, "scaling", scaling));
+  W4_TRY(check_ptr4(fn, "offsets", offsets));
+  W4_TRY(check_ptr4(fn, "which", which));
+  return check_ptr(fn, low_name, low);
+}
+
+// Kernel choice of the forward product, as w4a16_grouped_matmul's with one expert.
+int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                      const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
+                      int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
+                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, hipStream_t stream) {
+  static const char* fn = "w4a16_lora_matmul";
+  W4_TRY(check_weights(fn, n, k, group_size, sz_dtype));
+  W4_TRY(check_x(fn, "x", x_dtype));
+  W4_TRY(check_x(fn, "adapter", ab_dtype));
+  W4_TRY(check_y(fn, y_dtype));
+  W4_TRY(check_tokens(fn, m, k, n));
+  W4_TRY(check_adapters(fn, m, k, n, adapters, rank, segments));
+  if (m == 0 || n == 0) return ok();
+  W4_TRY(check_ptr(fn, "x", x));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "zeros", zeros));
+  W4_TRY(check_ptr(fn, "y", y));
+  w4::LoraOut lo{u, b, ab_dtype, adapters, rank, offsets, which, segments};
+  if (adapters == 0 || segments == 0) {
+    lo.segments = 0;
+  } else {
+    W4_TRY(check_adapter_ptrs(fn, a, b, scaling, offsets, which, "u", u));
+    const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u};
+    const hipError_t e = w4::launch_lora_into(in, stream);
+    if (e != hipSuccess) return hip_status(e, fn);
+  }
+  if (x_dtype == W4_BF16 && m > (group_size % 128 == 64 ? 8 : 16) && w4::w4a16_grouped_gemm_fits(k))
+    return hip_status(w4::launch_w4a16_lora_gemm(x, m, k, packed, scales, zeros, sz_dtype, n, group_size, y, y_dtype,
+                                                 lo, stream),
+                      fn);
+  return hip_status(w4::launch_w4a16_lora_rows(x, x_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, y,
+                                               y_dtype, lo, stream),
+                    fn);
+}
+
+size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype,
+                                     int dx_dtype) {
+  static const char* fn = "w4a16_matmul_t_workspace_size";
+  const bool valid = check_weights(fn, n, k, group_size, sz_dtype) == W4_OK && check_x(fn, "dy", dy_dtype) == W4_OK &&
+                     check_y(fn, dx_dtype) == W4_OK && check_tokens(fn, m, k, n) == W4_OK && m <= w4::kLoraMaxRows;
+  ok();
+  if (!valid || m == 0 || n == 0) return 0;
+  return w4::w4a16_t_workspace_bytes(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
+}
+
+static int matmul_t(const char* fn, const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
+                    const void* scales, const void* zeros, int sz_dtype, int64_t n, int32_t group_size,
+                    const w4::LoraInto& in, const w4::LoraOut& out, void* dx, int dx_dtype, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  W4_TRY(check_weights(fn, n, k, group_size, sz_dtype));
+  W4_TRY(check_x(fn, "dy", dy_dtype));
+  W4_TRY(check_y(fn, dx_dtype));
+  W4_TRY(check_tokens(fn, m, k, n));
+  if (in.rank != 0) {
+    W4_TRY(check_x(fn, "adapter", in.w_dtype));
+    W4_TRY(check_adapters(fn, m, k, n, in.count, in.rank, in.segments));
+  }
+  if (m > w4::kLoraMaxRows)
+    return fail(W4_EINVAL, "%s: m = %lld is too large (at most %lld)", fn, (long long)m, (long long)w4::kLoraMaxRows);
+  if (n == 0) return fail(W4_EINVAL, "%s: n must be > 0 (the sum runs over it)", fn);
+  if (m == 0) return ok();
+  W4_TRY(check_ptr(fn, "dx", dx));
+  W4_TRY(check_ptr(fn, "dy", dy));
+  W4_TRY(check_ptr(fn, "packed", packed));
+  W4_TRY(check_ptr(fn, "scales", scales));
+  W4_TRY(check_ptr(fn, "zeros", zeros));
+  const size_t need = w4::w4a16_t_workspace_bytes(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
+  if (need > 0) {
+    W4_TRY(check_ptr(fn, "workspace", workspace));
+    if (workspace_bytes < need)
+      return fail(W4_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+  }
+  w4::LoraOut lo = out;
+  if (in.rank == 0 || in.count == 0 || in.segments == 0) {
+    lo.count = lo.segments = 0;
+  } else {
+    W4_TRY(check_adapter_ptrs(fn, out.out, in.weights, in.scaling, in.offsets, in.which, "v", in.low));
+    const hipError_t e = w4::launch_lora_into(in, stream);
+    if (e != hipSuccess) return hip_status(e, fn);
+  }
+  return hip_status(w4::launch_w4a16_t(dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, dx, dx_dtype,
+                                       lo, workspace, stream),
+                    fn);
+}
+
+int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                   const void* zeros, int sz_dtype, int64_t n, int32_t group_size, void* dx, int dx_dtype,
+                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return matmul_t("w4a16_matmul_t", dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, w4::LoraInto{},
+                  w4::LoraOut{}, dx, dx_dtype, workspace, workspace_bytes, stream);
+}
+
+int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                        const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
+                        int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
+                        const int32_t* which, int64_t segments, float* v, void* dx, int dx_dtype, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  static const char* fn = "w4a16_lora_matmul_t";
+  if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
+  const w4::LoraInto in{false, dy, dy_dtype, m, n, b, ab_dtype, adapters, rank, scaling, offsets, which, segments, v};
+  const w4::LoraOut out{v, a, ab_dtype, adapters, rank, offsets, which, segments};
+  return matmul_t(fn, dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, in, out, dx, dx_dtype,
+                  workspace, workspace_bytes, stream);
+}
+
+static int check_grads(const char* fn, int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank,
+                       int64_t segments) {
+  W4_TRY(check_checkpoint(fn, m, k));
+  if (n < 0 || n > kMaxElems) return fail(W4_EINVAL, "%s: n = %lld out of range", fn, (long long)n);
+  W4_TRY(check_tokens(fn, m, k, n));
+  return check_adapters(fn, m, k, n, adapters, rank, segments);
+}
+
+size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank) {
+  const bool valid = check_grads("lora_grads_workspace_size", m, k, n, adapters, rank, 0) == W4_OK;
+  ok();
+  if (!valid || adapters == 0) return 0;
+  return w4::lora_grads_workspace_bytes(m, k, n, adapters, rank);
+}
+
+int lora_grads(const int8_t* xq, const float* xs, int64_t m, int64_t k, const void* dy, int dy_dtype, int64_t n,
+               const float* u, const float* v, const int32_t* offsets, const int32_t* which, int64_t segments,
+               int64_t adapters, int32_t rank, float* da, float* db, void* workspace, size_t workspace_bytes,
+               hipStream_t stream) {
+  static const char* fn = "lora_grads";
+  W4_TRY(check_grads(fn, m, k, n, adapters, rank, segments));
+  W4_TRY(check_x(fn, "dy", dy_dtype));
+  if (adapters == 0) return ok();
+  W4_TRY(check_ptr(fn, "da", da));
+  if (n > 0) W4_TRY(check_ptr(fn, "db", db));
+  if (m > 0 && segments > 0) {
+    W4_TRY(check_ptr(fn, "xq", xq));
+    W4_TRY(check_ptr4(fn, "xs", xs));
+    if (n > 0) W4_TRY(check_ptr(fn, "dy", dy));
+    W4_TRY(check_ptr(fn, "u", u));
+    W4_TRY(check_ptr(fn, "v", v));
+    W4_TRY(check_ptr4(fn, "offsets", offsets));
+    W4_TRY(check_ptr4(fn, "which", which));
+  }
+  const size_t need = w4::lora_grads_workspace_bytes(m, k, n, adapters, rank);
+  if (need > 0) {
+    W4_TRY(check_ptr(fn, "workspace", workspace));
+    if (workspace_bytes < need)
+      return fail(W4_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+  }
+  const w4::LoraGrads g{xq, xs, m, k, dy, dy_dtype, n, u, v, offsets, which, m > 0 ? segments : 0, adapters, rank, da, db, workspace};
+  return hip_status(w4::launch_lora_grads(g, stream), fn);
+}
+
 }  // extern "C"

@@ -1,0 +1,159 @@
+// Activation checkpoints in 8 bits: blocks of 128 consecutive columns of a row
+// (the last one shorter where K is no multiple of 128), each with a float32 scale.
+//   scale = fl32(max |block| / 127)
+//   code  = the whole number nearest to x / scale (ties to even), at most 127 in magnitude
+//   value = fl32(code scale)
+// The quotient that decides a code is the exact one: a first guess by the
+// reciprocal is at most one off, and the remainder x - code scale, which one fma
+// gives exactly next to the borders +- scale / 2, says which way.
+//
+// Bound by memory: 16 lanes have a block, 8 columns each.
+#include "w4_common.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int CB = 128;  // columns of a block
+
+template <typename TX>
+__device__ __forceinline__ void read8(const TX* p, float (&v)[8]) {
+  if constexpr (sizeof(TX) == 2) {
+    const u32x4 b = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(b[i]), v[2 * i + 1] = bf16_hi(b[i]);
+  } else {
+    const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  }
+}
+
+
+template <typename TX>
+__device__ __forceinline__ void quantize_block(const TX* __restrict__ x, uint32_t blk, int64_t K, uint32_t nb,
+                                               int8_t* __restrict__ xq, float* __restrict__ xs) {
+  const uint32_t row = blk / nb, j = blk - row * nb;
+  const int l = threadIdx.x & 15;
+  const int64_t col = (int64_t)CB * j + 8 * l;
+  const bool in = col < K;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (in) read8(x + row * K + col, v);
+  // magnitudes compare as their bits do, infinities and NaN above all others
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
+    top = a > top ? a : top;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const uint32_t a = (uint32_t)__shfl_xor((int)top, o, kWave);
+    top = a > top ? a : top;
+  }
+  const bool bad = top >= 0x7f800000u;
+  const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
+  if (l == 0) xs[blk] = s;
+  if (!in) return;
+  // tiny scales: x and scale times 2^64, exactly, so that the reciprocal and half the scale are normal numbers
+  const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
+  const float ss = s * up, inv = 1.0f / ss, half = 0.5f * ss;
+  uint32_t out[2] = {0, 0};
+  if (!bad && s != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = v[i] * up;
+      const float q = rintf(a * inv);
+      const float rest = fmaf(-q, ss, a);
+      const int c = (int)q;
+      const bool odd = c & 1;
+      int d = c;
+      if (rest > half || (rest == half && odd)) d = c + 1;
+      else if (rest < -half || (rest == -half && odd)) d = c - 1;
+      d = d > 127 ? 127 : d < -127 ? -127 : d;
+      out[i >> 2] |= (uint32_t)(uint8_t)d << (8 * (i & 3));
+    }
+  }
+  *(u32x2*)(xq + row * K + col) = u32x2{out[0], out[1]};
+}
+
+template <typename TY>
+__device__ __forceinline__ void dequant_block(const int8_t* __restrict__ xq, const float* __restrict__ xs, uint32_t blk,
+                                              int64_t K, uint32_t nb, TY* __restrict__ y) {
+  const uint32_t row = blk / nb, j = blk - row * nb;
+  const int64_t col = (int64_t)CB * j + 8 * (threadIdx.x & 15);
+  if (col >= K) return;
+  const float s = xs[blk];
+  const u32x2 q = *(const u32x2*)(xq + row * K + col);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = (float)(int8_t)(q[i >> 2] >> (8 * (i & 3))) * s;
+    // no instruction: keeps the compiler from making the product and its rounding to
+    // fp16 one instruction, which would round once where the definition rounds twice
+    asm("" : "+v"(v[i]));
+  }
+  TY* out = y + row * K + col;
+  if constexpr (sizeof(TY) == 4) {
+    ((f32x4*)out)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    ((f32x4*)out)[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (__is_same(TY, _Float16)) b[i] = f32_to_f16_bits(v[2 * i]) | f32_to_f16_bits(v[2 * i + 1]) << 16;
+      else b[i] = f32_to_bf16_bits(v[2 * i]) | f32_to_bf16_bits(v[2 * i + 1]) << 16;
+    }
+    *(u32x4*)out = b;
+  }
+}
+
+// A workgroup has 16 blocks at a time; launches of more than 2^20 workgroups loop.
+uint32_t checkpoint_grid(uint32_t blocks) {
+  const uint32_t g = (blocks + 15u) / 16u;
+  return g < (1u << 20) ? g : 1u << 20;
+}
+
+}  // namespace
+
+template <typename TX>
+__global__ __launch_bounds__(256) void k_quantize_checkpoint(const TX* __restrict__ x, uint32_t blocks, int64_t K,
+                                                             uint32_t nb, int8_t* __restrict__ xq,
+                                                             float* __restrict__ xs) {
+  for (uint32_t blk = blockIdx.x * 16u + (threadIdx.x >> 4); blk < blocks; blk += gridDim.x * 16u)
+    quantize_block(x, blk, K, nb, xq, xs);  // whole groups of 16 lanes
+}
+
+template <typename TY>
+__global__ __launch_bounds__(256) void k_dequant_checkpoint(const int8_t* __restrict__ xq,
+                                                            const float* __restrict__ xs, uint32_t blocks, int64_t K,
+                                                            uint32_t nb, TY* __restrict__ y) {
+  for (uint32_t blk = blockIdx.x * 16u + (threadIdx.x >> 4); blk < blocks; blk += gridDim.x * 16u)
+    dequant_block(xq, xs, blk, K, nb, y);
+}
+
+hipError_t launch_quantize_checkpoint(const void* x, int x_dtype, int64_t m, int64_t k, int8_t* xq, float* xs,
+                                      hipStream_t st) {
+  const uint32_t nb = (uint32_t)((k + CB - 1) / CB), blocks = (uint32_t)(m * nb);
+  const dim3 grid(checkpoint_grid(blocks));
+  if (x_dtype == W4_F32)
+    k_quantize_checkpoint<<<grid, 256, 0, st>>>((const float*)x, blocks, k, nb, xq, xs);
+  else
+    k_quantize_checkpoint<<<grid, 256, 0, st>>>((const uint16_t*)x, blocks, k, nb, xq, xs);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequant_checkpoint(const int8_t* xq, const float* xs, int64_t m, int64_t k, void* out, int out_dtype,
+                                     hipStream_t st) {
+  const uint32_t nb = (uint32_t)((k + CB - 1) / CB), blocks = (uint32_t)(m * nb);
+  const dim3 grid(checkpoint_grid(blocks));
+  if (out_dtype == W4_F32) k_dequant_checkpoint<<<grid, 256, 0, st>>>(xq, xs, blocks, k, nb, (float*)out);
+  else if (out_dtype == W4_F16) k_dequant_checkpoint<<<grid, 256, 0, st>>>(xq, xs, blocks, k, nb, (_Float16*)out);
+  else k_dequant_checkpoint<<<grid, 256, 0, st>>>(xq, xs, blocks, k, nb, (uint16_t*)out);
+  return hipGetLastError();
+}
+
+}  // namespace w4

@@ -129,6 +129,79 @@ bool w4a16_grouped_gemm_fits(int64_t k);
 hipError_t launch_w4a16_grouped_gemm(const void* x, int64_t t, int64_t k, const int* offsets, int experts,
                                      const uint8_t* packed, const void* scales, const void* zeros, int sz_dtype,
                                      int64_t n, int g, void* y, int y_dtype, hipStream_t st);
+// Activation checkpoints in 8 bits.
+hipError_t launch_quantize_checkpoint(const void* x, int x_dtype, int64_t m, int64_t k, int8_t* xq, float* xs,
+                                      hipStream_t st);
+hipError_t launch_dequant_checkpoint(const int8_t* xq, const float* xs, int64_t m, int64_t k, void* out, int out_dtype,
+                                     hipStream_t st);
+// Low-rank adapters.  Rows in segments (offsets and which in device memory),
+// matrices of `count` adapters of rank `rank` (a multiple of 8).
+// low [M, R] = scaling x W^T, down: W [L, R, D] (D % 32 == 0), otherwise W [L, D, R].
+struct LoraInto {
+  bool down;
+  const void* x;
+  int x_dtype;
+  int64_t m, d;
+  const void* weights;
+  int w_dtype;
+  int64_t count;
+  int rank;
+  const float* scaling;
+  const int* offsets;
+  const int* which;
+  int64_t segments;
+  float* low;
+};
+hipError_t launch_lora_into(const LoraInto& a, hipStream_t st);
+// The low-rank part that a product adds: low [M, R] times `out`, [L, N, R] beside
+// x W^T (whose columns are N) and [L, R, K] beside dy W.  count 0: none.
+struct LoraOut {
+  const float* low;
+  const void* out;
+  int dtype;
+  int64_t count;
+  int rank;
+  const int* offsets;
+  const int* which;
+  int64_t segments;
+};
+// y = x W^T + low out^T: few rows or float32 x, and many rows.
+hipError_t launch_w4a16_lora_rows(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed,
+                                  const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y,
+                                  int y_dtype, const LoraOut& lo, hipStream_t st);
+hipError_t launch_w4a16_lora_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                                  const void* zeros, int sz_dtype, int64_t n, int g, void* y, int y_dtype,
+                                  const LoraOut& lo, hipStream_t st);
+// dx = dy W + low out.  Bytes of workspace (0: none).
+size_t w4a16_t_workspace_bytes(int64_t m, int64_t k, int64_t n, int g, int dy_dtype, int sz_dtype, int dx_dtype);
+hipError_t launch_w4a16_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
+                          const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* dx,
+                          int dx_dtype, const LoraOut& lo, void* ws, hipStream_t st);
+// Gradients of the adapters from the 8-bit checkpoint of x, dy and the low-rank values.
+struct LoraGrads {
+  const int8_t* xq;
+  const float* xs;
+  int64_t m, k;
+  const void* dy;
+  int dy_dtype;
+  int64_t n;
+  const float* u;
+  const float* v;
+  const int* offsets;
+  const int* which;
+  int64_t segments, count;
+  int rank;
+  float* da;
+  float* db;
+  void* ws;
+};
+size_t lora_grads_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t count, int rank);
+hipError_t launch_lora_grads(const LoraGrads& a, hipStream_t st);
+// Limits of the adapters.
+constexpr int64_t kLoraMaxRows = (int64_t)1 << 24;
+constexpr int64_t kLoraMaxSegments = (int64_t)1 << 20;
+constexpr int64_t kLoraMaxAdapters = 65536;
+constexpr int kLoraMaxRank = 256;
 // Limits of the products by expert: tile numbers stay below 2^31.
 constexpr int64_t kGroupedMaxRows = (int64_t)1 << 24;
 constexpr int64_t kGroupedMaxExperts = 65536;

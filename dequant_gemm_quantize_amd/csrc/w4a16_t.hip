@@ -1,0 +1,271 @@
+// Product with the transposed INT4 weight, the gradient through it:
+//   dx[m, k] = sum_n dy[m, n] (q[n, k] - zp[n, j]) s[n, j]  (+ sum_r low[m, r] A[l(m), r, k])
+// with j the group of column k.  The scale changes along the sum, so it goes to the weight before the product.
+//
+// Few rows, and float32: k_w4a16_t_rows, on v_mfma_f32_16x16x32_bf16.  A wave has
+// 256 columns of 16 MB rows of dx and goes through N 32 weight rows at a time.
+// The sum runs over weight rows, the codes of a word over columns: lane (l16,
+// h) loads 16 codes (8 bytes) of each of rows 8 h .. 8 h + 7, and the eight
+// values of one column, one out of each word, are the operand of one of 16 MFMAs, whose 16
+// columns are 16 l16 + j.  So nothing is transposed in memory or LDS.  The waves of
+// a workgroup and the workgroups of a strip share N; the partial sums, float32, meet
+// in LDS and in the workspace, where k_w4a16_t_sum adds them in order, and the low-rank part.
+//
+// Rounding: bf16 dy with a bf16 result takes a weight rounded to bf16, as w4a16_matmul does
+// (half a step, 2^-8 at most, beside the result's own).  Otherwise the weight is the
+// exact sum of bf16 parts, two with fp16 scales (15 bits), three with float32 ones (24).
+#include "lora.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kTWaves = 4;
+constexpr int kTStrip = 256;  // columns of a workgroup
+constexpr int64_t kTGrid = 1 << 20;  // workgroups of a part; more tiles than that loop
+constexpr int64_t kTSumGrid = 1 << 22;
+
+template <typename TS>
+__device__ __forceinline__ float t_scale(const void* p, int64_t i) {
+  return ScaleT<TS>::load(p, i);
+}
+
+// How a call splits N: parts of `steps` steps of 32 weight rows.
+struct TPlan {
+  int mb;  // blocks of 16 rows a workgroup
+  int64_t rows, strips, parts, steps;
+};
+
+TPlan t_plan(int64_t m, int64_t k, int64_t n, bool exact) {
+  TPlan p;
+  p.mb = exact || m <= 16 ? 1 : 2;
+  p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
+  p.strips = (k + kTStrip - 1) / kTStrip;
+  const int64_t all = (n + 31) / 32, groups = p.rows * p.strips;
+  int64_t parts = 1024 / groups;
+  if (parts > all / (2 * kTWaves)) parts = all / (2 * kTWaves);
+  if (parts < 1) parts = 1;
+  p.steps = (all + parts - 1) / parts;
+  p.parts = (all + p.steps - 1) / p.steps;
+  return p;
+}
+
+}  // namespace
+
+// PW: bf16 parts of a weight.
+template <typename TX, typename TS, int PW, int MB>
+__global__ __launch_bounds__(64 * kTWaves) void k_w4a16_t_rows(
+    const TX* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
+    const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, int wide,
+    float* __restrict__ part) {
+  constexpr int PX = Parts<TX>::n;
+  constexpr int NA = PX + PW > 2 ? 2 : 1;  // sums: the upper parts' and the others'
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][16][256]
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, h = lane >> 4;
+  const int64_t strips = (K + kTStrip - 1) / kTStrip, tiles = strips * ((M + 16 * MB - 1) / (16 * MB));
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t k0 = kTStrip * (tile % strips), m0 = 16 * MB * (tile / strips);
+    const int64_t col = k0 + 16 * l16;
+    const int64_t cc = col < K ? col : 0;  // lanes past K compute what nobody stores
+    const int64_t ng = K / g, gi = cc / g, half = K / 2;
+    const int64_t all = (N + 31) / 32, first = (int64_t)steps * blockIdx.y;
+    const int64_t last = first + steps < all ? first + steps : all;
+
+    f32x4 acc[MB][16][NA];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int a = 0; a < NA; ++a) acc[b][j][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int64_t s = first + w; s < last; s += kTWaves) {
+      const int64_t n0 = 32 * s + 8 * h;
+      u32x2 p[8];
+      float sc[8], zp[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i < N ? n0 + i : N - 1;  // dy is zero there
+        p[i] = *(const u32x2*)(packed + n * half + cc / 2);
+        sc[i] = t_scale<TS>(scales, n * ng + gi);
+        zp[i] = t_scale<TS>(zeros, n * ng + gi);
+      }
+      bf16x8 a[MB][PX];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const int64_t m = m0 + 16 * b + l16;
+        row8(dy + (m < M ? m : 0) * N, n0, N, m < M, wide, a[b]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        u32x4 v0, v1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = (float)((p[i][j >> 3] >> (4 * (j & 7))) & 15u);
+          const float v = (q - zp[i]) * sc[i];
+          if (i < 4) v0[i] = __float_as_uint(v);
+          else v1[i - 4] = __float_as_uint(v);
+        }
+        bf16x8 b[PW];
+        if constexpr (PW == 1) {
+          u32x4 r;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v0[2 * i]), (__bf16)__uint_as_float(v0[2 * i + 1])});
+            r[2 + i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v1[2 * i]), (__bf16)__uint_as_float(v1[2 * i + 1])});
+          }
+          b[0] = __builtin_bit_cast(bf16x8, r);
+        } else {
+          bf16x8 all3[3];
+          split8(v0, v1, all3);
+#pragma unroll
+          for (int i = 0; i < PW; ++i) b[i] = all3[i];
+        }
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          if constexpr (NA == 1) acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[mb][0], b[0], acc[mb][j][0], 0, 0, 0);
+          else mfma_parts(a[mb], b, acc[mb][j]);
+        }
+      }
+    }
+
+    // register e: row 4 h + e, columns 16 l16 + j
+    float* out = part + (int64_t)blockIdx.y * M * K;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          f32x4 v;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = NA == 1 ? acc[b][j + t][0][e] : acc[b][j + t][0][e] + acc[b][j + t][NA - 1][e];
+          *(f32x4*)(sums + (w * 16 + 4 * h + e) * kTStrip + 16 * l16 + j) = v;
+        }
+      __syncthreads();
+      for (int o = 4 * threadIdx.x; o < 16 * kTStrip; o += 4 * 64 * kTWaves) {
+        const int64_t m = m0 + 16 * b + o / kTStrip, k = k0 + o % kTStrip;
+        if (m >= M || k >= K) continue;
+        f32x4 v = *(const f32x4*)(sums + o);
+#pragma unroll
+        for (int i = 1; i < kTWaves; ++i) v += *(const f32x4*)(sums + i * 16 * kTStrip + o);
+        *(f32x4*)(out + m * K + k) = v;
+      }
+    }
+  }
+}
+
+// 4 elements of dx: the partial sums, in order, and the low-rank part of adapter l.
+template <typename TY>
+__device__ __forceinline__ void t_sum4(const float* part, int parts, int64_t M, int64_t K, const Adapters& ad, TY* dx,
+                                       int64_t m, int64_t k, int l) {
+  const float* p = part + m * K + k;
+  f32x4 v = *(const f32x4*)p;
+#pragma unroll 8
+  for (int s = 1; s < parts; ++s) v += *(const f32x4*)(p + (int64_t)s * M * K);
+  if (l >= 0) {
+    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float* low = ad.low + m * ad.rank;
+    if (ad.wide) {
+      const float* a = (const float*)ad.out + (int64_t)l * ad.rank * K + k;
+#pragma unroll 8
+      for (int r = 0; r < ad.rank; ++r) {
+        const f32x4 c = *(const f32x4*)(a + r * K);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = fmaf(low[r], c[i], d[i]);
+      }
+    } else {
+      const uint16_t* a = (const uint16_t*)ad.out + (int64_t)l * ad.rank * K + k;
+#pragma unroll 8
+      for (int r = 0; r < ad.rank; ++r) {
+        const u32x2 c = *(const u32x2*)(a + r * K);
+        d[0] = fmaf(low[r], bf16_lo(c.x), d[0]);
+        d[1] = fmaf(low[r], bf16_hi(c.x), d[1]);
+        d[2] = fmaf(low[r], bf16_lo(c.y), d[2]);
+        d[3] = fmaf(low[r], bf16_hi(c.y), d[3]);
+      }
+    }
+    v += d;
+  }
+  TY* out = dx + m * K + k;
+  if constexpr (sizeof(TY) == 4) {
+    *(f32x4*)out = v;
+  } else {
+    u32x2 b;
+    b.x = f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16;
+    b.y = f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16;
+    *(u32x2*)out = b;
+  }
+}
+
+// A wave has 256 columns of one row of dx at a time.
+template <typename TY>
+__global__ __launch_bounds__(64) void k_w4a16_t_sum(const float* __restrict__ part, int parts, int64_t M, int64_t K,
+                                                    Adapters ad, TY* __restrict__ dx) {
+  const int lane = threadIdx.x;
+  const int64_t strips = (K + 255) / 256, tiles = M * strips;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t m = tile / strips, k = 256 * (tile % strips) + 4 * lane;
+    const int l = ad.count > 0 ? row_adapter(ad, m, lane) : -1;
+    if (k < K) t_sum4(part, parts, M, K, ad, dx, m, k, l);
+  }
+}
+
+// Whether weights keep all their bits: always but for bf16 dy with a bf16 result.
+static bool t_exact(int dy_dtype, int dx_dtype) { return dy_dtype != W4_BF16 || dx_dtype != W4_BF16; }
+
+size_t w4a16_t_workspace_bytes(int64_t m, int64_t k, int64_t n, int g, int dy_dtype, int sz_dtype, int dx_dtype) {
+  return (size_t)t_plan(m, k, n, t_exact(dy_dtype, dx_dtype)).parts * (size_t)m * (size_t)k * 4;
+}
+
+template <typename TX, typename TS, int PW, int MB>
+static hipError_t t_rows_go(const TX* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                            const void* zeros, int64_t n, int g, const TPlan& p, float* part, hipStream_t st) {
+  constexpr size_t lds = (size_t)kTWaves * 16 * kTStrip * 4;
+  const int64_t tiles = p.strips * p.rows;
+  k_w4a16_t_rows<TX, TS, PW, MB><<<dim3((unsigned)(tiles < kTGrid ? tiles : kTGrid), (unsigned)p.parts), 64 * kTWaves, lds, st>>>(
+      dy, m, n, packed, scales, zeros, k, g, (int)p.steps, n * (int64_t)sizeof(TX) % 16 == 0, part);
+  return hipGetLastError();
+}
+
+template <typename TX, typename TS>
+static hipError_t t_rows(const void* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                         const void* zeros, int64_t n, int g, const TPlan& p, bool exact, float* part, hipStream_t st) {
+  const TX* d = (const TX*)dy;
+  constexpr int PW = sizeof(TS) == 2 ? 2 : 3;
+  if (exact) return t_rows_go<TX, TS, PW, 1>(d, m, k, packed, scales, zeros, n, g, p, part, st);
+  if constexpr (sizeof(TX) == 2) {
+    if (p.mb == 1) return t_rows_go<TX, TS, 1, 1>(d, m, k, packed, scales, zeros, n, g, p, part, st);
+    return t_rows_go<TX, TS, 1, 2>(d, m, k, packed, scales, zeros, n, g, p, part, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_w4a16_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
+                          const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* dx,
+                          int dx_dtype, const LoraOut& lo, void* ws, hipStream_t st) {
+  const bool exact = t_exact(dy_dtype, dx_dtype);
+  const TPlan p = t_plan(m, k, n, exact);
+  float* part = (float*)ws;
+  hipError_t e;
+  if (dy_dtype == W4_F32)
+    e = sz_dtype == W4_F16 ? t_rows<float, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st)
+                           : t_rows<float, float>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st);
+  else
+    e = sz_dtype == W4_F16 ? t_rows<uint16_t, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st)
+                           : t_rows<uint16_t, float>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st);
+  if (e != hipSuccess) return e;
+  const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
+                    (int)lo.count, lo.rank, lo.dtype == W4_F32};
+  const int64_t tiles = m * ((k + 255) / 256);
+  const dim3 grid((unsigned)(tiles < kTSumGrid ? tiles : kTSumGrid));
+  if (dx_dtype == W4_F32) k_w4a16_t_sum<<<grid, 64, 0, st>>>(part, (int)p.parts, m, k, ad, (float*)dx);
+  else k_w4a16_t_sum<<<grid, 64, 0, st>>>(part, (int)p.parts, m, k, ad, (uint16_t*)dx);
+  return hipGetLastError();
+}
+
+}  // namespace w4

@@ -8,7 +8,8 @@ Every numeric step runs in the HIP kernels behind libw4.so: quantization at
 construction (asymmetric, symmetric, symmetric with a percentile or MSE
 calibrated scale, or GPTQ with calibration activations), the product in forward (W4A16, or W4A8 with per-token
 INT8 activations).  This module only reshapes tensors and keeps the buffers.
-The layers are for inference: no gradient flows through their results.
+The layers are for inference: no gradient flows through their results, but
+for LoRALinear, which trains low-rank adapters beside a frozen INT4 weight.
 """
 from __future__ import annotations
 
@@ -266,6 +267,109 @@ class QuantizedExperts(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"experts={self.experts}, in_features={self.in_features}, out_features={self.out_features}, "
                 f"fmt={self.fmt}, group_size={self.group_size}")
+
+
+class _LoRALinear(torch.autograd.Function):
+    """y of w4a16_lora_matmul, differentiable with respect to x, a and b.  What
+    is kept for the backward pass of x is its 8-bit checkpoint, and only if a or b is trained."""
+
+    @staticmethod
+    def forward(ctx, x, packed, scales, zeros, group_size, a, b, scaling, offsets, adapters):
+        u = x.new_empty((x.shape[0], a.shape[1]), dtype=torch.float32)
+        y = _lib.w4a16_lora_matmul(x, packed, scales, zeros, group_size, a, b, scaling, offsets, adapters, u=u)
+        trained = ctx.needs_input_grad[5] or ctx.needs_input_grad[6]
+        kept = (u, *_lib.quantize_checkpoint_int8(x)) if trained else ()
+        ctx.save_for_backward(packed, scales, zeros, a, b, scaling, offsets, adapters, *kept)
+        ctx.group_size = group_size
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        packed, scales, zeros, a, b, scaling, offsets, adapters, *kept = ctx.saved_tensors
+        dy = dy.contiguous()
+        v = dy.new_empty((dy.shape[0], a.shape[1]), dtype=torch.float32)
+        dx = _lib.w4a16_lora_matmul_t(dy, packed, scales, zeros, ctx.group_size, a, b, scaling, offsets, adapters, v=v)
+        da = db = None
+        if kept:
+            da, db = _lib.lora_grads(kept[1], kept[2], dy, kept[0], v, offsets, adapters, a.shape[0])
+            da, db = da.to(a.dtype), db.to(b.dtype)
+        return dx, None, None, None, None, da, db, None, None, None
+
+
+def lora_linear(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int,
+                a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor, offsets: torch.Tensor,
+                adapters: torch.Tensor) -> torch.Tensor:
+    """w4a16_lora_matmul (arguments as there; y in x's dtype), differentiable
+    once with respect to x, a and b; the INT4 weight stays frozen and scaling is a
+    constant.  Between forward and backward it keeps the weight (not copied),
+    u [M, R] and, if a or b needs a gradient, x in 8 bits: their gradients are those at
+    the values that the checkpoint stands for."""
+    args = (x, packed, scales, zeros, group_size, a, b, scaling, offsets, adapters)
+    if torch.is_grad_enabled() and (x.requires_grad or a.requires_grad or b.requires_grad):
+        return _LoRALinear.apply(*args)
+    return _lib.w4a16_lora_matmul(*args)
+
+
+class LoRALinear(torch.nn.Module):
+    """y = x . dequant(Wq)^T + alpha / rank (x . A_l^T) . B_l^T: a frozen INT4
+    projection with ``adapters`` trainable low-rank adapters beside it, one
+    chosen per request.
+
+    forward(x, offsets, which): x [..., in_features] in bf16, fp32 or fp16 on the
+    weight's GPU, its rows (all leading dimensions taken together) in requests: rows
+    offsets[s] .. offsets[s+1]-1 (int32 [S + 1] on the GPU) have adapter which[s]
+    (int32 [S]; negative: none).  Without them every row has adapter 0.
+    Returns [..., out_features] in x's dtype.
+
+    Differentiable with respect to x and the parameters a [L, R, in] (normal,
+    std 1 / sqrt(in)) and b [L, out, R] (zeros, so that a fresh adapter adds nothing);
+    between forward and backward x is kept in 8 bits (quantize_checkpoint_int8).  The INT4 buffers are
+    those of ``base``, not copies.  To capture a training step into a graph, run its
+    warm-up on the capturing stream and let no earlier autograd graph of the same
+    parameters live."""
+
+    def __init__(self, base: QuantizedLinear, rank: int = 16, alpha: Optional[float] = None, adapters: int = 1,
+                 dtype: torch.dtype = torch.float32):
+        super().__init__()
+        if rank <= 0 or rank % 8 or rank > 256:
+            raise ValueError(f"rank = {rank} must be a multiple of 8 in 8 .. 256")
+        if adapters < 1:
+            raise ValueError(f"adapters = {adapters} must be at least 1")
+        if dtype not in _lib.Y_DTYPES:
+            raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+        if base.act_int8:
+            raise ValueError("LoRALinear multiplies bf16 or fp32 activations; base has act_int8")
+        self.in_features, self.out_features, self.group_size = base.in_features, base.out_features, base.group_size
+        self.rank, self.adapters = rank, adapters
+        self.alpha = float(rank if alpha is None else alpha)
+        dev = base.packed.device
+        self.register_buffer("packed", base.packed)
+        self.register_buffer("scales", base.scales)
+        self.register_buffer("zeros", base.zeros)
+        self.register_buffer("scaling", torch.full((adapters,), self.alpha / rank, dtype=torch.float32, device=dev))
+        self.register_buffer("_all", torch.zeros((1,), dtype=torch.int32, device=dev), persistent=False)
+        self.a = torch.nn.Parameter(torch.randn((adapters, rank, self.in_features), device=dev).mul_(
+            self.in_features ** -0.5).to(dtype))
+        self.b = torch.nn.Parameter(torch.zeros((adapters, self.out_features, rank), dtype=dtype, device=dev))
+
+    def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                which: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"x has {x.shape[-1]} features, the layer takes {self.in_features}")
+        if (offsets is None) != (which is None):
+            raise ValueError("offsets and which come together")
+        x2 = _activations(x.reshape(-1, self.in_features).contiguous())
+        if offsets is None:
+            which = self._all
+            offsets = torch.nn.functional.pad(which.new_full((1,), x2.shape[0]), (1, 0))
+        y = lora_linear(x2, self.packed, self.scales, self.zeros, self.group_size, self.a, self.b, self.scaling,
+                        offsets, which)
+        return y.to(_result_dtype(x, None)).reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, group_size={self.group_size}, "
+                f"rank={self.rank}, alpha={self.alpha}, adapters={self.adapters}")
 
 
 def replace_linears(module: torch.nn.Module, group_size: int = 128, mode: str = "asym",

@@ -391,6 +391,96 @@ int w4a16_grouped_matmul(const void* x, int x_dtype, int64_t t, int64_t k, const
                          int sz_dtype, int64_t n, int32_t group_size, void* y, int y_dtype,
                          hipStream_t stream);
 
+/*
+ * Activation checkpoints in 8 bits -- what a forward pass keeps of x [M, K] for
+ * the backward pass.  A block is 128 consecutive columns of a row, the last one
+ * of a row shorter where K is no multiple of 128; K % 32 == 0, M <= 2^24.
+ *
+ * quantize_checkpoint_int8 -- per block
+ *     xs = max|block| / 127 in float32 (one rounding)
+ *     xq = the whole number nearest to x / xs, ties to even, decided on the exact
+ *          quotient, at most 127 in magnitude (0 where xs is 0)
+ *   x [M, K] W4_F32 or W4_BF16; xq [M, K] int8; xs [M, ceil(K / 128)] float32
+ *   (4-byte aligned).  A block that holds an infinity or a NaN gets a NaN for
+ *   its scale and codes 0, so it dequantizes to NaN.  Bit-exact.
+ * dequant_checkpoint_int8 -- out[m, k] = xq xs, one float32 product, rounded
+ *   (nearest-even) to out_dtype (W4_F32, W4_F16, W4_BF16).  Bit-exact.
+ */
+int quantize_checkpoint_int8(const void* x, int x_dtype, int64_t m, int64_t k, int8_t* xq, float* xs,
+                             hipStream_t stream);
+int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_t k, void* out, int out_dtype,
+                            hipStream_t stream);
+
+/*
+ * Low-rank adapters beside one INT4 weight: L adapters A [L, R, K], B [L, N, R]
+ * (ab_dtype W4_F32 or W4_BF16), scaling float32 [L], and the rows of a batch in
+ * S segments (requests): segment s has rows offsets[s] .. offsets[s + 1] - 1 and
+ * the adapter which[s]; a negative number, or one from L on, stands for none.
+ * Two segments may have the same adapter; a segment may have no row.  Rows
+ * before offsets[0] and from offsets[S] on have no adapter.
+ *
+ * offsets (S + 1 int32, 0 <= offsets[0] <= ... <= offsets[S] <= M) and which (S
+ * int32) are read on the device only, as in the products by expert: no wait, and
+ * a captured call can be replayed with others in the same buffers.  Offsets that
+ * fall or leave 0..M give unspecified (but memory-safe) results.
+ * scaling, offsets and which need 4-byte alignment only.
+ *
+ *   R a multiple of 8 in 8 .. 256; M <= 2^24, L <= 65536, S <= 2^20,
+ *   L*R*K and L*R*N <= 2^36 (W4_EINVAL beyond them).  With L == 0 or S == 0 no
+ *   row has an adapter, and a, b, scaling, offsets, which and u or v may be NULL.
+ *
+ * w4a16_lora_matmul -- with l the adapter of row m,
+ *     u[m, r] = scaling[l] sum_k x[m, k] A[l, r, k]         (float32 [M, R])
+ *     y[m, n] = sum_k x[m, k] W[n, k] + sum_r u[m, r] B[l, n, r]
+ *   x, packed, scales, zeros and y as in w4a16_matmul (x W4_BF16 or W4_F32, y
+ *   likewise).  No weight is rounded: as w4a16_grouped_matmul, sums are float32.
+ *   u is an output; rows of no adapter are left as they were.
+ *
+ * w4a16_matmul_t -- dx [M, K] = dy [M, N] . W, the gradient of w4a16_matmul
+ *   with respect to x.  dy and dx W4_BF16 or W4_F32; N > 0.  Sums are float32.
+ *   With bf16 dy and bf16 dx the weight is rounded to bf16 before the product;
+ *   otherwise it keeps the bits of (q - zp) s.
+ *   workspace: device memory, 16-byte aligned, of at least
+ *   w4a16_matmul_t_workspace_size bytes (W4_EINVAL below; 0: may be NULL), its
+ *   contents ignored on entry and unspecified on return.  Calls that overlap on
+ *   one workspace race.  The size depends only on the arguments, and is 0 for
+ *   arguments the call rejects.
+ *
+ * w4a16_lora_matmul_t -- the gradient of w4a16_lora_matmul with respect to x:
+ *     v[m, r]  = scaling[l] sum_n dy[m, n] B[l, n, r]       (float32 [M, R])
+ *     dx[m, k] = sum_n dy[m, n] W[n, k] + sum_r v[m, r] A[l, r, k]
+ *   v is an output; rows of no adapter are left as they were.  Otherwise as
+ *   w4a16_matmul_t, and the same workspace.
+ *
+ * lora_grads -- the gradients of the adapters, float32, from x's 8-bit
+ *   checkpoint (xq [M, K], xs), dy and the two calls' u and v:
+ *     da[l, r, k] = sum over rows m of adapter l of v[m, r] xq[m, k] xs[m, k / 128]
+ *     db[l, n, r] = sum over rows m of adapter l of u[m, r] dy[m, n]
+ *   An adapter without rows gets zeros.  Rows of no adapter are not read.
+ *   workspace as above, lora_grads_workspace_size bytes.
+ *
+ * All are deterministic.  A row that holds an infinity may give NaN.
+ */
+int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                      const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
+                      int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
+                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, hipStream_t stream);
+size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype,
+                                     int dx_dtype);
+int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                   const void* zeros, int sz_dtype, int64_t n, int32_t group_size, void* dx, int dx_dtype,
+                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                        const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
+                        int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
+                        const int32_t* which, int64_t segments, float* v, void* dx, int dx_dtype, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank);
+int lora_grads(const int8_t* xq, const float* xs, int64_t m, int64_t k, const void* dy, int dy_dtype, int64_t n,
+               const float* u, const float* v, const int32_t* offsets, const int32_t* which, int64_t segments,
+               int64_t adapters, int32_t rank, float* da, float* db, void* workspace, size_t workspace_bytes,
+               hipStream_t stream);
+
 /* Static description of a w4_status value (never NULL). */
 const char* w4_status_string(int status);
 
