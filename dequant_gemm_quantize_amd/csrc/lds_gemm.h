@@ -17,6 +17,11 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
 }
 
+// The same with 4 bytes a lane, to dst + 4 lane.
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 4, (int)off, 0, 0, 0);
+}
+
 // Orders R LDS reads among the M MFMAs that precede this call: at most 15 reads
 // of a wave can be outstanding, and one more would hold up the MFMAs behind it.
 template <int M, int R>

@@ -31,20 +31,39 @@ __device__ __forceinline__ float t_scale(const void* p, int64_t i) {
   return ScaleT<TS>::load(p, i);
 }
 
-// How a call splits N: parts of `steps` steps of 32 weight rows.
+// How a call is computed: in tiles (w4a16_t_gemm.h) or by k_w4a16_t_rows, and
+// how it splits N: parts of `steps` steps of 64 or 32 weight rows.
 struct TPlan {
-  int mb;  // blocks of 16 rows a workgroup
+  bool tiles;
+  int mi, pw;          // tiles of 128 mi rows; bf16 parts of a weight
+  int mb;              // blocks of 16 rows a workgroup of k_w4a16_t_rows
   int64_t rows, strips, parts, steps;
 };
 
-TPlan t_plan(int64_t m, int64_t k, int64_t n, bool exact) {
+TPlan t_plan(int64_t m, int64_t k, int64_t n, int dy_dtype, int sz_dtype, int dx_dtype) {
+  const bool exact = dy_dtype != W4_BF16 || dx_dtype != W4_BF16;  // weights keep their bits
   TPlan p;
-  p.mb = exact || m <= 16 ? 1 : 2;
-  p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
-  p.strips = (k + kTStrip - 1) / kTStrip;
-  const int64_t all = (n + 31) / 32, groups = p.rows * p.strips;
-  int64_t parts = 1024 / groups;
-  if (parts > all / (2 * kTWaves)) parts = all / (2 * kTWaves);
+  p.pw = !exact ? 1 : sz_dtype == W4_F16 ? 2 : 3;
+  // rows of dy start at 16-byte addresses; 256 of them stay below 2^31 bytes
+  p.tiles = dy_dtype == W4_BF16 && m > 32 && n % 8 == 0 && n <= ((int64_t)1 << 21);
+  int64_t parts, all;
+  if (p.tiles) {
+    p.mi = p.pw == 3 || m <= 128 ? 1 : 2;
+    p.mb = 0;
+    p.rows = (m + 128 * p.mi - 1) / (128 * p.mi);
+    p.strips = (k + 127) / 128;
+    all = (n + 63) / 64;
+    parts = 256 / (p.rows * p.strips);
+    if (parts > all / 8) parts = all / 8;
+  } else {
+    p.mi = 0;
+    p.mb = exact || m <= 16 ? 1 : 2;
+    p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
+    p.strips = (k + kTStrip - 1) / kTStrip;
+    all = (n + 31) / 32;
+    parts = 1024 / (p.rows * p.strips);
+    if (parts > all / (2 * kTWaves)) parts = all / (2 * kTWaves);
+  }
   if (parts < 1) parts = 1;
   p.steps = (all + parts - 1) / parts;
   p.parts = (all + p.steps - 1) / p.steps;
@@ -215,11 +234,9 @@ __global__ __launch_bounds__(64) void k_w4a16_t_sum(const float* __restrict__ pa
   }
 }
 
-// Whether weights keep all their bits: always but for bf16 dy with a bf16 result.
-static bool t_exact(int dy_dtype, int dx_dtype) { return dy_dtype != W4_BF16 || dx_dtype != W4_BF16; }
-
 size_t w4a16_t_workspace_bytes(int64_t m, int64_t k, int64_t n, int g, int dy_dtype, int sz_dtype, int dx_dtype) {
-  return (size_t)t_plan(m, k, n, t_exact(dy_dtype, dx_dtype)).parts * (size_t)m * (size_t)k * 4;
+  const TPlan p = t_plan(m, k, n, dy_dtype, sz_dtype, dx_dtype);
+  return p.tiles && p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)k * 4;
 }
 
 template <typename TX, typename TS, int PW, int MB>
@@ -234,10 +251,10 @@ static hipError_t t_rows_go(const TX* dy, int64_t m, int64_t k, const uint8_t* p
 
 template <typename TX, typename TS>
 static hipError_t t_rows(const void* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
-                         const void* zeros, int64_t n, int g, const TPlan& p, bool exact, float* part, hipStream_t st) {
+                         const void* zeros, int64_t n, int g, const TPlan& p, float* part, hipStream_t st) {
   const TX* d = (const TX*)dy;
   constexpr int PW = sizeof(TS) == 2 ? 2 : 3;
-  if (exact) return t_rows_go<TX, TS, PW, 1>(d, m, k, packed, scales, zeros, n, g, p, part, st);
+  if (p.pw > 1) return t_rows_go<TX, TS, PW, 1>(d, m, k, packed, scales, zeros, n, g, p, part, st);
   if constexpr (sizeof(TX) == 2) {
     if (p.mb == 1) return t_rows_go<TX, TS, 1, 1>(d, m, k, packed, scales, zeros, n, g, p, part, st);
     return t_rows_go<TX, TS, 1, 2>(d, m, k, packed, scales, zeros, n, g, p, part, st);
@@ -248,16 +265,22 @@ static hipError_t t_rows(const void* dy, int64_t m, int64_t k, const uint8_t* pa
 hipError_t launch_w4a16_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
                           const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* dx,
                           int dx_dtype, const LoraOut& lo, void* ws, hipStream_t st) {
-  const bool exact = t_exact(dy_dtype, dx_dtype);
-  const TPlan p = t_plan(m, k, n, exact);
+  const TPlan p = t_plan(m, k, n, dy_dtype, sz_dtype, dx_dtype);
   float* part = (float*)ws;
   hipError_t e;
-  if (dy_dtype == W4_F32)
-    e = sz_dtype == W4_F16 ? t_rows<float, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st)
-                           : t_rows<float, float>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st);
-  else
-    e = sz_dtype == W4_F16 ? t_rows<uint16_t, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st)
-                           : t_rows<uint16_t, float>(dy, m, k, packed, scales, zeros, n, g, p, exact, part, st);
+  if (p.tiles) {
+    const bool whole = p.parts == 1;  // dx itself, adapters and all
+    const LoraOut none{};
+    e = launch_w4a16_t_gemm(dy, m, k, packed, scales, zeros, sz_dtype, n, g, whole ? dx : ws,
+                            whole ? dx_dtype : (int)W4_F32, whole ? lo : none, p.mi, p.pw, (int)p.parts, (int)p.steps, st);
+    if (whole || e != hipSuccess) return e;
+  } else if (dy_dtype == W4_F32) {
+    e = sz_dtype == W4_F16 ? t_rows<float, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, part, st)
+                           : t_rows<float, float>(dy, m, k, packed, scales, zeros, n, g, p, part, st);
+  } else {
+    e = sz_dtype == W4_F16 ? t_rows<uint16_t, _Float16>(dy, m, k, packed, scales, zeros, n, g, p, part, st)
+                           : t_rows<uint16_t, float>(dy, m, k, packed, scales, zeros, n, g, p, part, st);
+  }
   if (e != hipSuccess) return e;
   const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
                     (int)lo.count, lo.rank, lo.dtype == W4_F32};

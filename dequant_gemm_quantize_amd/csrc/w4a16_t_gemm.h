@@ -1,0 +1,415 @@
+// Product with the transposed INT4 weight for many rows of bf16 dy:
+//   dx[m, k] = sum_n dy[m, n] (q[n, k] - zp[n, j]) s[n, j]  (+ sum_r low[m, r] A[l(m), r, k])
+// on v_mfma_f32_32x32x16_bf16 with float32 accumulation.
+//
+// The sum runs over weight rows, and a word of codes holds eight columns of one
+// row, so a tile of the weight is turned around on its way to the matrix cores: a thread
+// takes the same eight columns of four rows, makes weights of them, and stores four rows of each
+// column as one 8-byte piece of a row of the operand tile in LDS.  Codes are
+// converted once a workgroup.  The pairs that v_cvt_pk_bf16_f32 makes are two rows
+// of one column, so turning costs no instruction of its own.
+//
+// Workgroup tile 128 MI x 128 of eight waves, each 32 MI x 64 of it, 64 weight rows a step.
+// dy, codes, scales and zero-points go from memory to LDS directly.  Step t's MFMAs run while step t + 1 is converted
+// and the loads of steps behind it are under way: one barrier a step.
+//
+// PW bf16 parts of a weight, each a tile of its own: one (rounded: bf16 dx), two
+// (exact with fp16 scales: 15 bits) or three (float32 scales).
+#pragma once
+
+#include <type_traits>
+
+#include "lds_gemm.h"
+#include "lora.h"
+#include "w4_common.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kTgN = 128;   // columns of dx a tile
+constexpr int kTgB = 64;    // weight rows a step
+constexpr int kTgRaw = 4;   // stages of codes
+
+template <int MI_, int PW_, int SUBS_> struct TgTile {
+  static constexpr int MI = MI_, PW = PW_, SUBS = SUBS_;
+  static constexpr int BM = 128 * MI;  // eight waves, four by two of 32 MI x 64
+  static constexpr int AS = PW * MI <= 2 ? 3 : 2;               // stages of dy
+  static constexpr int A_STAGE = BM * 128, B_PART = kTgN * 128;  // bytes
+  static constexpr int RAW_STAGE = kTgB * kTgN / 2, TAB_STAGE = (SUBS > 1 ? 8 : 2) * kTgB * 4;
+  static constexpr int B_AT = AS * A_STAGE, RAW_AT = B_AT + 2 * PW * B_PART, TAB_AT = RAW_AT + kTgRaw * RAW_STAGE;
+  static constexpr int SPARE_AT = TAB_AT + kTgRaw * TAB_STAGE;
+  static constexpr size_t lds = SPARE_AT + 1024;
+  static constexpr int LS = SUBS > 1 ? 2 : 1;  // loads of codes and scales a wave and step
+};
+
+// Slot (16 bytes) of chunk c (0 .. 3) of row n of a stage of codes: the 16 lanes
+// that read one chunk of rows 4 b + i, b = 0 .. 15, meet every bank twice, the least there is.
+__device__ __forceinline__ int raw_row(int slot) {  // the row that a slot has
+  const int p = slot >> 2;
+  return (p & ~7) | ((p & 1) << 2) | ((p >> 1) & 3);
+}
+__device__ __forceinline__ int raw_slot(int n, int c) {
+  const int p = (n & ~7) | ((n >> 2) & 1) | ((n & 3) << 1);
+  return 4 * p + (c ^ ((n >> 3) & 3));
+}
+
+// acc += low A for the wave's 32 MI rows from m0 (those before mend) and 64
+// columns from n, segment by segment: rows of other segments are zero in the operand.
+template <int MI>
+__device__ __forceinline__ void add_adapters_t(const Adapters& ad, int lane, f32x16 (&acc)[MI][2], int64_t K,
+                                               int64_t m0, int64_t mend, int64_t k0) {
+  const int r = lane & 31, h = lane >> 5;
+  const int64_t top = mend < m0 + 32 * MI ? mend : m0 + 32 * MI;
+  for (int s = segments_before(ad.offsets, ad.segments, m0, lane); s < ad.segments; ++s) {
+    const int64_t lo = ad.offsets[s] > m0 ? ad.offsets[s] : m0, hi = ad.offsets[s + 1] < top ? ad.offsets[s + 1] : top;
+    if (lo >= top) break;
+    const int l = ad.which[s];
+    if (l < 0 || l >= ad.count || lo >= hi) continue;
+    for (int r0 = 0; r0 < ad.rank; r0 += 16) {
+      const bool in = r0 + 8 * h < ad.rank;
+      bf16x8 w[2][3];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t k = k0 + 32 * j + r;
+        const bool real = in && k < K;
+        const int64_t at = ((int64_t)l * ad.rank + r0 + 8 * h) * K + k;
+        w[j][0] = w[j][1] = w[j][2] = zero8();
+        if (ad.wide) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = real ? ((const float*)ad.out)[at + i * K] : 0.0f;
+          pack8(v, w[j]);
+        } else {
+          uint16_t v[8];
+          bf16x8 one[1];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = real ? ((const uint16_t*)ad.out)[at + i * K] : (uint16_t)0;
+          pack8(v, one);
+          w[j][0] = one[0];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int64_t m = m0 + 32 * i + r;
+        if (m0 + 32 * i >= hi || m0 + 32 * i + 32 <= lo) continue;  // the same in every lane
+        bf16x8 a[3] = {zero8(), zero8(), zero8()};
+        if (in && m >= lo && m < hi) load8(ad.low + m * ad.rank + r0 + 8 * h, a);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][0], a[p], acc[i][j], 0, 0, 0);
+            if (ad.wide) {
+#pragma unroll
+              for (int q = 1; q + p < 3; ++q)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][q], a[p], acc[i][j], 0, 0, 0);
+            }
+          }
+      }
+    }
+  }
+}
+
+// The order of a slice's instructions: the next slice's reads first, then MFMAs
+// with the conversions between them, six vector instructions (of 4 cycles) to an MFMA of 32.
+template <typename T>
+__device__ __forceinline__ void slice_order() {
+  constexpr int M = 2 * T::MI * T::PW;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (i % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+}  // namespace
+
+// Steps first .. first + steps - 1 of 64 weight rows are part blockIdx.y's; with
+// parts its float32 sums go to y + blockIdx.y * M * K (TY float), without
+// adapters, else dx to y.  SUBS: scale columns of a tile, 1 (groups of a multiple of 128) or 4.
+template <typename T, typename TS, typename TY>
+__global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
+    const uint16_t* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
+    const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, Adapters ad,
+    TY* __restrict__ y, uint32_t tiles_m, uint32_t tiles_n) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
+  constexpr int MI = T::MI, BM = T::BM, PW = T::PW, AS = T::AS, SUBS = T::SUBS;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t t, tm, tn;
+  int whole;
+  if (!xcd_tile<32, false>(tiles_m * tiles_n, t, whole)) return;
+  band(t, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)BM * tm, k0 = (int64_t)kTgN * tn;
+  const uint32_t half = (uint32_t)(K / 2), ng = (uint32_t)(K / g), drow = (uint32_t)(2 * N);
+  const int all = (int)((N + kTgB - 1) / kTgB), first = (int)blockIdx.y * steps;
+  const int nst = all - first < steps ? all - first : steps;  // steps of this part
+
+  // dy -> LDS: 8 rows x 128 bytes a load; slot s of row r holds chunk s ^ ((r / 2) % 8)
+  constexpr int LA = BM / 64;
+  const uint32_t mrows = (uint32_t)(M - m0 < BM ? M - m0 : BM);
+  const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(dy + m0 * N), mrows * drow);
+  uint32_t ao[LA];
+  const int lrow = lane >> 3, slot = lane & 7;
+#pragma unroll
+  for (int i = 0; i < LA; ++i) {
+    const int row = 8 * (w * LA + i) + lrow;
+    ao[i] = (uint32_t)row * drow + 16u * (slot ^ ((row >> 1) & 7));
+  }
+  // quarters q0 .. q1 - 1 of a step's loads
+  auto a_issue = [&](int st, int q0, int q1) {
+    const uint32_t n0 = st < nst ? (uint32_t)(first + st) * kTgB : (uint32_t)N;
+    const uint32_t left = (uint32_t)N - n0, o = 2 * n0;
+    uint8_t* dst = sm + (st % AS) * T::A_STAGE;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      if (i < q0 * LA / 4 || i >= q1 * LA / 4) continue;
+      const int row = 8 * (w * LA + i) + lrow;
+      const uint32_t n = 8 * (slot ^ ((row >> 1) & 7));  // the chunk's first row of the step
+      load_lds(ar, dst + 1024 * (w * LA + i), n < left ? ao[i] + o : kPastEnd);
+    }
+  };
+  // Codes, scales and zero-points -> LDS.  Codes: 16 bytes a lane of waves 0 to 3.
+  // Scales: for each of 64 rows the 4 bytes that hold the value of the tile's
+  // group (with fp16 two values, of which the value's number in the array, odd
+  // or even, says which; N % 8 == 0, so no word lies across the array's end).  SUBS 1:
+  // wave 4 loads scales, 5 zero-points; SUBS 4: wave 4 + i those of columns
+  // 32 i .. 32 i + 31.  Waves with fewer loads than others load nothing (past the
+  // end) to a place of their own, so that all have the same number under way.
+  const int rs = 64 * (w & 3) + lane, rn = raw_row(rs), rc = (rs & 3) ^ ((rn >> 3) & 3);
+  const bool rin = k0 / 2 + 16 * rc < half;
+  const uint32_t ro = rin ? (uint32_t)rn * half + (uint32_t)(k0 / 2) + 16u * rc : kPastEnd;
+  const int sub = SUBS > 1 ? w & 3 : 0;
+  const int64_t kc = k0 + 32 * sub;
+  const uint32_t gi = (uint32_t)((kc < K ? kc : K - 1) / g);
+  const uint32_t so = ((uint32_t)lane * ng + gi) * (uint32_t)sizeof(TS) & ~3u;
+  auto w_issue = [&](int st) {
+    const int64_t n0 = (int64_t)(first + st) * kTgB;
+    const int64_t have = st < nst ? (N - n0 < kTgB ? N - n0 : kTgB) : 0;
+    const int64_t at = st < nst ? n0 : 0;
+    uint8_t* tab = sm + T::TAB_AT + (st % kTgRaw) * T::TAB_STAGE;
+    if (w < 4) {
+      const __amdgpu_buffer_rsrc_t r = buf_rsrc_n(uniform_ptr(packed + at * half), (uint32_t)have * half);
+      load_lds(r, sm + T::RAW_AT + (st % kTgRaw) * T::RAW_STAGE + 1024 * w, ro);
+      if constexpr (SUBS > 1) load_lds4(r, sm + T::SPARE_AT + 256 * w, kPastEnd);
+    } else {
+      const uint32_t bytes = (uint32_t)have * ng * (uint32_t)sizeof(TS);
+      const __amdgpu_buffer_rsrc_t s = buf_rsrc_n(uniform_ptr((const char*)scales + at * ng * sizeof(TS)), bytes);
+      const __amdgpu_buffer_rsrc_t z = buf_rsrc_n(uniform_ptr((const char*)zeros + at * ng * sizeof(TS)), bytes);
+      if constexpr (SUBS > 1) {
+        load_lds4(s, tab + 256 * (w - 4), so);
+        load_lds4(z, tab + 1024 + 256 * (w - 4), so);
+      } else {
+        load_lds4(w == 4 ? s : z, w < 6 ? tab + 256 * (w - 4) : sm + T::SPARE_AT + 256 * (w - 4), w < 6 ? so : kPastEnd);
+      }
+    }
+  };
+
+  // the thread's piece: columns 8 kb + 4 up .. 8 kb + 4 up + 3 of weight rows 4 b .. 4 b + 3
+  const int b = lane & 15, kb = 4 * (w & 3) + (lane >> 4), up = w >> 2;
+  int rawo[4], bo[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rawo[i] = T::RAW_AT + 16 * raw_slot(4 * b + i, w & 3) + 4 * (kb & 3);
+  // row n of the operand tile has its chunk of rows 8 (b / 2) .. at slot (b / 2) ^ ((n / 2) % 8)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = 8 * kb + 4 * up + 2 * i;
+    bo[i] = T::B_AT + 128 * n + 16 * ((b >> 1) ^ ((n >> 1) & 7)) + 8 * (b & 1);
+  }
+  const int tabo = T::TAB_AT + 256 * sub + 16 * b;
+  uint32_t p[4];
+  u32x4 cs, cz;
+  int odd[4];  // 16 where the value is the upper half of its word
+#pragma unroll
+  for (int i = 0; i < 4; ++i) odd[i] = sizeof(TS) == 2 ? (int)((gi + i * ng) & 1) * 16 : 0;
+  auto c_read = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *(const uint32_t*)(sm + rawo[i] + (st % kTgRaw) * T::RAW_STAGE);
+    const uint8_t* tb = sm + tabo + (st % kTgRaw) * T::TAB_STAGE;
+    cs = *(const u32x4*)tb, cz = *(const u32x4*)(tb + (SUBS > 1 ? 1024 : 256));
+  };
+  uint32_t lo[4], hi[4];
+  float s[4], z[4];  // z: -zp s, or zp where weights keep their bits
+  auto value = [&](uint32_t word, int i) {
+    if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)(word >> odd[i]));
+    else return __uint_as_float(word);
+  };
+  auto c_mask = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = value(cs[i], i), z[i] = value(cz[i], i);
+      if constexpr (PW == 1) z[i] *= -s[i];
+      const uint32_t c = p[i] >> (16 * up);  // the piece's four codes
+      lo[i] = c & 0x0f0fu;
+      hi[i] = (c >> 4) & 0x0f0fu;
+      asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one
+    }
+  };
+  // columns J0 .. J1 - 1 of the piece
+  auto convert = [&](int st, auto j0, auto j1) {
+    uint8_t* out = sm + (st & 1) * PW * T::B_PART;
+#pragma unroll
+    for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float q = (float)(uint8_t)((j & 1 ? hi[i] : lo[i]) >> (8 * (j >> 1)));
+        v[i] = PW == 1 ? fmaf(q, s[i], z[i]) : (q - z[i]) * s[i];
+      }
+      uint8_t* at = out + bo[j >> 1] + 128 * (j & 1);
+      if constexpr (PW == 1) {
+        u32x2 d;
+        d.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
+        d.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
+        *(u32x2*)at = d;
+      } else {
+#pragma unroll
+        for (int q = 0; q < PW; ++q) {
+          u32x2 d;
+          d.x = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
+          d.y = __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u);
+          *(u32x2*)(at + q * T::B_PART) = d;
+          if (q + 1 < PW) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+          }
+        }
+      }
+    }
+  };
+
+  f32x16 acc[MI][2];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  const int r = lane & 31, h = lane >> 5, swz = (r >> 1) & 7;
+  const int wm = w >> 1, wn = w & 1;
+  // Slice q of a step: 16 weight rows, 8 a half.  The operands of a slice are read under the MFMAs of the one before.
+  int fa[4], fb[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    fa[q] = 128 * (32 * MI * wm + r) + 16 * ((2 * q + h) ^ swz);
+    fb[q] = T::B_AT + 128 * (64 * wn + r) + 16 * ((2 * q + h) ^ swz);
+  }
+  bf16x8 av[2][MI], bv[2][PW][2];
+  auto frag = [&](int st, auto qc) {
+    constexpr int q = decltype(qc)::value;
+    const uint8_t* a = sm + fa[q] + (st % AS) * T::A_STAGE;
+    const uint8_t* bt = sm + fb[q] + (st & 1) * PW * T::B_PART;
+#pragma unroll
+    for (int p = 0; p < PW; ++p)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) bv[q & 1][p][j] = *(const bf16x8*)(bt + p * T::B_PART + 128 * 32 * j);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) av[q & 1][i] = *(const bf16x8*)(a + 128 * 32 * i);
+  };
+  auto mma = [&](auto qc) {
+    constexpr int q = decltype(qc)::value;
+#pragma unroll
+    for (int p = 0; p < PW; ++p)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[q & 1][p][j], av[q & 1][i], acc[i][j], 0, 0, 0);
+  };
+  constexpr std::integral_constant<int, 0> n0{};
+  constexpr std::integral_constant<int, 1> n1{};
+  constexpr std::integral_constant<int, 2> n2{};
+  constexpr std::integral_constant<int, 3> n3{};
+  constexpr std::integral_constant<int, 4> n4{};
+
+  // what step 0 needs, and the loads of the steps behind it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w_issue(i);
+    if (i < 2) a_issue(i, 0, 4);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  c_read(0);
+  c_mask();
+  convert(0, n0, n4);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  w_issue(4);
+  if constexpr (AS == 3) a_issue(2, 0, 1);
+  frag(0, n0);
+  c_read(1);
+  c_mask();
+
+  // Step t multiplies with the weights of t while those of t + 1 are made.  Before the
+  // last slice every wave has read all of the step's operands, written its
+  // part of the next step's weights and waited for its share of the loads that the
+  // next step reads; behind the barrier all that is whole and the step's places are free.
+  // With three stages the loads of dy are spread over the slices: eight at once
+  // held the wave's MFMAs up (2048 x 11008 x 4096 217 us).
+  for (int st = 0; st < nst; ++st) {
+    frag(st, n1);
+    if constexpr (AS == 3) a_issue(st + 2, 1, 2);
+    convert(st + 1, n0, n1);
+    mma(n0);
+    slice_order<T>();
+    frag(st, n2);
+    if constexpr (AS == 3) a_issue(st + 2, 2, 3);
+    convert(st + 1, n1, n2);
+    mma(n1);
+    slice_order<T>();
+    frag(st, n3);
+    if constexpr (AS == 3) a_issue(st + 2, 3, 4);
+    convert(st + 1, n2, n4);
+    mma(n2);
+    slice_order<T>();
+    // all but the loads that were issued behind the last barrier; with two stages of dy those too
+    if constexpr (AS == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + T::LS) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    w_issue(st + 5);
+    a_issue(st + AS, 0, AS == 3 ? 1 : 4);
+    frag(st + 1, n0);
+    c_read(st + 2);
+    c_mask();
+    mma(n3);
+    slice_order<T>();
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  const int64_t mw = m0 + 32 * MI * wm, kw = k0 + 64 * wn;
+  if (ad.count > 0) add_adapters_t<MI>(ad, lane, acc, K, mw, M, kw);
+  constexpr int TURN = turn_bytes<TY, 2>();
+  static_assert(8 * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
+  turn_store<TY, MI, 2, true>(sm + w * TURN, lane, acc, y + (int64_t)blockIdx.y * M * K, K, mw, M, kw);
+}
+
+template <int MI, int PW, int SUBS, typename TS, typename TY>
+static hipError_t tg_go(const uint16_t* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                        const void* zeros, int64_t n, int g, int parts, int steps, const Adapters& ad, TY* y,
+                        hipStream_t st) {
+  typedef TgTile<MI, PW, SUBS> T;
+  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
+  const hipError_t e = once_per_device(attr_done, [] {
+    return hipFuncSetAttribute((const void*)k_w4a16_t_gemm<T, TS, TY>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)T::lds);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t tiles_m = (m + T::BM - 1) / T::BM, tiles_n = (k + kTgN - 1) / kTgN;
+  const dim3 grid((unsigned)xcd_grid<32, false>(tiles_m * tiles_n), (unsigned)parts);
+  k_w4a16_t_gemm<T, TS, TY><<<grid, 512, T::lds, st>>>(dy, m, n, packed, scales, zeros, k, g, steps, ad, y,
+                                                      (uint32_t)tiles_m, (uint32_t)tiles_n);
+  return hipGetLastError();
+}
+
+}  // namespace w4
