@@ -17,6 +17,12 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
 }
 
+// The same with a part of the offset that is the same in every lane; the range is that of the lane's part alone.
+__device__ __forceinline__ void load_lds_at(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off, uint32_t all) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, (int)off, (int)all, 0,
+                                           0);
+}
+
 // The same with 4 bytes a lane, to dst + 4 lane.
 __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 4, (int)off, 0, 0, 0);

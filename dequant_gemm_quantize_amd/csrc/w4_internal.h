@@ -177,7 +177,7 @@ size_t w4a16_t_workspace_bytes(int64_t m, int64_t k, int64_t n, int g, int dy_dt
 hipError_t launch_w4a16_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
                           const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* dx,
                           int dx_dtype, const LoraOut& lo, void* ws, hipStream_t st);
-// The same in tiles of 128 mi rows, for bf16 dy: pw bf16 parts of a weight (1; 2
+// The same in tiles of 64 mi rows, for bf16 dy: pw bf16 parts of a weight (1; 2
 // with fp16 scales or 3 with float32 ones for float32 dx); with parts > 1 float32 partial sums, without adapters.
 hipError_t launch_w4a16_t_gemm(const void* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                                const void* zeros, int sz_dtype, int64_t n, int g, void* dx, int dx_dtype,

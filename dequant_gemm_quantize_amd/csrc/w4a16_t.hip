@@ -35,7 +35,7 @@ __device__ __forceinline__ float t_scale(const void* p, int64_t i) {
 // how it splits N: parts of `steps` steps of 64 or 32 weight rows.
 struct TPlan {
   bool tiles;
-  int mi, pw;          // tiles of 128 mi rows; bf16 parts of a weight
+  int mi, pw;          // tiles of 64 mi rows; bf16 parts of a weight
   int mb;              // blocks of 16 rows a workgroup of k_w4a16_t_rows
   int64_t rows, strips, parts, steps;
 };
@@ -48,9 +48,9 @@ TPlan t_plan(int64_t m, int64_t k, int64_t n, int dy_dtype, int sz_dtype, int dx
   p.tiles = dy_dtype == W4_BF16 && m > 32 && n % 8 == 0 && n <= ((int64_t)1 << 21);
   int64_t parts, all;
   if (p.tiles) {
-    p.mi = p.pw == 3 || m <= 128 ? 1 : 2;
+    p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
     p.mb = 0;
-    p.rows = (m + 128 * p.mi - 1) / (128 * p.mi);
+    p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
     p.strips = (k + 127) / 128;
     all = (n + 63) / 64;
     parts = 256 / (p.rows * p.strips);

@@ -9,7 +9,8 @@
 // converted once a workgroup.  The pairs that v_cvt_pk_bf16_f32 makes are two rows
 // of one column, so turning costs no instruction of its own.
 //
-// Workgroup tile 128 MI x 128 of eight waves, each 32 MI x 64 of it, 64 weight rows a step.
+// Workgroup tile 64 MI x 128, 64 weight rows a step.  Four waves multiply, each 32 MI x 64
+// of the tile, and four load and convert, one of each on every SIMD.
 // dy, codes, scales and zero-points go from memory to LDS directly.  Step t's MFMAs run while step t + 1 is converted
 // and the loads of steps behind it are under way: one barrier a step.
 //
@@ -30,18 +31,16 @@ namespace {
 
 constexpr int kTgN = 128;   // columns of dx a tile
 constexpr int kTgB = 64;    // weight rows a step
-constexpr int kTgRaw = 4;   // stages of codes
 
 template <int MI_, int PW_, int SUBS_> struct TgTile {
   static constexpr int MI = MI_, PW = PW_, SUBS = SUBS_;
-  static constexpr int BM = 128 * MI;  // eight waves, four by two of 32 MI x 64
-  static constexpr int AS = PW * MI <= 2 ? 3 : 2;               // stages of dy
-  static constexpr int A_STAGE = BM * 128, B_PART = kTgN * 128;  // bytes
-  static constexpr int RAW_STAGE = kTgB * kTgN / 2, TAB_STAGE = (SUBS > 1 ? 8 : 2) * kTgB * 4;
-  static constexpr int B_AT = AS * A_STAGE, RAW_AT = B_AT + 2 * PW * B_PART, TAB_AT = RAW_AT + kTgRaw * RAW_STAGE;
-  static constexpr int SPARE_AT = TAB_AT + kTgRaw * TAB_STAGE;
-  static constexpr size_t lds = SPARE_AT + 1024;
-  static constexpr int LS = SUBS > 1 ? 2 : 1;  // loads of codes and scales a wave and step
+  static constexpr int BM = 64 * MI;  // four multiplying waves, two by two of 32 MI x 64
+  static constexpr int AS = MI * PW <= 4 ? 3 : 2;  // stages of dy: what fits in 160 KB
+  // bytes of a stage: dy (AS of them), weights (two), codes, and scales with zero-points (three)
+  static constexpr int A_STAGE = BM * 128, B_PART = kTgN * 128, B_STAGE = PW * B_PART;
+  static constexpr int RAW_STAGE = kTgB * kTgN / 2, TAB_STAGE = SUBS * 2 * kTgB * 4;
+  static constexpr int B_AT = AS * A_STAGE, RAW_AT = B_AT + 2 * B_STAGE, TAB_AT = RAW_AT + 3 * RAW_STAGE;
+  static constexpr size_t lds = TAB_AT + 3 * TAB_STAGE;
 };
 
 // Slot (16 bytes) of chunk c (0 .. 3) of row n of a stage of codes: the 16 lanes
@@ -112,18 +111,14 @@ __device__ __forceinline__ void add_adapters_t(const Adapters& ad, int lane, f32
   }
 }
 
-// The order of a slice's instructions: the next slice's reads first, then MFMAs
-// with the conversions between them, six vector instructions (of 4 cycles) to an MFMA of 32.
+// The order of a slice's instructions: the next slice's reads under the first MFMAs.
 template <typename T>
 __device__ __forceinline__ void slice_order() {
-  constexpr int M = 2 * T::MI * T::PW;
+  constexpr int M = 2 * T::MI * T::PW, R = T::MI + 2 * T::PW;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if (i % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
-    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+    if (i < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
 }
@@ -139,7 +134,7 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
     const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, Adapters ad,
     TY* __restrict__ y, uint32_t tiles_m, uint32_t tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
-  constexpr int MI = T::MI, BM = T::BM, PW = T::PW, AS = T::AS, SUBS = T::SUBS;
+  constexpr int MI = T::MI, BM = T::BM, PW = T::PW, SUBS = T::SUBS;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t t, tm, tn;
@@ -151,138 +146,177 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
   const int all = (int)((N + kTgB - 1) / kTgB), first = (int)blockIdx.y * steps;
   const int nst = all - first < steps ? all - first : steps;  // steps of this part
 
-  // dy -> LDS: 8 rows x 128 bytes a load; slot s of row r holds chunk s ^ ((r / 2) % 8)
-  constexpr int LA = BM / 64;
-  const uint32_t mrows = (uint32_t)(M - m0 < BM ? M - m0 : BM);
-  const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(dy + m0 * N), mrows * drow);
-  uint32_t ao[LA];
-  const int lrow = lane >> 3, slot = lane & 7;
-#pragma unroll
-  for (int i = 0; i < LA; ++i) {
-    const int row = 8 * (w * LA + i) + lrow;
-    ao[i] = (uint32_t)row * drow + 16u * (slot ^ ((row >> 1) & 7));
-  }
-  // quarters q0 .. q1 - 1 of a step's loads
-  auto a_issue = [&](int st, int q0, int q1) {
-    const uint32_t n0 = st < nst ? (uint32_t)(first + st) * kTgB : (uint32_t)N;
-    const uint32_t left = (uint32_t)N - n0, o = 2 * n0;
-    uint8_t* dst = sm + (st % AS) * T::A_STAGE;
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      if (i < q0 * LA / 4 || i >= q1 * LA / 4) continue;
-      const int row = 8 * (w * LA + i) + lrow;
-      const uint32_t n = 8 * (slot ^ ((row >> 1) & 7));  // the chunk's first row of the step
-      load_lds(ar, dst + 1024 * (w * LA + i), n < left ? ao[i] + o : kPastEnd);
-    }
+  constexpr std::integral_constant<int, 0> n0{};
+  constexpr std::integral_constant<int, 1> n1{};
+  constexpr std::integral_constant<int, 2> n2{};
+  constexpr std::integral_constant<int, 3> n3{};
+  constexpr std::integral_constant<int, 4> n4{};
+  constexpr std::integral_constant<int, 5> n5{};
+  auto barrier = [&]() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
-  // Codes, scales and zero-points -> LDS.  Codes: 16 bytes a lane of waves 0 to 3.
-  // Scales: for each of 64 rows the 4 bytes that hold the value of the tile's
-  // group (with fp16 two values, of which the value's number in the array, odd
-  // or even, says which; N % 8 == 0, so no word lies across the array's end).  SUBS 1:
-  // wave 4 loads scales, 5 zero-points; SUBS 4: wave 4 + i those of columns
-  // 32 i .. 32 i + 31.  Waves with fewer loads than others load nothing (past the
-  // end) to a place of their own, so that all have the same number under way.
-  const int rs = 64 * (w & 3) + lane, rn = raw_row(rs), rc = (rs & 3) ^ ((rn >> 3) & 3);
-  const bool rin = k0 / 2 + 16 * rc < half;
-  const uint32_t ro = rin ? (uint32_t)rn * half + (uint32_t)(k0 / 2) + 16u * rc : kPastEnd;
-  const int sub = SUBS > 1 ? w & 3 : 0;
-  const int64_t kc = k0 + 32 * sub;
-  const uint32_t gi = (uint32_t)((kc < K ? kc : K - 1) / g);
-  const uint32_t so = ((uint32_t)lane * ng + gi) * (uint32_t)sizeof(TS) & ~3u;
-  auto w_issue = [&](int st) {
-    const int64_t n0 = (int64_t)(first + st) * kTgB;
-    const int64_t have = st < nst ? (N - n0 < kTgB ? N - n0 : kTgB) : 0;
-    const int64_t at = st < nst ? n0 : 0;
-    uint8_t* tab = sm + T::TAB_AT + (st % kTgRaw) * T::TAB_STAGE;
-    if (w < 4) {
-      const __amdgpu_buffer_rsrc_t r = buf_rsrc_n(uniform_ptr(packed + at * half), (uint32_t)have * half);
-      load_lds(r, sm + T::RAW_AT + (st % kTgRaw) * T::RAW_STAGE + 1024 * w, ro);
-      if constexpr (SUBS > 1) load_lds4(r, sm + T::SPARE_AT + 256 * w, kPastEnd);
-    } else {
-      const uint32_t bytes = (uint32_t)have * ng * (uint32_t)sizeof(TS);
-      const __amdgpu_buffer_rsrc_t s = buf_rsrc_n(uniform_ptr((const char*)scales + at * ng * sizeof(TS)), bytes);
-      const __amdgpu_buffer_rsrc_t z = buf_rsrc_n(uniform_ptr((const char*)zeros + at * ng * sizeof(TS)), bytes);
-      if constexpr (SUBS > 1) {
-        load_lds4(s, tab + 256 * (w - 4), so);
-        load_lds4(z, tab + 1024 + 256 * (w - 4), so);
-      } else {
-        load_lds4(w == 4 ? s : z, w < 6 ? tab + 256 * (w - 4) : sm + T::SPARE_AT + 256 * (w - 4), w < 6 ? so : kPastEnd);
-      }
+  // step(number) for every step, the numbers counted modulo 6, the period of two and three stages
+  auto all_steps = [&](auto step) {
+    for (int st = 0;;) {
+      step(st, n0);
+      if (++st >= nst) break;
+      step(st, n1);
+      if (++st >= nst) break;
+      step(st, n2);
+      if (++st >= nst) break;
+      step(st, n3);
+      if (++st >= nst) break;
+      step(st, n4);
+      if (++st >= nst) break;
+      step(st, n5);
+      if (++st >= nst) break;
     }
   };
 
-  // the thread's piece: columns 8 kb + 4 up .. 8 kb + 4 up + 3 of weight rows 4 b .. 4 b + 3
-  const int b = lane & 15, kb = 4 * (w & 3) + (lane >> 4), up = w >> 2;
-  int rawo[4], bo[2];
+  // Waves 4 to 7 load and convert, waves 0 to 3 multiply.  Barrier t, before which
+  // the operands of step t have all been read, and those of t + 1 are whole, is passed by all.
+  if (w >= 4) {
+    const int pw = w - 4;
+    // dy -> LDS: 8 rows x 128 bytes a load; slot s of row r holds chunk s ^ ((r / 2) % 8)
+    constexpr int LA = BM / 32;
+    const uint32_t mrows = (uint32_t)(M - m0 < BM ? M - m0 : BM);
+    const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(dy + m0 * N), mrows * drow);
+    uint32_t ao[LA];
+    const int lrow = lane >> 3, slot = lane & 7;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) rawo[i] = T::RAW_AT + 16 * raw_slot(4 * b + i, w & 3) + 4 * (kb & 3);
-  // row n of the operand tile has its chunk of rows 8 (b / 2) .. at slot (b / 2) ^ ((n / 2) % 8)
+    for (int i = 0; i < LA; ++i) {
+      const int row = 8 * (pw * LA + i) + lrow;
+      ao[i] = (uint32_t)row * drow + 16u * (slot ^ ((row >> 1) & 7));
+    }
+    auto a_issue = [&](int st, int stage) {
+      const uint32_t n0 = (uint32_t)(first + st) * kTgB;
+      uint8_t* dst = sm + stage * T::A_STAGE + 1024 * pw * LA;
+      if (st < nst && n0 + kTgB <= (uint32_t)N) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = 8 * kb + 4 * up + 2 * i;
-    bo[i] = T::B_AT + 128 * n + 16 * ((b >> 1) ^ ((n >> 1) & 7)) + 8 * (b & 1);
-  }
-  const int tabo = T::TAB_AT + 256 * sub + 16 * b;
-  uint32_t p[4];
-  u32x4 cs, cz;
-  int odd[4];  // 16 where the value is the upper half of its word
+        for (int i = 0; i < LA; ++i) load_lds_at(ar, dst + 1024 * i, ao[i], 2 * n0);
+      } else {  // the last weight rows, or none: chunks past them read as zero
+        const uint32_t left = st < nst ? (uint32_t)N - n0 : 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) odd[i] = sizeof(TS) == 2 ? (int)((gi + i * ng) & 1) * 16 : 0;
-  auto c_read = [&](int st) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *(const uint32_t*)(sm + rawo[i] + (st % kTgRaw) * T::RAW_STAGE);
-    const uint8_t* tb = sm + tabo + (st % kTgRaw) * T::TAB_STAGE;
-    cs = *(const u32x4*)tb, cz = *(const u32x4*)(tb + (SUBS > 1 ? 1024 : 256));
-  };
-  uint32_t lo[4], hi[4];
-  float s[4], z[4];  // z: -zp s, or zp where weights keep their bits
-  auto value = [&](uint32_t word, int i) {
-    if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)(word >> odd[i]));
-    else return __uint_as_float(word);
-  };
-  auto c_mask = [&]() {
+        for (int i = 0; i < LA; ++i) {
+          const int row = 8 * (pw * LA + i) + lrow;
+          load_lds(ar, dst + 1024 * i, 8u * (slot ^ ((row >> 1) & 7)) < left ? ao[i] + 2 * n0 : kPastEnd);
+        }
+      }
+    };
+    // Codes, scales and zero-points -> LDS.  Codes: 16 bytes a lane.  Scales: for each
+    // of 64 rows the 4 bytes that hold the value of the tile's group (with fp16 two
+    // values, of which the value's number in the array, odd or even, says which;
+    // N % 8 == 0, so no word lies across the array's end).  SUBS 1: the first of these waves
+    // loads scales, the second zero-points; SUBS 4: wave i those of columns 32 i .. 32 i + 31.
+    const int rs = 64 * pw + lane, rn = raw_row(rs), rc = (rs & 3) ^ ((rn >> 3) & 3);
+    const bool rin = k0 / 2 + 16 * rc < half;
+    const uint32_t ro = rin ? (uint32_t)rn * half + (uint32_t)(k0 / 2) + 16u * rc : kPastEnd;
+    const int64_t kc = k0 + (SUBS > 1 ? 32 * pw : 0);
+    const uint32_t gi = (uint32_t)((kc < K ? kc : K - 1) / g);
+    const uint32_t so = ((uint32_t)lane * ng + gi) * (uint32_t)sizeof(TS) & ~3u;
+    auto w_issue = [&](int st, int stage) {
+      const int64_t n0 = (int64_t)(first + st) * kTgB;
+      const int64_t have = st < nst ? (N - n0 < kTgB ? N - n0 : kTgB) : 0;
+      const int64_t at = st < nst ? n0 : 0;
+      load_lds(buf_rsrc_n(uniform_ptr(packed + at * half), (uint32_t)have * half),
+               sm + T::RAW_AT + stage * T::RAW_STAGE + 1024 * pw, ro);
+      uint8_t* tab = sm + T::TAB_AT + stage * T::TAB_STAGE + 512 * (SUBS > 1 ? pw : 0);
+      const uint32_t bytes = (uint32_t)have * ng * (uint32_t)sizeof(TS);
+      const int64_t byte = at * ng * (int64_t)sizeof(TS);
+      if (SUBS > 1 || pw == 0) load_lds4(buf_rsrc_n(uniform_ptr((const char*)scales + byte), bytes), tab, so);
+      if (SUBS > 1 || pw == 1) load_lds4(buf_rsrc_n(uniform_ptr((const char*)zeros + byte), bytes), tab + 256, so);
+    };
+
+    // the thread's piece: columns 8 kb .. 8 kb + 7 of weight rows 4 b .. 4 b + 3
+    const int b = lane & 15, kb = 4 * pw + (lane >> 4);
+    int rawo[4], bo[4], odd[4];  // odd: 16 where the scale is the upper half of its word
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[i] = value(cs[i], i), z[i] = value(cz[i], i);
-      if constexpr (PW == 1) z[i] *= -s[i];
-      const uint32_t c = p[i] >> (16 * up);  // the piece's four codes
-      lo[i] = c & 0x0f0fu;
-      hi[i] = (c >> 4) & 0x0f0fu;
-      asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one
+      rawo[i] = T::RAW_AT + 16 * raw_slot(4 * b + i, pw) + 4 * (kb & 3);
+      odd[i] = sizeof(TS) == 2 ? (int)((gi + i * ng) & 1) * 16 : 0;
+      // row n of the operand tile has its chunk of rows 8 (b / 2) .. at slot (b / 2) ^ ((n / 2) % 8)
+      bo[i] = T::B_AT + 128 * (8 * kb + 2 * i) + 16 * ((b >> 1) ^ ((4 * kb + i) & 7)) + 8 * (b & 1);
     }
-  };
-  // columns J0 .. J1 - 1 of the piece
-  auto convert = [&](int st, auto j0, auto j1) {
-    uint8_t* out = sm + (st & 1) * PW * T::B_PART;
-#pragma unroll
-    for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j) {
-      float v[4];
+    const int tabo = T::TAB_AT + (SUBS > 1 ? 512 * pw : 0) + 16 * b;
+    // the weights of a step, from codes of stage cs to operands of stage bs
+    auto convert = [&](int cs, int bs) {
+      uint32_t lo[4], hi[4];
+      float s[4], z[4];  // z: -zp s, or zp where weights keep their bits
+      const uint8_t* tb = sm + tabo + cs * T::TAB_STAGE;
+      const u32x4 sw = *(const u32x4*)tb, zw = *(const u32x4*)(tb + 256);
+      auto value = [&](uint32_t word, int i) {
+        if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)(word >> odd[i]));
+        else return __uint_as_float(word);
+      };
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float q = (float)(uint8_t)((j & 1 ? hi[i] : lo[i]) >> (8 * (j >> 1)));
-        v[i] = PW == 1 ? fmaf(q, s[i], z[i]) : (q - z[i]) * s[i];
+        const uint32_t p = *(const uint32_t*)(sm + rawo[i] + cs * T::RAW_STAGE);
+        s[i] = value(sw[i], i), z[i] = value(zw[i], i);
+        if constexpr (PW == 1) z[i] *= -s[i];
+        lo[i] = p & 0x0f0f0f0fu;
+        hi[i] = (p >> 4) & 0x0f0f0f0fu;
+        asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one
       }
-      uint8_t* at = out + bo[j >> 1] + 128 * (j & 1);
-      if constexpr (PW == 1) {
-        u32x2 d;
-        d.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
-        d.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
-        *(u32x2*)at = d;
-      } else {
+      uint8_t* out = sm + bs * T::B_STAGE;
 #pragma unroll
-        for (int q = 0; q < PW; ++q) {
+      for (int j = 0; j < 8; ++j) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float q = (float)(uint8_t)((j & 1 ? hi[i] : lo[i]) >> (8 * (j >> 1)));
+          v[i] = PW == 1 ? fmaf(q, s[i], z[i]) : (q - z[i]) * s[i];
+        }
+        uint8_t* at = out + bo[j >> 1] + 128 * (j & 1);
+        if constexpr (PW == 1) {
           u32x2 d;
-          d.x = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
-          d.y = __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u);
-          *(u32x2*)(at + q * T::B_PART) = d;
-          if (q + 1 < PW) {
+          d.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
+          d.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
+          *(u32x2*)at = d;
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+          for (int q = 0; q < PW; ++q) {
+            u32x2 d;
+            d.x = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
+            d.y = __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u);
+            *(u32x2*)(at + q * T::B_PART) = d;
+            if (q + 1 < PW) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+            }
           }
         }
       }
-    }
-  };
+    };
+
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w_issue(i, i);
+    a_issue(0, 0);
+    if constexpr (T::AS == 3) a_issue(1, 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    barrier();  // all four waves' codes and scales of step 0 are there
+    convert(0, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier();
+    // In step t the loads of dy of t + 2 (t + 1 with two stages) and of codes of t + 3
+    // are issued, into the places that step t - 1 has left, and the weights of t + 1 made.
+    // Loads come in from the L2 cache 1000 to 2000 cycles after their issue: with three stages they have two steps.
+    all_steps([&](int st, auto number) {
+      constexpr int k = decltype(number)::value;
+      w_issue(st + 3, k % 3);
+      a_issue(st + T::AS - 1, (k + T::AS - 1) % T::AS);
+      convert((k + 1) % 3, (k + 1) % 2);
+      // all but this step's loads; with two stages of dy, those too
+      if constexpr (T::AS == 2) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else if (SUBS > 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 3) : "memory");
+      else if (pw < 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 2) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 1) : "memory");
+      barrier();
+    });
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS when the sums are turned there
+    barrier();
+    return;
+  }
 
   f32x16 acc[MI][2];
 #pragma unroll
@@ -293,7 +327,8 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
   const int r = lane & 31, h = lane >> 5, swz = (r >> 1) & 7;
   const int wm = w >> 1, wn = w & 1;
-  // Slice q of a step: 16 weight rows, 8 a half.  The operands of a slice are read under the MFMAs of the one before.
+  // Slice q of a step: 16 weight rows, 8 a half.  The operands of a slice are read
+  // under the MFMAs of the one before, those of a step's first behind the barrier before the last slice.
   int fa[4], fb[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -301,10 +336,10 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
     fb[q] = T::B_AT + 128 * (64 * wn + r) + 16 * ((2 * q + h) ^ swz);
   }
   bf16x8 av[2][MI], bv[2][PW][2];
-  auto frag = [&](int st, auto qc) {
+  auto frag = [&](int as, int bs, auto qc) {
     constexpr int q = decltype(qc)::value;
-    const uint8_t* a = sm + fa[q] + (st % AS) * T::A_STAGE;
-    const uint8_t* bt = sm + fb[q] + (st & 1) * PW * T::B_PART;
+    const uint8_t* a = sm + fa[q] + as * T::A_STAGE;
+    const uint8_t* bt = sm + fb[q] + bs * T::B_STAGE;
 #pragma unroll
     for (int p = 0; p < PW; ++p)
 #pragma unroll
@@ -322,75 +357,32 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[q & 1][p][j], av[q & 1][i], acc[i][j], 0, 0, 0);
   };
-  constexpr std::integral_constant<int, 0> n0{};
-  constexpr std::integral_constant<int, 1> n1{};
-  constexpr std::integral_constant<int, 2> n2{};
-  constexpr std::integral_constant<int, 3> n3{};
-  constexpr std::integral_constant<int, 4> n4{};
-
-  // what step 0 needs, and the loads of the steps behind it
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w_issue(i);
-    if (i < 2) a_issue(i, 0, 4);
-  }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  c_read(0);
-  c_mask();
-  convert(0, n0, n4);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  w_issue(4);
-  if constexpr (AS == 3) a_issue(2, 0, 1);
-  frag(0, n0);
-  c_read(1);
-  c_mask();
-
-  // Step t multiplies with the weights of t while those of t + 1 are made.  Before the
-  // last slice every wave has read all of the step's operands, written its
-  // part of the next step's weights and waited for its share of the loads that the
-  // next step reads; behind the barrier all that is whole and the step's places are free.
-  // With three stages the loads of dy are spread over the slices: eight at once
-  // held the wave's MFMAs up (2048 x 11008 x 4096 217 us).
-  for (int st = 0; st < nst; ++st) {
-    frag(st, n1);
-    if constexpr (AS == 3) a_issue(st + 2, 1, 2);
-    convert(st + 1, n0, n1);
+  barrier();
+  barrier();
+  frag(0, 0, n0);
+  all_steps([&](int st, auto number) {
+    constexpr int k = decltype(number)::value, a = k % T::AS, e = k % 2;
+    frag(a, e, n1);
     mma(n0);
     slice_order<T>();
-    frag(st, n2);
-    if constexpr (AS == 3) a_issue(st + 2, 2, 3);
-    convert(st + 1, n1, n2);
+    frag(a, e, n2);
     mma(n1);
     slice_order<T>();
-    frag(st, n3);
-    if constexpr (AS == 3) a_issue(st + 2, 3, 4);
-    convert(st + 1, n2, n4);
+    frag(a, e, n3);
     mma(n2);
     slice_order<T>();
-    // all but the loads that were issued behind the last barrier; with two stages of dy those too
-    if constexpr (AS == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + T::LS) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    w_issue(st + 5);
-    a_issue(st + AS, 0, AS == 3 ? 1 : 4);
-    frag(st + 1, n0);
-    c_read(st + 2);
-    c_mask();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier();
+    frag((a + 1) % T::AS, 1 - e, n0);
     mma(n3);
     slice_order<T>();
-  }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup has left it
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  });
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  barrier();
   const int64_t mw = m0 + 32 * MI * wm, kw = k0 + 64 * wn;
   if (ad.count > 0) add_adapters_t<MI>(ad, lane, acc, K, mw, M, kw);
   constexpr int TURN = turn_bytes<TY, 2>();
-  static_assert(8 * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
+  static_assert(4 * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
   turn_store<TY, MI, 2, true>(sm + w * TURN, lane, acc, y + (int64_t)blockIdx.y * M * K, K, mw, M, kw);
 }
 

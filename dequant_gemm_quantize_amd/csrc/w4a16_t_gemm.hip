@@ -19,16 +19,16 @@ static hipError_t tg_types(const void* dy, int64_t m, int64_t k, const uint8_t* 
                            int steps, const Adapters& ad, hipStream_t st) {
   if (pw == 1) {
     if (dx_dtype == W4_F32)
-      return mi == 1 ? tg_subs<1, 1, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
-                     : tg_subs<2, 1, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
-    return mi == 1 ? tg_subs<1, 1, TS, __bf16>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
-                   : tg_subs<2, 1, TS, __bf16>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
+      return mi == 2 ? tg_subs<2, 1, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
+                     : tg_subs<4, 1, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
+    return mi == 2 ? tg_subs<2, 1, TS, __bf16>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
+                   : tg_subs<4, 1, TS, __bf16>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
   }
   if constexpr (sizeof(TS) == 2)
-    return mi == 1 ? tg_subs<1, 2, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
-                   : tg_subs<2, 2, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
+    return mi == 2 ? tg_subs<2, 2, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st)
+                   : tg_subs<4, 2, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
   else
-    return tg_subs<1, 3, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
+    return tg_subs<2, 3, TS, float>(dy, m, k, packed, scales, zeros, n, g, parts, steps, ad, dx, st);
 }
 
 hipError_t launch_w4a16_t_gemm(const void* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
