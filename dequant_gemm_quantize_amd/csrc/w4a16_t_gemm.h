@@ -189,20 +189,11 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
       const int row = 8 * (pw * LA + i) + lrow;
       ao[i] = (uint32_t)row * drow + 16u * (slot ^ ((row >> 1) & 7));
     }
-    auto a_issue = [&](int st, int stage) {
-      const uint32_t n0 = (uint32_t)(first + st) * kTgB;
-      uint8_t* dst = sm + stage * T::A_STAGE + 1024 * pw * LA;
-      if (st < nst && n0 + kTgB <= (uint32_t)N) {
-#pragma unroll
-        for (int i = 0; i < LA; ++i) load_lds_at(ar, dst + 1024 * i, ao[i], 2 * n0);
-      } else {  // the last weight rows, or none: chunks past them read as zero
-        const uint32_t left = st < nst ? (uint32_t)N - n0 : 0;
-#pragma unroll
-        for (int i = 0; i < LA; ++i) {
-          const int row = 8 * (pw * LA + i) + lrow;
-          load_lds(ar, dst + 1024 * i, 8u * (slot ^ ((row >> 1) & 7)) < left ? ao[i] + 2 * n0 : kPastEnd);
-        }
-      }
+    auto a_issue = [&](int st, int stage, int i) {  // load i of a step
+      const uint32_t n0 = st < nst ? (uint32_t)(first + st) * kTgB : (uint32_t)N, left = (uint32_t)N - n0;
+      const int row = 8 * (pw * LA + i) + lrow;  // chunks past the last weight row read as zero
+      load_lds_at(ar, sm + stage * T::A_STAGE + 1024 * (pw * LA + i),
+                  8u * (slot ^ ((row >> 1) & 7)) < left ? ao[i] : kPastEnd, 2 * n0);
     };
     // Codes, scales and zero-points -> LDS.  Codes: 16 bytes a lane.  Scales: for each
     // of 64 rows the 4 bytes that hold the value of the tile's group (with fp16 two
@@ -239,8 +230,8 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
       bo[i] = T::B_AT + 128 * (8 * kb + 2 * i) + 16 * ((b >> 1) ^ ((4 * kb + i) & 7)) + 8 * (b & 1);
     }
     const int tabo = T::TAB_AT + (SUBS > 1 ? 512 * pw : 0) + 16 * b;
-    // the weights of a step, from codes of stage cs to operands of stage bs
-    auto convert = [&](int cs, int bs) {
+    // the weights of a step, from codes of stage cs to operands of stage bs; `load` is called before each column
+    auto convert = [&](int cs, int bs, auto load) {
       uint32_t lo[4], hi[4];
       float s[4], z[4];  // z: -zp s, or zp where weights keep their bits
       const uint8_t* tb = sm + tabo + cs * T::TAB_STAGE;
@@ -261,6 +252,7 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
       uint8_t* out = sm + bs * T::B_STAGE;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        load(j);
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -286,26 +278,33 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_t_gemm(
             }
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
 #pragma unroll
     for (int i = 0; i < 3; ++i) w_issue(i, i);
-    a_issue(0, 0);
-    if constexpr (T::AS == 3) a_issue(1, 1);
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      a_issue(0, 0, i);
+      if constexpr (T::AS == 3) a_issue(1, 1, i);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     barrier();  // all four waves' codes and scales of step 0 are there
-    convert(0, 0);
+    convert(0, 0, [](int) {});
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     barrier();
     // In step t the loads of dy of t + 2 (t + 1 with two stages) and of codes of t + 3
     // are issued, into the places that step t - 1 has left, and the weights of t + 1 made.
     // Loads come in from the L2 cache 1000 to 2000 cycles after their issue: with three stages they have two steps.
+    // A CU takes in 64 bytes a cycle, a load of 1 KB every 16, so the loads of dy are
+    // spread over the conversion; issued together they held it up (185 us).
     all_steps([&](int st, auto number) {
       constexpr int k = decltype(number)::value;
       w_issue(st + 3, k % 3);
-      a_issue(st + T::AS - 1, (k + T::AS - 1) % T::AS);
-      convert((k + 1) % 3, (k + 1) % 2);
+      convert((k + 1) % 3, (k + 1) % 2, [&](int j) {
+        if (j % (8 / LA) == 0) a_issue(st + T::AS - 1, (k + T::AS - 1) % T::AS, j / (8 / LA));
+      });
       // all but this step's loads; with two stages of dy, those too
       if constexpr (T::AS == 2) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       else if (SUBS > 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 3) : "memory");
