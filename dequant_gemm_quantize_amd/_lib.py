@@ -50,8 +50,9 @@ SIGNATURES = [
     ("w4a16_grouped_matmul", _I, [_VP, _I, _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP]),
     ("quantize_checkpoint_int8", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP]),
     ("dequant_checkpoint_int8", _I, [_VP, _VP, _I64, _I64, _VP, _I, _VP]),
+    ("w4a16_lora_matmul_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I32, _I, _I, _I]),
     ("w4a16_lora_matmul", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP, _VP,
-                               _VP, _I64, _VP, _VP, _I, _VP]),
+                               _VP, _I64, _VP, _VP, _I, _VP, ctypes.c_size_t, _VP]),
     ("w4a16_matmul_t_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I32, _I, _I, _I]),
     ("w4a16_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP, ctypes.c_size_t, _VP]),
     ("w4a16_lora_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP,
@@ -669,6 +670,20 @@ def _int4_product(x, name: str, packed, scales, zeros, group_size: int, transpos
     return m, k, n
 
 
+def w4a16_lora_matmul_workspace_size(m: int, k: int, n: int, group_size: int, x_dtype: torch.dtype = torch.bfloat16,
+                                     sz_dtype: torch.dtype = torch.float16,
+                                     y_dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that w4a16_lora_matmul needs for this shape (0: none)."""
+    return int(load().w4a16_lora_matmul_workspace_size(m, k, n, group_size, _dtype_code(x_dtype), _dtype_code(sz_dtype),
+                                                       _dtype_code(y_dtype)))
+
+
+def _lora_workspace(size, x, m, k, n, group_size, scales, y) -> Optional[torch.Tensor]:
+    """The workspace that a product asks for, from torch, beside x."""
+    nbytes = size(m, k, n, group_size, _DT[x.dtype], _DT[scales.dtype], _DT[y.dtype])
+    return x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+
+
 def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
                       group_size: int, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor,
                       offsets: torch.Tensor, adapters: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
@@ -680,7 +695,7 @@ def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
     int32 [S] on the GPU (never read on the host): rows offsets[s] ..
     offsets[s+1]-1 have adapter adapters[s], none if that is no number of 0 .. L-1.
     u: a float32 [M, R] tensor that takes u (rows of no adapter are left as they
-    were).  out_dtype defaults to x's dtype."""
+    were).  out_dtype defaults to x's dtype.  The workspace comes from torch."""
     m, k, n = _int4_product(x, "x", packed, scales, zeros, group_size, False)
     count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
     given = tuple(t for t in (out, u) if t is not None)
@@ -690,9 +705,11 @@ def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
         u = x.new_empty((m, rank), dtype=torch.float32)
     elif u.shape != (m, rank) or u.dtype is not torch.float32:
         _expect(u, "u", (m, rank), (torch.float32,))
+    ws = _lora_workspace(load().w4a16_lora_matmul_workspace_size, x, m, k, n, group_size, scales, y)
     _launch(dev, load().w4a16_lora_matmul, _ptr(x), _dtype_code(x.dtype), m, k, _ptr(packed), _ptr(scales),
             _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
-            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(u), _ptr(y), _dtype_code(y.dtype))
+            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(u), _ptr(y), _dtype_code(y.dtype),
+            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
     return y
 
 
@@ -704,12 +721,6 @@ def w4a16_matmul_t_workspace_size(m: int, k: int, n: int, group_size: int, dy_dt
                                                     _dtype_code(dx_dtype)))
 
 
-def _t_workspace(dy, m, k, n, group_size, scales, dx) -> Optional[torch.Tensor]:
-    nbytes = load().w4a16_matmul_t_workspace_size(m, k, n, group_size, _dtype_code(dy.dtype),
-                                                  _dtype_code(scales.dtype), _dtype_code(dx.dtype))
-    return dy.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
-
-
 def w4a16_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int,
                    out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None):
     """dx [M, K] = dy [M, N] . dequant(W): the gradient of w4a16_matmul with respect to x.
@@ -718,7 +729,7 @@ def w4a16_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
     dev = _device(dy, packed, scales, zeros) if out is None else _device(dy, packed, scales, zeros, out)
     dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
-    ws = _t_workspace(dy, m, k, n, group_size, scales, dx)
+    ws = _lora_workspace(load().w4a16_matmul_t_workspace_size, dy, m, k, n, group_size, scales, dx)
     _launch(dev, load().w4a16_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales), _ptr(zeros),
             _dtype_code(scales.dtype), n, group_size, _ptr(dx), _dtype_code(dx.dtype),
             None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
@@ -743,7 +754,7 @@ def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Te
         v = dy.new_empty((m, rank), dtype=torch.float32)
     elif v.shape != (m, rank) or v.dtype is not torch.float32:
         _expect(v, "v", (m, rank), (torch.float32,))
-    ws = _t_workspace(dy, m, k, n, group_size, scales, dx)
+    ws = _lora_workspace(load().w4a16_matmul_t_workspace_size, dy, m, k, n, group_size, scales, dx)
     _launch(dev, load().w4a16_lora_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales),
             _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
             _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(v), _ptr(dx), _dtype_code(dx.dtype),

@@ -650,85 +650,38 @@ static int check_x(const char* fn, const char* name, int dtype) {
   return W4_OK;
 }
 
-// Pointers of the adapters' arguments, where there is any adapter.
-static int check_adapter_ptrs(const char* fn, const void* a, const void* b, const float* scaling,
-                              const int32_t* offsets, const int32_t* which, const char* low_name, const float* low) {
-  W4_TRY(check_ptr(fn, "a", a));
-  W4_TRY(check_ptr(fn, "b", b));
-  W4_TRY(check_ptr4(fn, "scaling", scaling));
-  W4_TRY(check_ptr4(fn, "offsets", offsets));
-  W4_TRY(check_ptr4(fn, "which", which));
-  return check_ptr(fn, low_name, low);
-}
-
-// Kernel choice of the forward product, as w4a16_grouped_matmul's with one expert.
-int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
-                      const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
-                      int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
-                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, hipStream_t stream) {
-  static const char* fn = "w4a16_lora_matmul";
-  W4_TRY(check_weights(fn, n, k, group_size, sz_dtype));
-  W4_TRY(check_x(fn, "x", x_dtype));
-  W4_TRY(check_x(fn, "adapter", ab_dtype));
-  W4_TRY(check_y(fn, y_dtype));
-  W4_TRY(check_tokens(fn, m, k, n));
-  W4_TRY(check_adapters(fn, m, k, n, adapters, rank, segments));
-  if (m == 0 || n == 0) return ok();
-  W4_TRY(check_ptr(fn, "x", x));
-  W4_TRY(check_ptr(fn, "packed", packed));
-  W4_TRY(check_ptr(fn, "scales", scales));
-  W4_TRY(check_ptr(fn, "zeros", zeros));
-  W4_TRY(check_ptr(fn, "y", y));
-  w4::LoraOut lo{u, b, ab_dtype, adapters, rank, offsets, which, segments};
-  if (adapters == 0 || segments == 0) {
-    lo.segments = 0;
-  } else {
-    W4_TRY(check_adapter_ptrs(fn, a, b, scaling, offsets, which, "u", u));
-    const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u};
-    const hipError_t e = w4::launch_lora_into(in, stream);
-    if (e != hipSuccess) return hip_status(e, fn);
-  }
-  if (x_dtype == W4_BF16 && m > (group_size % 128 == 64 ? 8 : 16) && w4::w4a16_grouped_gemm_fits(k))
-    return hip_status(w4::launch_w4a16_lora_gemm(x, m, k, packed, scales, zeros, sz_dtype, n, group_size, y, y_dtype,
-                                                 lo, stream),
-                      fn);
-  return hip_status(w4::launch_w4a16_lora_rows(x, x_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, y,
-                                               y_dtype, lo, stream),
-                    fn);
-}
-
-size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype,
-                                     int dx_dtype) {
-  static const char* fn = "w4a16_matmul_t_workspace_size";
-  const bool valid = check_weights(fn, n, k, group_size, sz_dtype) == W4_OK && check_x(fn, "dy", dy_dtype) == W4_OK &&
-                     check_y(fn, dx_dtype) == W4_OK && check_tokens(fn, m, k, n) == W4_OK && m <= w4::kLoraMaxRows;
+// Both directions: x [m, k] W^T forward, x [m, n] W back, with adapters where `in` has a rank.
+static size_t lora_workspace(bool back, int64_t m, int64_t k, int64_t n, int32_t group_size, int x_dtype, int sz_dtype,
+                             int y_dtype) {
+  static const char* fn = "workspace_size";
+  const bool valid = check_weights(fn, n, k, group_size, sz_dtype) == W4_OK && check_x(fn, "x", x_dtype) == W4_OK &&
+                     check_y(fn, y_dtype) == W4_OK && check_tokens(fn, m, k, n) == W4_OK && m <= w4::kLoraMaxRows;
   ok();
   if (!valid || m == 0 || n == 0) return 0;
-  return w4::w4a16_t_workspace_bytes(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
+  return w4::w4a16_lora_workspace_bytes(back, m, k, n, group_size, x_dtype, sz_dtype, y_dtype);
 }
 
-static int matmul_t(const char* fn, const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
-                    const void* scales, const void* zeros, int sz_dtype, int64_t n, int32_t group_size,
-                    const w4::LoraInto& in, const w4::LoraOut& out, void* dx, int dx_dtype, void* workspace,
-                    size_t workspace_bytes, hipStream_t stream) {
-  W4_TRY(check_weights(fn, n, k, group_size, sz_dtype));
-  W4_TRY(check_x(fn, "dy", dy_dtype));
-  W4_TRY(check_y(fn, dx_dtype));
-  W4_TRY(check_tokens(fn, m, k, n));
+static int lora_product(const char* fn, int x_dtype, const w4::TilesArgs& p, const w4::LoraInto& in,
+                        const w4::LoraOut& out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* low_name = p.back ? "v" : "u";
+  W4_TRY(check_weights(fn, p.n, p.k, p.g, p.sz_dtype));
+  W4_TRY(check_x(fn, p.back ? "dy" : "x", x_dtype));
+  W4_TRY(check_y(fn, p.y_dtype));
+  W4_TRY(check_tokens(fn, p.m, p.k, p.n));
   if (in.rank != 0) {
     W4_TRY(check_x(fn, "adapter", in.w_dtype));
-    W4_TRY(check_adapters(fn, m, k, n, in.count, in.rank, in.segments));
+    W4_TRY(check_adapters(fn, p.m, p.k, p.n, in.count, in.rank, in.segments));
   }
-  if (m > w4::kLoraMaxRows)
-    return fail(W4_EINVAL, "%s: m = %lld is too large (at most %lld)", fn, (long long)m, (long long)w4::kLoraMaxRows);
-  if (n == 0) return fail(W4_EINVAL, "%s: n must be > 0 (the sum runs over it)", fn);
-  if (m == 0) return ok();
-  W4_TRY(check_ptr(fn, "dx", dx));
-  W4_TRY(check_ptr(fn, "dy", dy));
-  W4_TRY(check_ptr(fn, "packed", packed));
-  W4_TRY(check_ptr(fn, "scales", scales));
-  W4_TRY(check_ptr(fn, "zeros", zeros));
-  const size_t need = w4::w4a16_t_workspace_bytes(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
+  if (p.m > w4::kLoraMaxRows)
+    return fail(W4_EINVAL, "%s: m = %lld is too large (at most %lld)", fn, (long long)p.m, (long long)w4::kLoraMaxRows);
+  if (p.n == 0 && p.back) return fail(W4_EINVAL, "%s: n must be > 0 (the sum runs over it)", fn);
+  if (p.m == 0 || p.n == 0) return ok();
+  W4_TRY(check_ptr(fn, p.back ? "dy" : "x", p.x));
+  W4_TRY(check_ptr(fn, "packed", p.packed));
+  W4_TRY(check_ptr(fn, "scales", p.scales));
+  W4_TRY(check_ptr(fn, "zeros", p.zeros));
+  W4_TRY(check_ptr(fn, p.back ? "dx" : "y", p.y));
+  const size_t need = w4::w4a16_lora_workspace_bytes(p.back, p.m, p.k, p.n, p.g, x_dtype, p.sz_dtype, p.y_dtype);
   if (need > 0) {
     W4_TRY(check_ptr(fn, "workspace", workspace));
     if (workspace_bytes < need)
@@ -738,20 +691,46 @@ static int matmul_t(const char* fn, const void* dy, int dy_dtype, int64_t m, int
   if (in.rank == 0 || in.count == 0 || in.segments == 0) {
     lo.count = lo.segments = 0;
   } else {
-    W4_TRY(check_adapter_ptrs(fn, out.out, in.weights, in.scaling, in.offsets, in.which, "v", in.low));
+    W4_TRY(check_ptr(fn, "a", in.down ? in.weights : out.out));
+    W4_TRY(check_ptr(fn, "b", in.down ? out.out : in.weights));
+    W4_TRY(check_ptr4(fn, "scaling", in.scaling));
+    W4_TRY(check_ptr4(fn, "offsets", in.offsets));
+    W4_TRY(check_ptr4(fn, "which", in.which));
+    W4_TRY(check_ptr(fn, low_name, in.low));
     const hipError_t e = w4::launch_lora_into(in, stream);
     if (e != hipSuccess) return hip_status(e, fn);
   }
-  return hip_status(w4::launch_w4a16_t(dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, dx, dx_dtype,
-                                       lo, workspace, stream),
-                    fn);
+  return hip_status(w4::launch_w4a16_lora(p.x, x_dtype, p, lo, workspace, stream), fn);
+}
+
+size_t w4a16_lora_matmul_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int x_dtype, int sz_dtype,
+                                        int y_dtype) {
+  return lora_workspace(false, m, k, n, group_size, x_dtype, sz_dtype, y_dtype);
+}
+
+int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
+                      const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
+                      int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
+                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  static const char* fn = "w4a16_lora_matmul";
+  if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
+  const w4::TilesArgs p{false, x, m, k, n, packed, scales, zeros, sz_dtype, group_size, y, y_dtype, 0, 0, 0, 0};
+  const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u};
+  const w4::LoraOut out{u, b, ab_dtype, adapters, rank, offsets, which, segments};
+  return lora_product(fn, x_dtype, p, in, out, workspace, workspace_bytes, stream);
+}
+
+size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype,
+                                     int dx_dtype) {
+  return lora_workspace(true, m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
 }
 
 int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                    const void* zeros, int sz_dtype, int64_t n, int32_t group_size, void* dx, int dx_dtype,
                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  return matmul_t("w4a16_matmul_t", dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, w4::LoraInto{},
-                  w4::LoraOut{}, dx, dx_dtype, workspace, workspace_bytes, stream);
+  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0};
+  return lora_product("w4a16_matmul_t", dy_dtype, p, w4::LoraInto{}, w4::LoraOut{}, workspace, workspace_bytes, stream);
 }
 
 int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
@@ -763,8 +742,8 @@ int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, cons
   if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
   const w4::LoraInto in{false, dy, dy_dtype, m, n, b, ab_dtype, adapters, rank, scaling, offsets, which, segments, v};
   const w4::LoraOut out{v, a, ab_dtype, adapters, rank, offsets, which, segments};
-  return matmul_t(fn, dy, dy_dtype, m, k, packed, scales, zeros, sz_dtype, n, group_size, in, out, dx, dx_dtype,
-                  workspace, workspace_bytes, stream);
+  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0};
+  return lora_product(fn, dy_dtype, p, in, out, workspace, workspace_bytes, stream);
 }
 
 static int check_grads(const char* fn, int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank,

@@ -45,6 +45,41 @@ __device__ __forceinline__ int row_adapter(const Adapters& a, int64_t m, int lan
   return w >= 0 && w < a.count ? w : -1;
 }
 
+// A tile of bm rows of one segment, `width` tiles side by side.
+struct SegmentTile {
+  int adapter;   // -1: none
+  int64_t m0;    // first row
+  int rows;
+  uint32_t side;  // which of the `width`
+};
+// Tile `want` of the list in which every segment has its tiles of bm rows times
+// `width`, as find_group_tile; the adapters' numbers are loaded beside the offsets, not behind them.
+__device__ __forceinline__ bool find_segment_tile(const int* offsets, const int* which, int segments, int count, int M,
+                                                  int bm, uint32_t width, int64_t want, int lane, SegmentTile& t) {
+  int64_t before = 0;
+  for (int base = 0; base < segments; base += kWave) {
+    int row0;
+    const int w = base + lane < segments ? which[base + lane] : -1;
+    const int rows = group_rows(offsets, segments, M, base, lane, row0);
+    const int mine = (rows + bm - 1) / bm;
+    const int upto = wave_scan(mine);
+    const uint64_t past = __ballot((before + upto) * width > want);
+    if (past != 0) {
+      const int f = __builtin_ctzll(past);
+      const int ad = __builtin_amdgcn_readlane(w, f), have = __builtin_amdgcn_readlane(rows, f);
+      const uint32_t tile = (uint32_t)(want - (before + __builtin_amdgcn_readlane(upto - mine, f)) * width);
+      const int skip = bm * (int)(tile / width);
+      t.adapter = ad >= 0 && ad < count ? ad : -1;
+      t.m0 = __builtin_amdgcn_readlane(row0, f) + skip;
+      t.rows = have - skip < bm ? have - skip : bm;
+      t.side = tile % width;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  return false;
+}
+
 // 8 float32 as hi + mid + lo, each 8 bf16: the upper halves of the words, of
 // what they lack, and of what that lacks, which is exact for normal values.
 __device__ __forceinline__ void split8(u32x4 v0, u32x4 v1, bf16x8 (&out)[3]) {

@@ -4,126 +4,275 @@
 // float32, on v_mfma_f32_16x16x32_bf16: bf16 values as they are, float32 ones as the
 // exact sum of three bf16 values.  Rows of no adapter are left as they were.
 //
-// A workgroup has 16 MT rows of one segment and RT ranks; its waves go through D in
-// turn, 128 values at a time, and add their sums through LDS.  Few rows take
-// four ranks a workgroup, so that more CUs read the adapter's rows.
+// A workgroup has 16 MT rows of one segment and some ranks; its waves go through D in
+// turn, 128 values at a time, and add their sums through LDS.  Few rows take four
+// ranks a workgroup, so that more CUs read the adapter's rows.
+//
+// Bound by latency where rows are few, by what a CU takes in from the L2 cache
+// where they are many: a wave has all loads of its 128 values under way before it waits.
 #include "lora.h"
+#include "lds_gemm.h"
 #include "w4_internal.h"
 
 namespace w4 {
 
 namespace {
 
-constexpr int kIntoWaves = 8;
 constexpr int64_t kIntoGrid = 1 << 20;  // workgroups; more tiles than that loop
 
-// The adapter's values at rank r, 8 of them along D from d on.  DOWN: [R, D] (D % 32 == 0), otherwise [D, R].
-template <bool DOWN, typename TW>
-__device__ __forceinline__ void adapter8(const TW* w, int64_t d, int64_t D, int r, int R, bool real,
-                                         bf16x8 (&out)[Parts<TW>::n]) {
-  if constexpr (DOWN) {
-    if (real && d < D) {
-      load8(w + (int64_t)r * D + d, out);
-      return;
-    }
-#pragma unroll
-    for (int p = 0; p < Parts<TW>::n; ++p) out[p] = zero8();
-  } else {
-    TW v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = real && d + i < D ? w[(d + i) * R + r] : (TW)0;
-    pack8(v, out);
+// The waves' sums, added: part [waves][rows][ranks] -> low.
+template <int BM, int RANKS>
+__device__ __forceinline__ void into_store(const float* part, int waves, const SegmentTile& t, int rank0, int R,
+                                           float c, float* low) {
+  for (int o = threadIdx.x; o < t.rows * RANKS; o += blockDim.x) {
+    const int row = o / RANKS, q = o % RANKS;
+    if (rank0 + q >= R) continue;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < waves; ++i) v += part[(i * BM + row) * RANKS + q];
+    low[(t.m0 + row) * R + rank0 + q] = c * v;
   }
 }
 
 }  // namespace
 
-template <bool DOWN, int MT, int RT, typename TX, typename TW>
-__global__ __launch_bounds__(64 * kIntoWaves) void k_lora_into(
+// x into A.  RANKS: 4 or 16 RB ranks.
+constexpr int kDownWaves = 16;
+template <int MT, int RANKS, typename TX, typename TW>
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(
     const TX* __restrict__ x, int64_t M, int64_t D, const TW* __restrict__ weights, int count, int R,
     const float* __restrict__ scaling, const int* __restrict__ offsets, const int* __restrict__ which, int segments,
-    float* __restrict__ low, uint32_t rblocks, int64_t tiles, int wide) {
-  __shared__ float part[kIntoWaves][16 * MT][RT];
+    float* __restrict__ low, uint32_t rblocks, int64_t tiles) {
+  constexpr int RB = RANKS < 16 ? 1 : RANKS / 16, RC = RANKS < 16 ? RANKS : 16;  // blocks of ranks, ranks of a block
+  // values of D that a wave loads at a time: what its registers hold
+  constexpr int CK = MT * (int)sizeof(TX) + RB * (int)sizeof(TW) <= 4 ? 256 : 128;
+  extern __shared__ __attribute__((aligned(16))) float part[];                 // [waves][16 MT][RANKS]
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, h = lane >> 4;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    GroupTile gt;
-    if (!find_group_tile(offsets, segments, (int)M, 16 * MT, rblocks, tile, lane, gt)) return;
-    const int ad = which[gt.expert];
-    if (ad < 0 || ad >= count) continue;
-    const int rb = (int)(gt.tile % rblocks) * RT;
-    const int64_t m0 = gt.row0 + (int64_t)16 * MT * (gt.tile / rblocks);
-    const int64_t left = gt.row0 + gt.rows - m0;
-    const int rows = (int)(left < 16 * MT ? left : 16 * MT);
-    const TW* wl = weights + (int64_t)ad * R * D;
-    const int r = rb + l16;
-    const bool rank = l16 < RT && r < R;
-
-    f32x4 acc[MT][2];
+    SegmentTile t;
+    if (!find_segment_tile(offsets, which, segments, count, (int)M, 16 * MT, rblocks, tile, lane, t)) return;
+    if (t.adapter < 0) continue;
+    const int rank0 = RANKS * (int)t.side;
+    const float c = scaling[t.adapter];
+    // rows and ranks past the end repeat the last: nobody stores what they give
+    const TX* xp[MT];
+    const TW* wp[RB];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t][0] = acc[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t d0 = 128 * w; d0 < D; d0 += 128 * kIntoWaves) {
+    for (int i = 0; i < MT; ++i) {
+      const int row = 16 * i + l16;
+      xp[i] = x + (t.m0 + (row < t.rows ? row : t.rows - 1)) * D + 8 * h;
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t d = d0 + 32 * q + 8 * h;
-        bf16x8 b[Parts<TW>::n];
-        adapter8<DOWN>(wl, d, D, r, R, rank, b);
+    for (int i = 0; i < RB; ++i) {
+      const int r = rank0 + 16 * i + l16 % RC;
+      wp[i] = weights + ((int64_t)t.adapter * R + (r < R ? r : R - 1)) * D + 8 * h;
+    }
+    f32x4 acc[MT][RB][2];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          bf16x8 a[Parts<TX>::n];
-          const int row = 16 * t + l16;
-          row8(x + (m0 + (row < rows ? row : 0)) * D, d, D, row < rows, wide, a);
-          mfma_parts(a, b, acc[t]);
-        }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < RB; ++j) acc[i][j][0] = acc[i][j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto slices = [&](int64_t d0, auto count_c) {
+      constexpr int n = decltype(count_c)::value;
+      bf16x8 a[n][MT][Parts<TX>::n], b[n][RB][Parts<TW>::n];
+#pragma unroll
+      for (int q = 0; q < n; ++q) {
+#pragma unroll
+        for (int j = 0; j < RB; ++j) load8(wp[j] + d0 + 32 * q, b[q][j]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) load8(xp[i] + d0 + 32 * q, a[q][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // every load is on its way before the first is waited for
+#pragma unroll
+      for (int q = 0; q < n; ++q)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < RB; ++j) mfma_parts(a[q][i], b[q][j], acc[i][j]);
+    };
+    for (int64_t d0 = CK * w; d0 < D; d0 += CK * kDownWaves) {
+      if (d0 + CK <= D) {
+        slices(d0, std::integral_constant<int, CK / 32>{});
+      } else {
+        for (int64_t d = d0; d < D; d += 32) slices(d, std::integral_constant<int, 1>{});
       }
     }
     // lane holds rows 4 h + e of rank l16
-    if (l16 < RT) {
+    if (l16 < RC) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[w][16 * t + 4 * h + e][l16] = acc[t][0][e] + acc[t][1][e];
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            part[(w * 16 * MT + 16 * i + 4 * h + e) * RANKS + 16 * j + l16] = acc[i][j][0][e] + acc[i][j][1][e];
     }
     __syncthreads();
-    const float c = scaling[ad];
-    for (int o = threadIdx.x; o < rows * RT; o += 64 * kIntoWaves) {
-      const int row = o / RT, q = o % RT;
-      if (rb + q >= R) continue;
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kIntoWaves; ++i) v += part[i][row][q];
-      low[(m0 + row) * R + rb + q] = c * v;
-    }
+    into_store<16 * MT, RANKS>(part, kDownWaves, t, rank0, R, c, low);
     __syncthreads();  // the next tile writes part again
   }
 }
 
-template <bool DOWN, int MT, int RT, typename TX, typename TW>
-static hipError_t into_go(const LoraInto& a, hipStream_t st) {
-  const int64_t rblocks = (a.rank + RT - 1) / RT;
+// dy into B, 16 rows and 16 ranks a workgroup.  The sum runs over rows of B, so an
+// operand's 8 values are a column of it: B goes from memory to the wave's own place in LDS,
+// 2 or 4 KB at a time, and is read from there value by value; row n of 32 is at place
+// 4 (n % 8) + n / 8, which puts the four rows that a read meets beside each other, on
+// all banks once.  dy takes the same way where its rows start at 16-byte addresses
+// (piece c of row m at slot c ^ m, modulo the row's pieces).  (Loads of single values of B from memory, 16
+// lanes an address pass, took 77 us for 12 rows against [11008, 16].)
+constexpr int kUpWaves = 8;
+template <typename TX, typename TW> struct UpPlace {
+  static constexpr int CH = sizeof(TX) + sizeof(TW) > 4 ? 64 : 128;  // rows of B a step
+  static constexpr int WB = 16 * CH * (int)sizeof(TW), XB = 16 * CH * (int)sizeof(TX);  // bytes of B and of 16 rows of dy
+  static constexpr int STAGE = WB + XB;
+  static constexpr size_t lds = 2 * (size_t)kUpWaves * STAGE;
+};
+template <typename TX, typename TW, bool WIDE>
+__global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
+    const TX* __restrict__ x, int64_t M, int64_t D, const TW* __restrict__ weights, int count, int R,
+    const float* __restrict__ scaling, const int* __restrict__ offsets, const int* __restrict__ which, int segments,
+    float* __restrict__ low, uint32_t rblocks, int64_t tiles) {
+  typedef UpPlace<TX, TW> P;
+  constexpr int CH = P::CH, Q = CH / 32;
+  constexpr int XC = CH * (int)sizeof(TX) / 16;          // 16-byte pieces of a row of dy
+  constexpr int XL = P::XB / 1024, WL = P::WB / 1024;    // loads of dy and B a step
+  constexpr int PX = Parts<TX>::n, PW = Parts<TW>::n, LOADS = WL + (WIDE ? XL : 0);
+  extern __shared__ __attribute__((aligned(1024))) uint8_t su[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, h = lane >> 4;
+  uint8_t* mine = su + w * 2 * P::STAGE;
+  float* part = (float*)su;  // [waves][16][16], when the places are done with
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    SegmentTile t;
+    if (!find_segment_tile(offsets, which, segments, count, (int)M, 16, rblocks, tile, lane, t)) return;
+    if (t.adapter < 0) continue;
+    const int rank0 = 16 * (int)t.side;
+    const float c = scaling[t.adapter];
+    const TW* wl = weights + (int64_t)t.adapter * D * R;
+    const TX* xt = x + t.m0 * D;
+    const uint32_t xrow = (uint32_t)(D * (int64_t)sizeof(TX)), wrow = (uint32_t)R * (uint32_t)sizeof(TW);
+    const __amdgpu_buffer_rsrc_t xr = buf_rsrc_n(uniform_ptr(xt), (uint32_t)t.rows * xrow);
+    constexpr int SL = (int)sizeof(TW);  // 16-byte pieces of a row's 16 ranks
+    auto issue = [&](int64_t d0, int stage) {
+      uint8_t* place = mine + stage * P::STAGE;
+      const int64_t have = d0 < D ? (D - d0 < CH ? D - d0 : CH) : 0;
+      const __amdgpu_buffer_rsrc_t wr = buf_rsrc_n(uniform_ptr(wl + (d0 < D ? d0 : 0) * R), (uint32_t)have * wrow);
+#pragma unroll
+      for (int i = 0; i < WL; ++i) {
+        const int s = 64 * i + lane, p = s / SL, piece = s % SL;
+        const int n = (p & 31) / 4 + 8 * (p & 3) + (p & ~31);
+        const bool in = rank0 + piece * (16 / (int)sizeof(TW)) < R;
+        load_lds(wr, place + 1024 * i,
+                 in ? (uint32_t)n * wrow + (uint32_t)rank0 * (uint32_t)sizeof(TW) + 16u * piece : kPastEnd);
+      }
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+          const int s = 64 * i + lane, row = s / XC, piece = (s % XC) ^ (row & (XC - 1));
+          const bool in = d0 + (int64_t)piece * (16 / (int)sizeof(TX)) < D;
+          load_lds(xr, place + P::WB + 1024 * i,
+                   in ? (uint32_t)row * xrow + (uint32_t)(d0 * (int64_t)sizeof(TX)) + 16u * piece : kPastEnd);
+        }
+      }
+    };
+    f32x4 acc[2];
+    acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int64_t stride = CH * kUpWaves;
+    int stage = 0;
+    if ((int64_t)CH * w < D) issue((int64_t)CH * w, 0);
+    for (int64_t d0 = (int64_t)CH * w; d0 < D; d0 += stride, stage ^= 1) {
+      issue(d0 + stride, stage ^ 1);  // past D nothing, as many loads
+      bf16x8 a[Q][PX];
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) row8(xt + (l16 < t.rows ? l16 : 0) * D, d0 + 32 * q + 8 * h, D, true, false, a[q]);
+      }
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+      const uint8_t* place = mine + stage * P::STAGE;
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          constexpr int per = (int)sizeof(TX) / 2;  // pieces of 8 values
+          u32x4 v[per];
+#pragma unroll
+          for (int i = 0; i < per; ++i)
+            v[i] = *(const u32x4*)(place + P::WB + 16 * (XC * l16 + ((per * (4 * q + h) + i) ^ (l16 & (XC - 1)))));
+          if constexpr (per == 1) a[q][0] = __builtin_bit_cast(bf16x8, v[0]);
+          else split8(v[0], v[1], a[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        TW v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ((const TW*)place)[16 * (32 * q + 4 * i + h) + l16];
+        bf16x8 b[PW];
+        pack8(v, b);
+        mfma_parts(a[q], b, acc);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the place is written again
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[(w * 16 + 4 * h + e) * 16 + l16] = acc[0][e] + acc[1][e];
+    __syncthreads();
+    into_store<16, 16>(part, kUpWaves, t, rank0, R, c, low);
+    __syncthreads();  // the next tile writes there again
+  }
+}
+
+template <int MT, int RANKS, typename TX, typename TW>
+static hipError_t down_go(const LoraInto& a, hipStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
+  constexpr size_t lds = (size_t)kDownWaves * 16 * MT * RANKS * 4;
+  const hipError_t e = once_per_device(attr_done, [] {
+    return hipFuncSetAttribute((const void*)k_lora_down<MT, RANKS, TX, TW>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lds);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t rblocks = (a.rank + RANKS - 1) / RANKS;
   const int64_t tiles = grouped_max_tiles(a.m, a.segments, 16 * MT) * rblocks;
-  k_lora_into<DOWN, MT, RT><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kIntoWaves, 0, st>>>(
+  k_lora_down<MT, RANKS, TX, TW><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kDownWaves, lds, st>>>(
       (const TX*)a.x, a.m, a.d, (const TW*)a.weights, (int)a.count, a.rank, a.scaling, a.offsets, a.which,
-      (int)a.segments, a.low, (uint32_t)rblocks, tiles, a.d * (int64_t)sizeof(TX) % 16 == 0);
+      (int)a.segments, a.low, (uint32_t)rblocks, tiles);
   return hipGetLastError();
 }
 
-template <bool DOWN, typename TX, typename TW>
-static hipError_t into_size(const LoraInto& a, hipStream_t st) {
-  if (a.m <= 16 * a.segments) return into_go<DOWN, 1, 4, TX, TW>(a, st);
-  return into_go<DOWN, 1, 16, TX, TW>(a, st);
+template <typename TX, typename TW, bool WIDE>
+static hipError_t up_go(const LoraInto& a, hipStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
+  constexpr size_t lds = UpPlace<TX, TW>::lds;
+  const hipError_t e = once_per_device(attr_done, [] {
+    return hipFuncSetAttribute((const void*)k_lora_up<TX, TW, WIDE>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t rblocks = (a.rank + 15) / 16;
+  const int64_t tiles = grouped_max_tiles(a.m, a.segments, 16) * rblocks;
+  k_lora_up<TX, TW, WIDE><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kUpWaves, lds, st>>>(
+      (const TX*)a.x, a.m, a.d, (const TW*)a.weights, (int)a.count, a.rank, a.scaling, a.offsets, a.which,
+      (int)a.segments, a.low, (uint32_t)rblocks, tiles);
+  return hipGetLastError();
 }
 
-template <bool DOWN>
+template <typename TX, typename TW>
 static hipError_t into_types(const LoraInto& a, hipStream_t st) {
-  if (a.x_dtype == W4_F32)
-    return a.w_dtype == W4_F32 ? into_size<DOWN, float, float>(a, st) : into_size<DOWN, float, uint16_t>(a, st);
-  return a.w_dtype == W4_F32 ? into_size<DOWN, uint16_t, float>(a, st) : into_size<DOWN, uint16_t, uint16_t>(a, st);
+  if (a.down) {
+    if (a.m <= 16 * a.segments || a.m <= 256) return down_go<1, 4, TX, TW>(a, st);
+    return a.rank > 16 ? down_go<1, 32, TX, TW>(a, st) : down_go<1, 16, TX, TW>(a, st);
+  }
+  // 16 rows of dy by byte offsets below 2^31
+  if (a.d * (int64_t)sizeof(TX) % 16 == 0 && a.d * (int64_t)sizeof(TX) < ((int64_t)1 << 27)) return up_go<TX, TW, true>(a, st);
+  return up_go<TX, TW, false>(a, st);
 }
 
 hipError_t launch_lora_into(const LoraInto& a, hipStream_t st) {
-  return a.down ? into_types<true>(a, st) : into_types<false>(a, st);
+  if (a.x_dtype == W4_F32)
+    return a.w_dtype == W4_F32 ? into_types<float, float>(a, st) : into_types<float, uint16_t>(a, st);
+  return a.w_dtype == W4_F32 ? into_types<uint16_t, float>(a, st) : into_types<uint16_t, uint16_t>(a, st);
 }
 
 }  // namespace w4

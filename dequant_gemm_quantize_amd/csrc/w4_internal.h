@@ -165,23 +165,31 @@ struct LoraOut {
   const int* which;
   int64_t segments;
 };
-// y = x W^T + low out^T: few rows or float32 x, and many rows.
+// A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles of 64 mi
+// rows, for bf16 x: pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
+// ones for a float32 result), and with parts > 1 float32 partial sums, without adapters.
+struct TilesArgs {
+  bool back;
+  const void* x;
+  int64_t m, k, n;
+  const uint8_t* packed;
+  const void* scales;
+  const void* zeros;
+  int sz_dtype, g;
+  void* y;
+  int y_dtype;
+  int mi, pw, parts, steps;
+};
+hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st);
+// Forward for few rows, and for float32 x.
 hipError_t launch_w4a16_lora_rows(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed,
                                   const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y,
                                   int y_dtype, const LoraOut& lo, hipStream_t st);
-hipError_t launch_w4a16_lora_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
-                                  const void* zeros, int sz_dtype, int64_t n, int g, void* y, int y_dtype,
-                                  const LoraOut& lo, hipStream_t st);
-// dx = dy W + low out.  Bytes of workspace (0: none).
-size_t w4a16_t_workspace_bytes(int64_t m, int64_t k, int64_t n, int g, int dy_dtype, int sz_dtype, int dx_dtype);
-hipError_t launch_w4a16_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed,
-                          const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* dx,
-                          int dx_dtype, const LoraOut& lo, void* ws, hipStream_t st);
-// The same in tiles of 64 mi rows, for bf16 dy: pw bf16 parts of a weight (1; 2
-// with fp16 scales or 3 with float32 ones for float32 dx); with parts > 1 float32 partial sums, without adapters.
-hipError_t launch_w4a16_t_gemm(const void* dy, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
-                               const void* zeros, int sz_dtype, int64_t n, int g, void* dx, int dx_dtype,
-                               const LoraOut& lo, int mi, int pw, int parts, int steps, hipStream_t st);
+// Either direction, whatever the sizes (args without x, mi, pw, parts and steps), and the workspace's bytes (0: none).
+size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
+                                  int y_dtype);
+hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, const LoraOut& lo, void* ws,
+                             hipStream_t st);
 // Gradients of the adapters from the 8-bit checkpoint of x, dy and the low-rank values.
 struct LoraGrads {
   const int8_t* xq;

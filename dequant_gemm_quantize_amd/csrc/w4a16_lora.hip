@@ -1,0 +1,320 @@
+// W4A16 products with low-rank adapters, x W^T forward and dy W back: the choice of
+// a kernel, the kernel for few rows back, and the sum of split products.
+//
+// Forward, few rows and float32 x take the few-row kernel (w4a16_lora_rows.hip).
+// Back, few rows and float32 dy take k_w4a16_back_rows, on v_mfma_f32_16x16x32_bf16.  A wave has
+// 256 columns of 16 MB rows of dx and goes through N 32 weight rows at a time.
+// The sum runs over weight rows, the codes of a word over columns: lane (l16,
+// h) loads 16 codes (8 bytes) of each of rows 8 h .. 8 h + 7, and the eight
+// values of one column, one out of each word, are the operand of one of 16 MFMAs, whose 16
+// columns are 16 l16 + j.  So nothing is transposed in memory or LDS.  The waves of
+// a workgroup and the workgroups of a strip share N; the partial sums, float32, meet
+// in LDS and in the workspace, where k_w4a16_sum adds them in order, and the low-rank part.
+//
+// Many rows of bf16 x take tiles in both directions (w4a16_tiles.h), split over the sum where
+// the tiles are few.
+//
+// Rounding: bf16 x with a bf16 result takes, in tiles and back, a weight rounded to bf16, as
+// w4a16_matmul does (half a step, 2^-8 at most, beside the result's own).  Otherwise the weight is the
+// exact sum of bf16 parts, two with fp16 scales (15 bits), three with float32 ones (24).
+#include "lora.h"
+#include "w4_internal.h"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kTWaves = 4;
+constexpr int kTStrip = 256;  // columns of a workgroup
+constexpr int64_t kTGrid = 1 << 20;  // workgroups of a part; more tiles than that loop
+constexpr int64_t kTSumGrid = 1 << 22;
+
+template <typename TS>
+__device__ __forceinline__ float t_scale(const void* p, int64_t i) {
+  return ScaleT<TS>::load(p, i);
+}
+
+// How a call is computed: in tiles (w4a16_tiles.h) or by a kernel for few rows, and
+// how it splits the sum: parts of `steps` steps of 64 or 32.
+struct LoraPlan {
+  bool tiles;
+  int mi, pw;          // tiles of 64 mi rows; bf16 parts of a weight
+  int mb;              // blocks of 16 rows a workgroup of k_w4a16_back_rows
+  int64_t rows, strips, parts, steps;
+  size_t bytes;        // of workspace
+};
+
+void split(LoraPlan& p, int64_t all, int64_t parts) {
+  if (parts < 1) parts = 1;
+  p.steps = (all + parts - 1) / parts;
+  p.parts = (all + p.steps - 1) / p.steps;
+}
+
+LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype) {
+  const int64_t d = back ? n : k, c = back ? k : n;
+  const bool exact = x_dtype != W4_BF16 || y_dtype != W4_BF16;  // weights keep their bits
+  LoraPlan p{};
+  p.pw = !exact ? 1 : sz_dtype == W4_F16 ? 2 : 3;
+  p.parts = 1;
+  // Rows of x start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
+  // below 2^31 bytes; 2^16 blocks of 32 columns; forward, an even number of fp16 scales.
+  p.tiles = x_dtype == W4_BF16 && m > 32 && d % 8 == 0 && d <= ((int64_t)1 << 21) &&
+            (back || sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
+  if (p.tiles) {
+    p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
+    p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
+    p.strips = (c + 127) / 128;
+    const int64_t all = (d + 63) / 64, parts = 256 / (p.rows * p.strips);
+    split(p, all, parts < all / 8 ? parts : all / 8);
+    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)c * 4;
+  } else if (back) {
+    p.mb = exact || m <= 16 ? 1 : 2;
+    p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
+    p.strips = (c + kTStrip - 1) / kTStrip;
+    const int64_t all = (d + 31) / 32, parts = 1024 / (p.rows * p.strips);
+    split(p, all, parts < all / (2 * kTWaves) ? parts : all / (2 * kTWaves));
+    p.bytes = (size_t)p.parts * (size_t)m * (size_t)c * 4;
+  }
+  return p;
+}
+
+}  // namespace
+
+// PW: bf16 parts of a weight.
+template <typename TX, typename TS, int PW, int MB>
+__global__ __launch_bounds__(64 * kTWaves) void k_w4a16_back_rows(
+    const TX* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
+    const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, int wide,
+    float* __restrict__ part) {
+  constexpr int PX = Parts<TX>::n;
+  constexpr int NA = PX + PW > 2 ? 2 : 1;  // sums: the upper parts' and the others'
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][16][256]
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, h = lane >> 4;
+  const int64_t strips = (K + kTStrip - 1) / kTStrip, tiles = strips * ((M + 16 * MB - 1) / (16 * MB));
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t k0 = kTStrip * (tile % strips), m0 = 16 * MB * (tile / strips);
+    const int64_t col = k0 + 16 * l16;
+    const int64_t cc = col < K ? col : 0;  // lanes past K compute what nobody stores
+    const int64_t ng = K / g, gi = cc / g, half = K / 2;
+    const int64_t all = (N + 31) / 32, first = (int64_t)steps * blockIdx.y;
+    const int64_t last = first + steps < all ? first + steps : all;
+
+    f32x4 acc[MB][16][NA];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int a = 0; a < NA; ++a) acc[b][j][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int64_t s = first + w; s < last; s += kTWaves) {
+      const int64_t n0 = 32 * s + 8 * h;
+      u32x2 p[8];
+      float sc[8], zp[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i < N ? n0 + i : N - 1;  // dy is zero there
+        p[i] = *(const u32x2*)(packed + n * half + cc / 2);
+        sc[i] = t_scale<TS>(scales, n * ng + gi);
+        zp[i] = t_scale<TS>(zeros, n * ng + gi);
+      }
+      bf16x8 a[MB][PX];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const int64_t m = m0 + 16 * b + l16;
+        row8(dy + (m < M ? m : 0) * N, n0, N, m < M, wide, a[b]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        u32x4 v0, v1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = (float)((p[i][j >> 3] >> (4 * (j & 7))) & 15u);
+          const float v = (q - zp[i]) * sc[i];
+          if (i < 4) v0[i] = __float_as_uint(v);
+          else v1[i - 4] = __float_as_uint(v);
+        }
+        bf16x8 b[PW];
+        if constexpr (PW == 1) {
+          u32x4 r;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v0[2 * i]), (__bf16)__uint_as_float(v0[2 * i + 1])});
+            r[2 + i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v1[2 * i]), (__bf16)__uint_as_float(v1[2 * i + 1])});
+          }
+          b[0] = __builtin_bit_cast(bf16x8, r);
+        } else {
+          bf16x8 all3[3];
+          split8(v0, v1, all3);
+#pragma unroll
+          for (int i = 0; i < PW; ++i) b[i] = all3[i];
+        }
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          if constexpr (NA == 1) acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[mb][0], b[0], acc[mb][j][0], 0, 0, 0);
+          else mfma_parts(a[mb], b, acc[mb][j]);
+        }
+      }
+    }
+
+    // register e: row 4 h + e, columns 16 l16 + j
+    float* out = part + (int64_t)blockIdx.y * M * K;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          f32x4 v;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] = NA == 1 ? acc[b][j + t][0][e] : acc[b][j + t][0][e] + acc[b][j + t][NA - 1][e];
+          *(f32x4*)(sums + (w * 16 + 4 * h + e) * kTStrip + 16 * l16 + j) = v;
+        }
+      __syncthreads();
+      for (int o = 4 * threadIdx.x; o < 16 * kTStrip; o += 4 * 64 * kTWaves) {
+        const int64_t m = m0 + 16 * b + o / kTStrip, k = k0 + o % kTStrip;
+        if (m >= M || k >= K) continue;
+        f32x4 v = *(const f32x4*)(sums + o);
+#pragma unroll
+        for (int i = 1; i < kTWaves; ++i) v += *(const f32x4*)(sums + i * 16 * kTStrip + o);
+        *(f32x4*)(out + m * K + k) = v;
+      }
+    }
+  }
+}
+
+// V elements of a row of the result (V 4: at 16-byte addresses): the partial sums, in
+// order, and the low-rank part of adapter l.  BACK: `out` is [L, R, C], otherwise [L, C, R].
+template <bool BACK, int V, typename TY>
+__device__ __forceinline__ void sum_elements(const float* part, int parts, int64_t M, int64_t C, const Adapters& ad,
+                                             TY* y, int64_t m, int64_t c, int l) {
+  typedef float fV __attribute__((ext_vector_type(V)));
+  const float* p = part + m * C + c;
+  fV v = *(const fV*)p;
+#pragma unroll 8
+  for (int s = 1; s < parts; ++s) v += *(const fV*)(p + (int64_t)s * M * C);
+  if (l >= 0) {
+    const float* low = ad.low + m * ad.rank;
+    if constexpr (!BACK) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += rank_dot(low, ad.out, ((int64_t)l * C + c + i) * ad.rank, ad.rank, ad.wide);
+    } else {
+      static_assert(!BACK || V == 4, "C is a multiple of 32");
+      fV d = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (ad.wide) {
+        const float* a = (const float*)ad.out + (int64_t)l * ad.rank * C + c;
+#pragma unroll 8
+        for (int r = 0; r < ad.rank; ++r) {
+          const f32x4 e = *(const f32x4*)(a + r * C);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = fmaf(low[r], e[i], d[i]);
+        }
+      } else {
+        const uint16_t* a = (const uint16_t*)ad.out + (int64_t)l * ad.rank * C + c;
+#pragma unroll 8
+        for (int r = 0; r < ad.rank; ++r) {
+          const u32x2 e = *(const u32x2*)(a + r * C);
+          d[0] = fmaf(low[r], bf16_lo(e.x), d[0]);
+          d[1] = fmaf(low[r], bf16_hi(e.x), d[1]);
+          d[2] = fmaf(low[r], bf16_lo(e.y), d[2]);
+          d[3] = fmaf(low[r], bf16_hi(e.y), d[3]);
+        }
+      }
+      v += d;
+    }
+  }
+  TY* out = y + m * C + c;
+  if constexpr (sizeof(TY) == 4) {
+    *(fV*)out = v;
+  } else if constexpr (V == 4) {
+    u32x2 b;
+    b.x = f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16;
+    b.y = f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16;
+    *(u32x2*)out = b;
+  } else {
+    *out = (TY)f32_to_bf16_bits(v[0]);
+  }
+}
+
+// A wave has 64 V columns of one row of the result at a time.
+template <bool BACK, int V, typename TY>
+__global__ __launch_bounds__(64) void k_w4a16_sum(const float* __restrict__ part, int parts, int64_t M, int64_t C,
+                                                  Adapters ad, TY* __restrict__ y) {
+  const int lane = threadIdx.x;
+  const int64_t strips = (C + 64 * V - 1) / (64 * V), tiles = M * strips;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t m = tile / strips, c = 64 * V * (tile % strips) + V * lane;
+    const int l = ad.count > 0 ? row_adapter(ad, m, lane) : -1;
+    if (c < C) sum_elements<BACK, V>(part, parts, M, C, ad, y, m, c, l);
+  }
+}
+
+template <bool BACK, int V>
+static hipError_t sum_go(const float* part, int parts, int64_t m, int64_t c, const Adapters& ad, void* y, int y_dtype,
+                         hipStream_t st) {
+  const int64_t tiles = m * ((c + 64 * V - 1) / (64 * V));
+  const dim3 grid((unsigned)(tiles < kTSumGrid ? tiles : kTSumGrid));
+  if (y_dtype == W4_F32) k_w4a16_sum<BACK, V><<<grid, 64, 0, st>>>(part, parts, m, c, ad, (float*)y);
+  else k_w4a16_sum<BACK, V><<<grid, 64, 0, st>>>(part, parts, m, c, ad, (uint16_t*)y);
+  return hipGetLastError();
+}
+
+size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
+                                  int y_dtype) {
+  return lora_plan(back, m, k, n, g, x_dtype, sz_dtype, y_dtype).bytes;
+}
+
+template <typename TX, typename TS, int PW, int MB>
+static hipError_t back_rows_go(const TilesArgs& a, const LoraPlan& p, float* part, hipStream_t st) {
+  constexpr size_t lds = (size_t)kTWaves * 16 * kTStrip * 4;
+  const int64_t tiles = p.strips * p.rows;
+  k_w4a16_back_rows<TX, TS, PW, MB>
+      <<<dim3((unsigned)(tiles < kTGrid ? tiles : kTGrid), (unsigned)p.parts), 64 * kTWaves, lds, st>>>(
+          (const TX*)a.x, a.m, a.n, a.packed, a.scales, a.zeros, a.k, a.g, (int)p.steps,
+          a.n * (int64_t)sizeof(TX) % 16 == 0, part);
+  return hipGetLastError();
+}
+
+template <typename TX, typename TS>
+static hipError_t back_rows(const TilesArgs& a, const LoraPlan& p, float* part, hipStream_t st) {
+  constexpr int PW = sizeof(TS) == 2 ? 2 : 3;
+  if (p.pw > 1) return back_rows_go<TX, TS, PW, 1>(a, p, part, st);
+  if constexpr (sizeof(TX) == 2) {
+    if (p.mb == 1) return back_rows_go<TX, TS, 1, 1>(a, p, part, st);
+    return back_rows_go<TX, TS, 1, 2>(a, p, part, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, const LoraOut& lo, void* ws,
+                             hipStream_t st) {
+  const LoraPlan p = lora_plan(args.back, args.m, args.k, args.n, args.g, x_dtype, args.sz_dtype, args.y_dtype);
+  TilesArgs a = args;
+  a.x = x;
+  a.mi = p.mi, a.pw = p.pw, a.parts = (int)p.parts, a.steps = (int)p.steps;
+  float* part = (float*)ws;
+  hipError_t e;
+  if (p.tiles) {
+    if (p.parts == 1) return launch_w4a16_tiles(a, lo, st);
+    a.y = ws, a.y_dtype = W4_F32;
+    e = launch_w4a16_tiles(a, LoraOut{}, st);
+  } else if (!a.back) {
+    return launch_w4a16_lora_rows(x, x_dtype, a.m, a.k, a.packed, a.scales, a.zeros, a.sz_dtype, a.n, a.g, a.y,
+                                  a.y_dtype, lo, st);
+  } else if (x_dtype == W4_F32) {
+    e = a.sz_dtype == W4_F16 ? back_rows<float, _Float16>(a, p, part, st) : back_rows<float, float>(a, p, part, st);
+  } else {
+    e = a.sz_dtype == W4_F16 ? back_rows<uint16_t, _Float16>(a, p, part, st) : back_rows<uint16_t, float>(a, p, part, st);
+  }
+  if (e != hipSuccess) return e;
+  const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
+                    (int)lo.count, lo.rank, lo.dtype == W4_F32};
+  if (a.back) return sum_go<true, 4>(part, (int)p.parts, a.m, a.k, ad, args.y, args.y_dtype, st);
+  if (a.n % 4 == 0) return sum_go<false, 4>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);
+  return sum_go<false, 1>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);
+}
+
+}  // namespace w4

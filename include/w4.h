@@ -433,24 +433,24 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *     u[m, r] = scaling[l] sum_k x[m, k] A[l, r, k]         (float32 [M, R])
  *     y[m, n] = sum_k x[m, k] W[n, k] + sum_r u[m, r] B[l, n, r]
  *   x, packed, scales, zeros and y as in w4a16_matmul (x W4_BF16 or W4_F32, y
- *   likewise).  No weight is rounded: as w4a16_grouped_matmul, sums are float32.
- *   u is an output; rows of no adapter are left as they were.
+ *   likewise).  u is an output; rows of no adapter are left as they were.
  *
  * w4a16_matmul_t -- dx [M, K] = dy [M, N] . W, the gradient of w4a16_matmul
- *   with respect to x.  dy and dx W4_BF16 or W4_F32; N > 0.  Sums are float32.
- *   With bf16 dy and bf16 dx the weight is rounded to bf16 before the product;
- *   otherwise it keeps the bits of (q - zp) s.
- *   workspace: device memory, 16-byte aligned, of at least
- *   w4a16_matmul_t_workspace_size bytes (W4_EINVAL below; 0: may be NULL), its
- *   contents ignored on entry and unspecified on return.  Calls that overlap on
- *   one workspace race.  The size depends only on the arguments, and is 0 for
- *   arguments the call rejects.
+ *   with respect to x.  dy and dx W4_BF16 or W4_F32; N > 0.
  *
  * w4a16_lora_matmul_t -- the gradient of w4a16_lora_matmul with respect to x:
  *     v[m, r]  = scaling[l] sum_n dy[m, n] B[l, n, r]       (float32 [M, R])
  *     dx[m, k] = sum_n dy[m, n] W[n, k] + sum_r v[m, r] A[l, r, k]
- *   v is an output; rows of no adapter are left as they were.  Otherwise as
- *   w4a16_matmul_t, and the same workspace.
+ *   v is an output; rows of no adapter are left as they were.
+ *
+ *   In all three sums are float32, and the result is rounded once.  With bf16 x (dy) and a
+ *   bf16 result the weight may be rounded to bf16 before the product, as in
+ *   w4a16_matmul; otherwise no operand loses bits that float32 has.
+ *   workspace: device memory, 16-byte aligned, of at least the bytes that
+ *   w4a16_lora_matmul_workspace_size and w4a16_matmul_t_workspace_size (for both
+ *   transposed products) give (W4_EINVAL below; 0: may be NULL), its contents ignored on
+ *   entry and unspecified on return.  Calls that overlap on one workspace
+ *   race.  The size depends only on the arguments, and is 0 for arguments the call rejects.
  *
  * lora_grads -- the gradients of the adapters, float32, from x's 8-bit
  *   checkpoint (xq [M, K], xs), dy and the two calls' u and v:
@@ -461,10 +461,13 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *
  * All are deterministic.  A row that holds an infinity may give NaN.
  */
+size_t w4a16_lora_matmul_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int x_dtype, int sz_dtype,
+                                        int y_dtype);
 int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                       const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
                       int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
-                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, hipStream_t stream);
+                      const int32_t* which, int64_t segments, float* u, void* y, int y_dtype, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
 size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype,
                                      int dx_dtype);
 int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
