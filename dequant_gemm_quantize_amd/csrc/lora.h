@@ -37,12 +37,20 @@ __device__ __forceinline__ int segments_before(const int* offsets, int segments,
   return n;
 }
 
-// The adapter of row m, or -1.  The same in every lane; all 64 lanes call it.
+// The adapter of row m, or -1.  The same in every lane; all 64 lanes call it.  The
+// adapters' numbers are loaded beside the offsets, not behind them.
 __device__ __forceinline__ int row_adapter(const Adapters& a, int64_t m, int lane) {
-  const int s = segments_before(a.offsets, a.segments, m, lane);
-  if (s >= a.segments || a.offsets[s] > m) return -1;
-  const int w = a.which[s];
-  return w >= 0 && w < a.count ? w : -1;
+  for (int base = 0; base < a.segments; base += kWave) {
+    const bool in = base + lane < a.segments;
+    const int begin = in ? a.offsets[base + lane] : 0, end = in ? a.offsets[base + lane + 1] : 0;
+    const int w = in ? a.which[base + lane] : -1;
+    const uint64_t past = __ballot(in && end > m);
+    if (past != 0) {  // the first segment that ends behind m
+      const int f = __builtin_ctzll(past), ad = __builtin_amdgcn_readlane(w, f);
+      return __builtin_amdgcn_readlane(begin, f) <= m && ad >= 0 && ad < a.count ? ad : -1;
+    }
+  }
+  return -1;
 }
 
 // A tile of bm rows of one segment, `width` tiles side by side.

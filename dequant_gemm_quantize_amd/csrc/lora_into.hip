@@ -4,9 +4,10 @@
 // float32, on v_mfma_f32_16x16x32_bf16: bf16 values as they are, float32 ones as the
 // exact sum of three bf16 values.  Rows of no adapter are left as they were.
 //
-// A workgroup has 16 MT rows of one segment and some ranks; its waves go through D in
-// turn, 128 values at a time, and add their sums through LDS.  Few rows take four
-// ranks a workgroup, so that more CUs read the adapter's rows.
+// A workgroup has 16 rows of one segment and some ranks; its waves go through D in
+// turn and add their sums through LDS.  Segments of a row or two (decode) leave
+// most of an MFMA's rows empty, and its loads, 16 rows each, with them: they take the
+// vector unit, four rows and four ranks a workgroup.
 //
 // Bound by latency where rows are few, by what a CU takes in from the L2 cache
 // where they are many: a wave has all loads of its 128 values under way before it waits.
@@ -36,61 +37,121 @@ __device__ __forceinline__ void into_store(const float* part, int waves, const S
 
 }  // namespace
 
-// x into A.  RANKS: 4 or 16 RB ranks.
+// x into A, 16 RB ranks a workgroup.
 constexpr int kDownWaves = 16;
-template <int MT, int RANKS, typename TX, typename TW>
+// The same for tiles of up to four rows, four ranks a workgroup: a lane has 8 values of D of
+// each, on the vector unit, so every load is 1 KB (2 KB) of one row.
+constexpr int kFewWaves = 8;
+template <typename T>
+__device__ __forceinline__ void values8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 b = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(b[i]), v[2 * i + 1] = bf16_hi(b[i]);
+  } else {
+    const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  }
+}
+template <int ROWS, typename TX, typename TW>
+__device__ __forceinline__ void few_rows(const TX* x, int64_t D, const TW* weights, int w, int lane, float* part) {
+  float acc[ROWS][4];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  for (int64_t d = 512 * w + 8 * lane; d < D; d += 512 * kFewWaves) {
+    float wv[4][8], xv[ROWS][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) values8(weights + j * D + d, wv[j]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) values8(x + i * D + d, xv[i]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][j] = fmaf(xv[i][e], wv[j][e], acc[i][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = wave_sum<64>(acc[i][j]);
+      if (lane == 0) part[(w * 4 + i) * 4 + j] = v;
+    }
+}
+
+template <typename TX, typename TW>
+__global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(
+    const TX* __restrict__ x, int64_t M, int64_t D, const TW* __restrict__ weights, int count, int R,
+    const float* __restrict__ scaling, const int* __restrict__ offsets, const int* __restrict__ which, int segments,
+    float* __restrict__ low, uint32_t rblocks, int64_t tiles) {
+  __shared__ float part[kFewWaves * 16];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    SegmentTile t;
+    if (!find_segment_tile(offsets, which, segments, count, (int)M, 4, rblocks, tile, lane, t)) return;
+    if (t.adapter < 0) continue;
+    const int rank0 = 4 * (int)t.side;  // R is a multiple of 8
+    const float c = scaling[t.adapter];
+    const TX* xt = x + t.m0 * D;
+    const TW* wt = weights + ((int64_t)t.adapter * R + rank0) * D;
+    if (t.rows == 1) few_rows<1>(xt, D, wt, w, lane, part);
+    else if (t.rows == 2) few_rows<2>(xt, D, wt, w, lane, part);
+    else if (t.rows == 3) few_rows<3>(xt, D, wt, w, lane, part);
+    else few_rows<4>(xt, D, wt, w, lane, part);
+    __syncthreads();
+    into_store<4, 4>(part, kFewWaves, t, rank0, R, c, low);
+    __syncthreads();  // the next tile writes part again
+  }
+}
+
+template <int RB, typename TX, typename TW>
 __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(
     const TX* __restrict__ x, int64_t M, int64_t D, const TW* __restrict__ weights, int count, int R,
     const float* __restrict__ scaling, const int* __restrict__ offsets, const int* __restrict__ which, int segments,
     float* __restrict__ low, uint32_t rblocks, int64_t tiles) {
-  constexpr int RB = RANKS < 16 ? 1 : RANKS / 16, RC = RANKS < 16 ? RANKS : 16;  // blocks of ranks, ranks of a block
+  constexpr int RANKS = 16 * RB;
   // values of D that a wave loads at a time: what its registers hold
-  constexpr int CK = MT * (int)sizeof(TX) + RB * (int)sizeof(TW) <= 4 ? 256 : 128;
-  extern __shared__ __attribute__((aligned(16))) float part[];                 // [waves][16 MT][RANKS]
+  constexpr int LB = (int)sizeof(TX) + RB * (int)sizeof(TW), CK = LB <= 4 ? 256 : LB <= 8 ? 128 : LB < 12 ? 64 : 32;
+  extern __shared__ __attribute__((aligned(16))) float part[];  // [waves][16][RANKS]
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, h = lane >> 4;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     SegmentTile t;
-    if (!find_segment_tile(offsets, which, segments, count, (int)M, 16 * MT, rblocks, tile, lane, t)) return;
+    if (!find_segment_tile(offsets, which, segments, count, (int)M, 16, rblocks, tile, lane, t)) return;
     if (t.adapter < 0) continue;
     const int rank0 = RANKS * (int)t.side;
     const float c = scaling[t.adapter];
     // rows and ranks past the end repeat the last: nobody stores what they give
-    const TX* xp[MT];
+    const TX* xp = x + (t.m0 + (l16 < t.rows ? l16 : t.rows - 1)) * D + 8 * h;
     const TW* wp[RB];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int row = 16 * i + l16;
-      xp[i] = x + (t.m0 + (row < t.rows ? row : t.rows - 1)) * D + 8 * h;
-    }
-#pragma unroll
     for (int i = 0; i < RB; ++i) {
-      const int r = rank0 + 16 * i + l16 % RC;
+      const int r = rank0 + 16 * i + l16;
       wp[i] = weights + ((int64_t)t.adapter * R + (r < R ? r : R - 1)) * D + 8 * h;
     }
-    f32x4 acc[MT][RB][2];
+    f32x4 acc[RB][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < RB; ++j) acc[i][j][0] = acc[i][j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < RB; ++j) acc[j][0] = acc[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto slices = [&](int64_t d0, auto count_c) {
       constexpr int n = decltype(count_c)::value;
-      bf16x8 a[n][MT][Parts<TX>::n], b[n][RB][Parts<TW>::n];
+      bf16x8 a[n][Parts<TX>::n], b[n][RB][Parts<TW>::n];
 #pragma unroll
       for (int q = 0; q < n; ++q) {
 #pragma unroll
         for (int j = 0; j < RB; ++j) load8(wp[j] + d0 + 32 * q, b[q][j]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) load8(xp[i] + d0 + 32 * q, a[q][i]);
+        load8(xp + d0 + 32 * q, a[q]);
       }
       __builtin_amdgcn_sched_barrier(0);  // every load is on its way before the first is waited for
 #pragma unroll
       for (int q = 0; q < n; ++q)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < RB; ++j) mfma_parts(a[q][i], b[q][j], acc[i][j]);
+        for (int j = 0; j < RB; ++j) mfma_parts(a[q], b[q][j], acc[j]);
     };
     for (int64_t d0 = CK * w; d0 < D; d0 += CK * kDownWaves) {
       if (d0 + CK <= D) {
@@ -100,17 +161,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(
       }
     }
     // lane holds rows 4 h + e of rank l16
-    if (l16 < RC) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < RB; ++j)
 #pragma unroll
-        for (int j = 0; j < RB; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part[(w * 16 * MT + 16 * i + 4 * h + e) * RANKS + 16 * j + l16] = acc[i][j][0][e] + acc[i][j][1][e];
-    }
+      for (int e = 0; e < 4; ++e) part[(w * 16 + 4 * h + e) * RANKS + 16 * j + l16] = acc[j][0][e] + acc[j][1][e];
     __syncthreads();
-    into_store<16 * MT, RANKS>(part, kDownWaves, t, rank0, R, c, low);
+    into_store<16, RANKS>(part, kDownWaves, t, rank0, R, c, low);
     __syncthreads();  // the next tile writes part again
   }
 }
@@ -225,18 +281,21 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
   }
 }
 
-template <int MT, int RANKS, typename TX, typename TW>
+template <int RB, typename TX, typename TW>
 static hipError_t down_go(const LoraInto& a, hipStream_t st) {
-  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
-  constexpr size_t lds = (size_t)kDownWaves * 16 * MT * RANKS * 4;
-  const hipError_t e = once_per_device(attr_done, [] {
-    return hipFuncSetAttribute((const void*)k_lora_down<MT, RANKS, TX, TW>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)lds);
-  });
-  if (e != hipSuccess) return e;
-  const int64_t rblocks = (a.rank + RANKS - 1) / RANKS;
-  const int64_t tiles = grouped_max_tiles(a.m, a.segments, 16 * MT) * rblocks;
-  k_lora_down<MT, RANKS, TX, TW><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kDownWaves, lds, st>>>(
+  constexpr size_t lds = (size_t)kDownWaves * 16 * 16 * RB * 4;  // at most 64 KB
+  const int64_t rblocks = (a.rank + 16 * RB - 1) / (16 * RB);
+  const int64_t tiles = grouped_max_tiles(a.m, a.segments, 16) * rblocks;
+  k_lora_down<RB, TX, TW><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kDownWaves, lds, st>>>(
+      (const TX*)a.x, a.m, a.d, (const TW*)a.weights, (int)a.count, a.rank, a.scaling, a.offsets, a.which,
+      (int)a.segments, a.low, (uint32_t)rblocks, tiles);
+  return hipGetLastError();
+}
+
+template <typename TX, typename TW>
+static hipError_t few_go(const LoraInto& a, hipStream_t st) {
+  const int64_t rblocks = a.rank / 4, tiles = grouped_max_tiles(a.m, a.segments, 4) * rblocks;
+  k_lora_down_few<TX, TW><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kFewWaves, 0, st>>>(
       (const TX*)a.x, a.m, a.d, (const TW*)a.weights, (int)a.count, a.rank, a.scaling, a.offsets, a.which,
       (int)a.segments, a.low, (uint32_t)rblocks, tiles);
   return hipGetLastError();
@@ -261,8 +320,17 @@ static hipError_t up_go(const LoraInto& a, hipStream_t st) {
 template <typename TX, typename TW>
 static hipError_t into_types(const LoraInto& a, hipStream_t st) {
   if (a.down) {
-    if (a.m <= 16 * a.segments || a.m <= 256) return down_go<1, 4, TX, TW>(a, st);
-    return a.rank > 16 ? down_go<1, 32, TX, TW>(a, st) : down_go<1, 16, TX, TW>(a, st);
+    // A CU takes in about 40 KB a us from the L2 cache, whatever the kernel, so the
+    // tile is the one whose rounds of 256 workgroups read the least: rows and ranks, D values each.  (us
+    // for 2048 rows of nine segments, D 4096, 64 ranks in blocks of 16, 32 and 64: 28, 27 and 21.)
+    auto rounds = [&](int rows, int ranks) {
+      const int64_t tiles = grouped_max_tiles(a.m, a.segments, rows) * ((a.rank + ranks - 1) / ranks);
+      return (tiles + 255) / 256 * (rows + ranks);
+    };
+    const int64_t few = rounds(4, 4), r1 = rounds(16, 16), r2 = rounds(16, 32), r4 = rounds(16, 64);
+    if (5 * few <= 4 * r1 && 5 * few <= 4 * r2 && 5 * few <= 4 * r4) return few_go<TX, TW>(a, st);
+    if (r1 <= r2 && r1 <= r4) return down_go<1, TX, TW>(a, st);
+    return r2 <= r4 ? down_go<2, TX, TW>(a, st) : down_go<4, TX, TW>(a, st);
   }
   // 16 rows of dy by byte offsets below 2^31
   if (a.d * (int64_t)sizeof(TX) % 16 == 0 && a.d * (int64_t)sizeof(TX) < ((int64_t)1 << 27)) return up_go<TX, TW, true>(a, st);

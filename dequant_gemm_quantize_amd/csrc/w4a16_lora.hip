@@ -17,6 +17,7 @@
 // Rounding: bf16 x with a bf16 result takes, in tiles and back, a weight rounded to bf16, as
 // w4a16_matmul does (half a step, 2^-8 at most, beside the result's own).  Otherwise the weight is the
 // exact sum of bf16 parts, two with fp16 scales (15 bits), three with float32 ones (24).
+#include "lds_gemm.h"
 #include "lora.h"
 #include "w4_internal.h"
 
@@ -24,15 +25,10 @@ namespace w4 {
 
 namespace {
 
-constexpr int kTWaves = 4;
+constexpr int kTWaves = 8;
 constexpr int kTStrip = 256;  // columns of a workgroup
 constexpr int64_t kTGrid = 1 << 20;  // workgroups of a part; more tiles than that loop
 constexpr int64_t kTSumGrid = 1 << 22;
-
-template <typename TS>
-__device__ __forceinline__ float t_scale(const void* p, int64_t i) {
-  return ScaleT<TS>::load(p, i);
-}
 
 // How a call is computed: in tiles (w4a16_tiles.h) or by a kernel for few rows, and
 // how it splits the sum: parts of `steps` steps of 64 or 32.
@@ -58,7 +54,11 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
   p.parts = 1;
   // Rows of x start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
   // below 2^31 bytes; 2^16 blocks of 32 columns; forward, an even number of fp16 scales.
-  p.tiles = x_dtype == W4_BF16 && m > 32 && d % 8 == 0 && d <= ((int64_t)1 << 21) &&
+  // Few rows, forward: us of the few-row kernel / tiles: [4096, 11008] 64 rows 27 / 31, 96 rows 50 / 32;
+  // [11008, 4096] 64 rows 32 / 36, 96 rows 46 / 37; [4096, 4096] 128 rows 22 / 24, 200 rows
+  // 44 / 27; [2050, 2048] 300 rows 28 / 35.
+  const bool few = back ? m <= 32 : m <= 64 || m * n * k <= ((int64_t)1 << 31);
+  p.tiles = x_dtype == W4_BF16 && !few && d % 8 == 0 && d <= ((int64_t)1 << 21) &&
             (back || sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
   if (p.tiles) {
     p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
@@ -71,8 +71,10 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
     p.mb = exact || m <= 16 ? 1 : 2;
     p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
     p.strips = (c + kTStrip - 1) / kTStrip;
-    const int64_t all = (d + 31) / 32, parts = 1024 / (p.rows * p.strips);
-    split(p, all, parts < all / (2 * kTWaves) ? parts : all / (2 * kTWaves));
+    // a workgroup a CU; two steps a wave at least, for the partial sums cost as much as
+    // the codes with 16 rows and 44 parts of [11008, 4096]
+    const int64_t all = (d + 31) / 32, parts = 256 / (p.rows * p.strips), most = (all + 2 * kTWaves - 1) / (2 * kTWaves);
+    split(p, all, parts < most ? parts : most);
     p.bytes = (size_t)p.parts * (size_t)m * (size_t)c * 4;
   }
   return p;
@@ -82,24 +84,29 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
 
 // PW: bf16 parts of a weight.
 template <typename TX, typename TS, int PW, int MB>
-__global__ __launch_bounds__(64 * kTWaves) void k_w4a16_back_rows(
+__global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
     const TX* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
     const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, int wide,
     float* __restrict__ part) {
   constexpr int PX = Parts<TX>::n;
   constexpr int NA = PX + PW > 2 ? 2 : 1;  // sums: the upper parts' and the others'
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][16][256]
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves / 2][16][256], then the waves' scales
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, h = lane >> 4;
+  float* mine = sums + kTWaves / 2 * 16 * kTStrip + w * 512;  // [scales, zero-points][groups of the strip][32 rows]
   const int64_t strips = (K + kTStrip - 1) / kTStrip, tiles = strips * ((M + 16 * MB - 1) / (16 * MB));
+  const int64_t ng = K / g, half = K / 2;
+  const int64_t all = (N + 31) / 32, first = (int64_t)steps * blockIdx.y;
+  const int64_t last = first + steps < all ? first + steps : all;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t k0 = kTStrip * (tile % strips), m0 = 16 * MB * (tile / strips);
     const int64_t col = k0 + 16 * l16;
-    const int64_t cc = col < K ? col : 0;  // lanes past K compute what nobody stores
-    const int64_t ng = K / g, gi = cc / g, half = K / 2;
-    const int64_t all = (N + 31) / 32, first = (int64_t)steps * blockIdx.y;
-    const int64_t last = first + steps < all ? first + steps : all;
+    const int64_t cc = col < K ? col : k0;  // lanes past K compute what nobody stores
+    // The strip's groups, eight at most.  One value a lane, 64 at a time: loaded where they are
+    // used, 16 loads of which 16 lanes get the same, they took longer than the codes.
+    const int64_t g0 = k0 / g, g1 = ((k0 + kTStrip < K ? k0 + kTStrip : K) - 1) / g;
+    const int values = 32 * (int)(g1 - g0 + 1), mygroup = (int)(cc / g - g0);
 
     f32x4 acc[MB][16][NA];
 #pragma unroll
@@ -109,42 +116,96 @@ __global__ __launch_bounds__(64 * kTWaves) void k_w4a16_back_rows(
 #pragma unroll
         for (int a = 0; a < NA; ++a) acc[b][j][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int64_t s = first + w; s < last; s += kTWaves) {
-      const int64_t n0 = 32 * s + 8 * h;
+    struct Step {
       u32x2 p[8];
-      float sc[8], zp[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t n = n0 + i < N ? n0 + i : N - 1;  // dy is zero there
-        p[i] = *(const u32x2*)(packed + n * half + cc / 2);
-        sc[i] = t_scale<TS>(scales, n * ng + gi);
-        zp[i] = t_scale<TS>(zeros, n * ng + gi);
-      }
+      uint32_t s[4], z[4];
       bf16x8 a[MB][PX];
+    };
+    // 32-bit offsets from a step's first weight row; rows past the last read as zero
+    const uint32_t po = (uint32_t)(8 * h) * (uint32_t)half + (uint32_t)(cc / 2);
+    uint32_t so[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = lane + 64 * i;
+      so[i] = ((uint32_t)(v & 31) * (uint32_t)ng + (uint32_t)g0 + (v < values ? v >> 5 : 0)) * (uint32_t)sizeof(TS);
+    }
+    const TX* dyp = dy + (m0 + l16 < M ? m0 + l16 : M - 1) * N;
+    auto load = [&](int64_t st, Step& r) {
+      const int64_t n0 = st < last ? 32 * st : N;  // steps past the last: nothing
+      const uint32_t have = (uint32_t)(N - n0 < 32 ? N - n0 : 32);
+      const __amdgpu_buffer_rsrc_t pr = buf_rsrc_n(uniform_ptr(packed + n0 * half), have * (uint32_t)half);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        r.p[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(pr, po + i * (uint32_t)half, 0, 0));
+      const uint32_t bytes = have * (uint32_t)ng * (uint32_t)sizeof(TS);
+      const int64_t at = n0 * ng * (int64_t)sizeof(TS);
+      const __amdgpu_buffer_rsrc_t sr = buf_rsrc_n(uniform_ptr((const char*)scales + at), bytes);
+      const __amdgpu_buffer_rsrc_t zr = buf_rsrc_n(uniform_ptr((const char*)zeros + at), bytes);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (64 * i >= values) break;  // the same in every lane
+        if constexpr (sizeof(TS) == 2) {
+          r.s[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], 0, 0);
+          r.z[i] = __builtin_amdgcn_raw_buffer_load_b16(zr, so[i], 0, 0);
+        } else {
+          r.s[i] = __builtin_amdgcn_raw_buffer_load_b32(sr, so[i], 0, 0);
+          r.z[i] = __builtin_amdgcn_raw_buffer_load_b32(zr, so[i], 0, 0);
+        }
+      }
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
         const int64_t m = m0 + 16 * b + l16;
-        row8(dy + (m < M ? m : 0) * N, n0, N, m < M, wide, a[b]);
+        row8(MB == 1 ? dyp : dy + (m < M ? m : 0) * N, n0 + 8 * h, N, m < M, wide, r.a[b]);
       }
+    };
+    auto value = [](uint32_t v) {
+      if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+      else return __uint_as_float(v);
+    };
+    auto compute = [&](const Step& r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (64 * i >= values) break;
+        mine[lane + 64 * i] = value(r.s[i]), mine[256 + lane + 64 * i] = value(r.z[i]);
+      }
+      __builtin_amdgcn_wave_barrier();  // LDS operations of a wave complete in order
+      const float* sp = mine + 32 * mygroup + 8 * h;
+      const f32x4 s0 = *(const f32x4*)sp, s1 = *(const f32x4*)(sp + 4);
+      f32x4 z0 = *(const f32x4*)(sp + 256), z1 = *(const f32x4*)(sp + 260);
+      __builtin_amdgcn_wave_barrier();
+      if constexpr (PW == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z0[i] *= -s0[i], z1[i] *= -s1[i];
+      }
+      uint32_t lo[8], hi[8];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
+        if (j % 8 == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            lo[i] = r.p[i][j >> 3] & 0x0f0f0f0fu;
+            hi[i] = (r.p[i][j >> 3] >> 4) & 0x0f0f0f0fu;
+            asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again
+          }
+        }
         u32x4 v0, v1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float q = (float)((p[i][j >> 3] >> (4 * (j & 7))) & 15u);
-          const float v = (q - zp[i]) * sc[i];
+          const float q = (float)(uint8_t)((j & 1 ? hi : lo)[i] >> (8 * (j >> 1 & 3)));
+          const float s = i < 4 ? s0[i] : s1[i - 4], z = i < 4 ? z0[i] : z1[i - 4];
+          const float v = PW == 1 ? fmaf(q, s, z) : (q - z) * s;
           if (i < 4) v0[i] = __float_as_uint(v);
           else v1[i - 4] = __float_as_uint(v);
         }
         bf16x8 b[PW];
         if constexpr (PW == 1) {
-          u32x4 r;
+          u32x4 e;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v0[2 * i]), (__bf16)__uint_as_float(v0[2 * i + 1])});
-            r[2 + i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v1[2 * i]), (__bf16)__uint_as_float(v1[2 * i + 1])});
+            e[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v0[2 * i]), (__bf16)__uint_as_float(v0[2 * i + 1])});
+            e[2 + i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v1[2 * i]), (__bf16)__uint_as_float(v1[2 * i + 1])});
           }
-          b[0] = __builtin_bit_cast(bf16x8, r);
+          b[0] = __builtin_bit_cast(bf16x8, e);
         } else {
           bf16x8 all3[3];
           split8(v0, v1, all3);
@@ -153,102 +214,146 @@ __global__ __launch_bounds__(64 * kTWaves) void k_w4a16_back_rows(
         }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          if constexpr (NA == 1) acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[mb][0], b[0], acc[mb][j][0], 0, 0, 0);
-          else mfma_parts(a[mb], b, acc[mb][j]);
+          if constexpr (NA == 1)
+            acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r.a[mb][0], b[0], acc[mb][j][0], 0, 0, 0);
+          else mfma_parts(r.a[mb], b, acc[mb][j]);
         }
+        __builtin_amdgcn_sched_barrier(0);  // one column's values at a time: registers
+      }
+    };
+    Step one;
+    if constexpr (NA == 2 || MB == 2) {  // their sums leave no registers for a second step
+      for (int64_t st = first + w; st < last; st += kTWaves) {
+        load(st, one);
+        asm volatile("" ::: "memory");
+        compute(one);
+      }
+    } else {
+      // the next step's loads are under way while one is computed; the compiler would sink them to their use
+      Step two;
+      load(first + w, one);
+      for (int64_t st = first + w; st < last; st += 2 * kTWaves) {
+        load(st + kTWaves, two);
+        asm volatile("" ::: "memory");
+        compute(one);
+        __builtin_amdgcn_sched_barrier(0);
+        load(st + 2 * kTWaves, one);
+        asm volatile("" ::: "memory");
+        compute(two);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 
-    // register e: row 4 h + e, columns 16 l16 + j
+    // register e: row 4 h + e, columns 16 l16 + j.  The upper four waves' sums go to
+    // LDS, the lower four add their own, and all threads add the four.
     float* out = part + (int64_t)blockIdx.y * M * K;
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
+      float* place = sums + (w & (kTWaves / 2 - 1)) * 16 * kTStrip + 4 * h * kTStrip + 16 * l16;
+      auto sum4 = [&](int e, int j) {
+        f32x4 v;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] = NA == 1 ? acc[b][j + t][0][e] : acc[b][j + t][0][e] + acc[b][j + t][NA - 1][e];
+        return v;
+      };
       __syncthreads();
+      if (w >= kTWaves / 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          f32x4 v;
+          for (int j = 0; j < 16; j += 4) *(f32x4*)(place + e * kTStrip + j) = sum4(e, j);
+      }
+      __syncthreads();
+      if (w < kTWaves / 2) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) v[t] = NA == 1 ? acc[b][j + t][0][e] : acc[b][j + t][0][e] + acc[b][j + t][NA - 1][e];
-          *(f32x4*)(sums + (w * 16 + 4 * h + e) * kTStrip + 16 * l16 + j) = v;
-        }
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            f32x4* at = (f32x4*)(place + e * kTStrip + j);
+            *at = *at + sum4(e, j);
+          }
+      }
       __syncthreads();
       for (int o = 4 * threadIdx.x; o < 16 * kTStrip; o += 4 * 64 * kTWaves) {
         const int64_t m = m0 + 16 * b + o / kTStrip, k = k0 + o % kTStrip;
         if (m >= M || k >= K) continue;
         f32x4 v = *(const f32x4*)(sums + o);
 #pragma unroll
-        for (int i = 1; i < kTWaves; ++i) v += *(const f32x4*)(sums + i * 16 * kTStrip + o);
+        for (int i = 1; i < kTWaves / 2; ++i) v += *(const f32x4*)(sums + i * 16 * kTStrip + o);
         *(f32x4*)(out + m * K + k) = v;
       }
     }
   }
 }
 
-// V elements of a row of the result (V 4: at 16-byte addresses): the partial sums, in
-// order, and the low-rank part of adapter l.  BACK: `out` is [L, R, C], otherwise [L, C, R].
-template <bool BACK, int V, typename TY>
-__device__ __forceinline__ void sum_elements(const float* part, int parts, int64_t M, int64_t C, const Adapters& ad,
-                                             TY* y, int64_t m, int64_t c, int l) {
-  typedef float fV __attribute__((ext_vector_type(V)));
-  const float* p = part + m * C + c;
-  fV v = *(const fV*)p;
-#pragma unroll 8
-  for (int s = 1; s < parts; ++s) v += *(const fV*)(p + (int64_t)s * M * C);
-  if (l >= 0) {
-    const float* low = ad.low + m * ad.rank;
-    if constexpr (!BACK) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += rank_dot(low, ad.out, ((int64_t)l * C + c + i) * ad.rank, ad.rank, ad.wide);
-    } else {
-      static_assert(!BACK || V == 4, "C is a multiple of 32");
-      fV d = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (ad.wide) {
-        const float* a = (const float*)ad.out + (int64_t)l * ad.rank * C + c;
-#pragma unroll 8
-        for (int r = 0; r < ad.rank; ++r) {
-          const f32x4 e = *(const f32x4*)(a + r * C);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = fmaf(low[r], e[i], d[i]);
-        }
-      } else {
-        const uint16_t* a = (const uint16_t*)ad.out + (int64_t)l * ad.rank * C + c;
-#pragma unroll 8
-        for (int r = 0; r < ad.rank; ++r) {
-          const u32x2 e = *(const u32x2*)(a + r * C);
-          d[0] = fmaf(low[r], bf16_lo(e.x), d[0]);
-          d[1] = fmaf(low[r], bf16_hi(e.x), d[1]);
-          d[2] = fmaf(low[r], bf16_lo(e.y), d[2]);
-          d[3] = fmaf(low[r], bf16_hi(e.y), d[3]);
-        }
-      }
-      v += d;
-    }
-  }
-  TY* out = y + m * C + c;
-  if constexpr (sizeof(TY) == 4) {
-    *(fV*)out = v;
-  } else if constexpr (V == 4) {
-    u32x2 b;
-    b.x = f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16;
-    b.y = f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16;
-    *(u32x2*)out = b;
-  } else {
-    *out = (TY)f32_to_bf16_bits(v[0]);
-  }
-}
-
-// A wave has 64 V columns of one row of the result at a time.
+// A wave has 64 V columns of one row of the result at a time (V 4: at 16-byte
+// addresses): the partial sums, in order, and the low-rank part of the row's
+// adapter.  BACK: `out` is [L, R, C], otherwise [L, C, R].
 template <bool BACK, int V, typename TY>
 __global__ __launch_bounds__(64) void k_w4a16_sum(const float* __restrict__ part, int parts, int64_t M, int64_t C,
                                                   Adapters ad, TY* __restrict__ y) {
+  typedef float fV __attribute__((ext_vector_type(V)));
   const int lane = threadIdx.x;
   const int64_t strips = (C + 64 * V - 1) / (64 * V), tiles = M * strips;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t m = tile / strips, c = 64 * V * (tile % strips) + V * lane;
+    const bool in = c < C;
+    const float* p = part + m * C + (in ? c : 0);
+    // eight loads of the sums are under way while the row's adapter is found
+    fV first[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) first[s] = *(const fV*)(p + (int64_t)(s < parts ? s : 0) * M * C);
+    asm volatile("" ::: "memory");
     const int l = ad.count > 0 ? row_adapter(ad, m, lane) : -1;
-    if (c < C) sum_elements<BACK, V>(part, parts, M, C, ad, y, m, c, l);
+    fV v = first[0];
+#pragma unroll
+    for (int s = 1; s < 8; ++s)
+      if (s < parts) v += first[s];
+#pragma unroll 8
+    for (int s = 8; s < parts; ++s) v += *(const fV*)(p + (int64_t)s * M * C);
+    if (in && l >= 0) {
+      const float* low = ad.low + m * ad.rank;
+      if constexpr (!BACK) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += rank_dot(low, ad.out, ((int64_t)l * C + c + i) * ad.rank, ad.rank, ad.wide);
+      } else {
+        static_assert(!BACK || V == 4, "C is a multiple of 32");
+        fV d = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (ad.wide) {
+          const float* a = (const float*)ad.out + (int64_t)l * ad.rank * C + c;
+#pragma unroll 8
+          for (int r = 0; r < ad.rank; ++r) {
+            const f32x4 e = *(const f32x4*)(a + r * C);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = fmaf(low[r], e[i], d[i]);
+          }
+        } else {
+          const uint16_t* a = (const uint16_t*)ad.out + (int64_t)l * ad.rank * C + c;
+#pragma unroll 8
+          for (int r = 0; r < ad.rank; ++r) {
+            const u32x2 e = *(const u32x2*)(a + r * C);
+            d[0] = fmaf(low[r], bf16_lo(e.x), d[0]);
+            d[1] = fmaf(low[r], bf16_hi(e.x), d[1]);
+            d[2] = fmaf(low[r], bf16_lo(e.y), d[2]);
+            d[3] = fmaf(low[r], bf16_hi(e.y), d[3]);
+          }
+        }
+        v += d;
+      }
+    }
+    if (in) {
+      TY* out = y + m * C + c;
+      if constexpr (sizeof(TY) == 4) {
+        *(fV*)out = v;
+      } else if constexpr (V == 4) {
+        u32x2 b;
+        b.x = f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16;
+        b.y = f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16;
+        *(u32x2*)out = b;
+      } else {
+        *out = (TY)f32_to_bf16_bits(v[0]);
+      }
+    }
   }
 }
 
@@ -269,7 +374,13 @@ size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, in
 
 template <typename TX, typename TS, int PW, int MB>
 static hipError_t back_rows_go(const TilesArgs& a, const LoraPlan& p, float* part, hipStream_t st) {
-  constexpr size_t lds = (size_t)kTWaves * 16 * kTStrip * 4;
+  static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
+  constexpr size_t lds = (size_t)kTWaves / 2 * 16 * kTStrip * 4 + (size_t)kTWaves * 2048;
+  const hipError_t e = once_per_device(attr_done, [] {
+    return hipFuncSetAttribute((const void*)k_w4a16_back_rows<TX, TS, PW, MB>,
+                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  });
+  if (e != hipSuccess) return e;
   const int64_t tiles = p.strips * p.rows;
   k_w4a16_back_rows<TX, TS, PW, MB>
       <<<dim3((unsigned)(tiles < kTGrid ? tiles : kTGrid), (unsigned)p.parts), 64 * kTWaves, lds, st>>>(
