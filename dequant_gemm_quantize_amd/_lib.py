@@ -57,7 +57,7 @@ SIGNATURES = [
     ("w4a16_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP, ctypes.c_size_t, _VP]),
     ("w4a16_lora_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP,
                                  _VP, _VP, _I64, _VP, _VP, _I, _VP, ctypes.c_size_t, _VP]),
-    ("lora_grads_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I32]),
+    ("lora_grads_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I, _I64, _I32]),
     ("lora_grads", _I, [_VP, _VP, _I64, _I64, _VP, _I, _I64, _VP, _VP, _VP, _VP, _I64, _I64, _I32, _VP, _VP, _VP,
                         ctypes.c_size_t, _VP]),
     ("w4_status_string", ctypes.c_char_p, [_I]),
@@ -762,9 +762,10 @@ def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Te
     return dx
 
 
-def lora_grads_workspace_size(m: int, k: int, n: int, adapters: int, rank: int) -> int:
+def lora_grads_workspace_size(m: int, k: int, n: int, adapters: int, rank: int,
+                              dy_dtype: torch.dtype = torch.bfloat16) -> int:
     """Bytes of workspace that lora_grads needs for this shape (0: none)."""
-    return int(load().lora_grads_workspace_size(m, k, n, adapters, rank))
+    return int(load().lora_grads_workspace_size(m, k, n, _dtype_code(dy_dtype), adapters, rank))
 
 
 def lora_grads(xq: torch.Tensor, xs: torch.Tensor, dy: torch.Tensor, u: torch.Tensor, v: torch.Tensor,
@@ -793,7 +794,7 @@ def lora_grads(xq: torch.Tensor, xs: torch.Tensor, dy: torch.Tensor, u: torch.Te
     else:
         dev = _device(xq, xs, dy, u, v, offsets, adapters)
         da, db = u.new_empty(shapes[0]), u.new_empty(shapes[1])
-    nbytes = load().lora_grads_workspace_size(m, k, n, num_adapters, rank)
+    nbytes = load().lora_grads_workspace_size(m, k, n, _DT[dy.dtype], num_adapters, rank)
     ws = u.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     _launch(dev, load().lora_grads, _ptr(xq), _ptr(xs), m, k, _ptr(dy), _dtype_code(dy.dtype), n, _ptr(u), _ptr(v),
             _ptr(offsets), _ptr(adapters), s, num_adapters, rank, _ptr(da), _ptr(db),

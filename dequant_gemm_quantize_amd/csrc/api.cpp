@@ -754,11 +754,12 @@ static int check_grads(const char* fn, int64_t m, int64_t k, int64_t n, int64_t 
   return check_adapters(fn, m, k, n, adapters, rank, segments);
 }
 
-size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank) {
-  const bool valid = check_grads("lora_grads_workspace_size", m, k, n, adapters, rank, 0) == W4_OK;
+size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int dy_dtype, int64_t adapters, int32_t rank) {
+  static const char* fn = "lora_grads_workspace_size";
+  const bool valid = check_grads(fn, m, k, n, adapters, rank, 0) == W4_OK && check_x(fn, "dy", dy_dtype) == W4_OK;
   ok();
   if (!valid || adapters == 0) return 0;
-  return w4::lora_grads_workspace_bytes(m, k, n, adapters, rank);
+  return w4::lora_grads_workspace_bytes(m, k, n, dy_dtype, adapters, rank);
 }
 
 int lora_grads(const int8_t* xq, const float* xs, int64_t m, int64_t k, const void* dy, int dy_dtype, int64_t n,
@@ -780,7 +781,7 @@ int lora_grads(const int8_t* xq, const float* xs, int64_t m, int64_t k, const vo
     W4_TRY(check_ptr4(fn, "offsets", offsets));
     W4_TRY(check_ptr4(fn, "which", which));
   }
-  const size_t need = w4::lora_grads_workspace_bytes(m, k, n, adapters, rank);
+  const size_t need = w4::lora_grads_workspace_bytes(m, k, n, dy_dtype, adapters, rank);
   if (need > 0) {
     W4_TRY(check_ptr(fn, "workspace", workspace));
     if (workspace_bytes < need)

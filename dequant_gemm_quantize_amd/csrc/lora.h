@@ -135,26 +135,27 @@ __device__ __forceinline__ void pack8(const float (&v)[8], bf16x8 (&out)[3]) {
   split8(a, b, out);
 }
 
+// 16 bytes at an address that is a multiple of the element's size only (global loads take any).
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+__device__ __forceinline__ void load8_any(const uint16_t* p, bf16x8 (&out)[1]) {
+  out[0] = __builtin_bit_cast(bf16x8, (u32x4) * (const u32x4_at2*)p);
+}
+__device__ __forceinline__ void load8_any(const float* p, bf16x8 (&out)[3]) {
+  split8(*(const u32x4_at4*)p, *(const u32x4_at4*)(p + 4), out);
+}
+
 // 8 consecutive values of a row at d, zeros from D on or where the row is not real.
-// wide: rows start at 16-byte addresses (the same in every lane).
 template <typename TX>
-__device__ __forceinline__ void row8(const TX* row, int64_t d, int64_t D, bool real, bool wide,
-                                     bf16x8 (&out)[Parts<TX>::n]) {
-  if (wide) {
-    if (real && d + 8 <= D) {
-      load8(row + d, out);
-      return;
-    }
-    if (!real || d >= D) {
+__device__ __forceinline__ void row8(const TX* row, int64_t d, int64_t D, bool real, bf16x8 (&out)[Parts<TX>::n]) {
+  if (real && d + 8 <= D) {
+    load8_any(row + d, out);
+  } else {
+    TX v[8];
 #pragma unroll
-      for (int p = 0; p < Parts<TX>::n; ++p) out[p] = zero8();
-      return;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = real && d + i < D ? row[d + i] : (TX)0;
+    pack8(v, out);
   }
-  TX v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = real && d + i < D ? row[d + i] : (TX)0;
-  pack8(v, out);
 }
 
 // acc += a b, 16 x 16 with 32 products each, of operands in parts.  The upper

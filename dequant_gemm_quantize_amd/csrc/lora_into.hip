@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
       bf16x8 a[Q][PX];
       if constexpr (!WIDE) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) row8(xt + (l16 < t.rows ? l16 : 0) * D, d0 + 32 * q + 8 * h, D, true, false, a[q]);
+        for (int q = 0; q < Q; ++q) row8(xt + (l16 < t.rows ? l16 : 0) * D, d0 + 32 * q + 8 * h, D, true, a[q]);
       }
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
       const uint8_t* place = mine + stage * P::STAGE;

@@ -208,7 +208,7 @@ struct LoraGrads {
   float* db;
   void* ws;
 };
-size_t lora_grads_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t count, int rank);
+size_t lora_grads_workspace_bytes(int64_t m, int64_t k, int64_t n, int dy_dtype, int64_t count, int rank);
 hipError_t launch_lora_grads(const LoraGrads& a, hipStream_t st);
 // Limits of the adapters.
 constexpr int64_t kLoraMaxRows = (int64_t)1 << 24;

@@ -86,7 +86,7 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
 template <typename TX, typename TS, int PW, int MB>
 __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
     const TX* __restrict__ dy, int64_t M, int64_t N, const uint8_t* __restrict__ packed,
-    const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps, int wide,
+    const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps,
     float* __restrict__ part) {
   constexpr int PX = Parts<TX>::n;
   constexpr int NA = PX + PW > 2 ? 2 : 1;  // sums: the upper parts' and the others'
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
         const int64_t m = m0 + 16 * b + l16;
-        row8(MB == 1 ? dyp : dy + (m < M ? m : 0) * N, n0 + 8 * h, N, m < M, wide, r.a[b]);
+        row8(MB == 1 ? dyp : dy + (m < M ? m : 0) * N, n0 + 8 * h, N, m < M, r.a[b]);
       }
     };
     auto value = [](uint32_t v) {
@@ -384,8 +384,7 @@ static hipError_t back_rows_go(const TilesArgs& a, const LoraPlan& p, float* par
   const int64_t tiles = p.strips * p.rows;
   k_w4a16_back_rows<TX, TS, PW, MB>
       <<<dim3((unsigned)(tiles < kTGrid ? tiles : kTGrid), (unsigned)p.parts), 64 * kTWaves, lds, st>>>(
-          (const TX*)a.x, a.m, a.n, a.packed, a.scales, a.zeros, a.k, a.g, (int)p.steps,
-          a.n * (int64_t)sizeof(TX) % 16 == 0, part);
+          (const TX*)a.x, a.m, a.n, a.packed, a.scales, a.zeros, a.k, a.g, (int)p.steps, part);
   return hipGetLastError();
 }
 

@@ -478,7 +478,7 @@ int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, cons
                         int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
                         const int32_t* which, int64_t segments, float* v, void* dx, int dx_dtype, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
-size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int64_t adapters, int32_t rank);
+size_t lora_grads_workspace_size(int64_t m, int64_t k, int64_t n, int dy_dtype, int64_t adapters, int32_t rank);
 int lora_grads(const int8_t* xq, const float* xs, int64_t m, int64_t k, const void* dy, int dy_dtype, int64_t n,
                const float* u, const float* v, const int32_t* offsets, const int32_t* which, int64_t segments,
                int64_t adapters, int32_t rank, float* da, float* db, void* workspace, size_t workspace_bytes,
