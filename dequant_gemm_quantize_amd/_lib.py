@@ -8,6 +8,7 @@ tensor is not on the GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -633,6 +634,9 @@ def dequant_checkpoint_int8(xq: torch.Tensor, xs: torch.Tensor, out_dtype: torch
     return out
 
 
+# The wrappers of these products ask each tensor's shape and type once, look for
+# the words of an error (the _expect calls) only behind a comparison that
+# failed, and keep the workspaces' sizes, which depend on the arguments alone.
 def _check_segments(offsets: torch.Tensor, adapters: torch.Tensor) -> int:
     """offsets int32 [S + 1] and adapters int32 [S]; returns S."""
     if adapters.dim() != 1:
@@ -648,26 +652,47 @@ def _check_lora(a, b, scaling, offsets, adapters, k: int, n: int) -> Tuple[int, 
     """a [L, R, K] and b [L, N, R] of one dtype, scaling float32 [L], and the segments; returns (L, R, S)."""
     if a.dim() != 3:
         raise ValueError(f"a must be a 3-D tensor, got {a.dim()} dimensions")
-    count, rank = a.shape[0], a.shape[1]
-    if a.shape != (count, rank, k) or a.dtype not in Y_DTYPES:
+    count, rank, width = a.shape
+    dt = a.dtype
+    if width != k or (dt is not torch.bfloat16 and dt is not torch.float32):
         _expect(a, "a", (count, rank, k), Y_DTYPES)
-    if b.shape != (count, n, rank) or b.dtype is not a.dtype:
-        _expect(b, "b", (count, n, rank), (a.dtype,))
-    if scaling.shape != (count,) or scaling.dtype is not torch.float32:
+    if b.dtype is not dt or b.shape != (count, n, rank):
+        _expect(b, "b", (count, n, rank), (dt,))
+    if scaling.dtype is not torch.float32 or scaling.shape != (count,):
         _expect(scaling, "scaling", (count,), (torch.float32,))
     return count, rank, _check_segments(offsets, adapters)
 
 
 def _int4_product(x, name: str, packed, scales, zeros, group_size: int, transposed: bool) -> Tuple[int, int, int]:
     """x [M, K] (or dy [M, N]) against an INT4 weight; returns (M, K, N)."""
-    m, d = _matrix(x, name)
-    if x.dtype not in Y_DTYPES:
+    if x.dim() != 2 or packed.dim() != 2:
+        _matrix(x, name), _matrix(packed, "packed")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise ValueError(f"{name} has dtype {x.dtype}, expected float32 or bfloat16")
-    k = 2 * _matrix(packed, "packed")[1]
-    n = _check_weights(packed, scales, zeros, k, group_size)
+    m, d = x.shape
+    n, half = packed.shape
+    k = 2 * half
+    groups = (n, _ngroups(k, group_size))
+    if (packed.dtype is not torch.uint8 or scales.shape != groups or zeros.shape != groups
+            or scales.dtype not in SZ_DTYPES or zeros.dtype is not scales.dtype):
+        _check_weights(packed, scales, zeros, k, group_size)
     if d != (n if transposed else k):
         raise ValueError(f"{name} has {d} columns, the weight [N, K] is [{n}, {k}]")
     return m, k, n
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *args) -> int:
+    return int(getattr(load(), name)(*args))
+
+
+def _low(given: Optional[torch.Tensor], name: str, m: int, rank: int, like: torch.Tensor) -> torch.Tensor:
+    """The tensor that takes the rows' low-rank values: the caller's, checked, or a new one."""
+    if given is None:
+        return like.new_empty((m, rank), dtype=torch.float32)
+    if given.dtype is not torch.float32 or given.shape != (m, rank):
+        _expect(given, name, (m, rank), (torch.float32,))
+    return given
 
 
 def w4a16_lora_matmul_workspace_size(m: int, k: int, n: int, group_size: int, x_dtype: torch.dtype = torch.bfloat16,
@@ -678,10 +703,13 @@ def w4a16_lora_matmul_workspace_size(m: int, k: int, n: int, group_size: int, x_
                                                        _dtype_code(y_dtype)))
 
 
-def _lora_workspace(size, x, m, k, n, group_size, scales, y) -> Optional[torch.Tensor]:
-    """The workspace that a product asks for, from torch, beside x."""
-    nbytes = size(m, k, n, group_size, _DT[x.dtype], _DT[scales.dtype], _DT[y.dtype])
-    return x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+def _lora_workspace(name: str, x, m, k, n, group_size, scales, y):
+    """The workspace that a product asks for, from torch, beside x: (tensor that keeps it, pointer, bytes)."""
+    nbytes = _workspace_bytes(name, m, k, n, group_size, _DT[x.dtype], _DT[scales.dtype], _DT[y.dtype])
+    if not nbytes:
+        return None, None, 0
+    ws = x.new_empty((nbytes,), dtype=torch.uint8)
+    return ws, ws.data_ptr(), nbytes
 
 
 def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
@@ -698,18 +726,15 @@ def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
     were).  out_dtype defaults to x's dtype.  The workspace comes from torch."""
     m, k, n = _int4_product(x, "x", packed, scales, zeros, group_size, False)
     count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
-    given = tuple(t for t in (out, u) if t is not None)
+    given = () if out is None and u is None else tuple(t for t in (out, u) if t is not None)
     dev = _device(x, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
     y = _y_out(out, out_dtype or x.dtype, (m, n), x)
-    if u is None:
-        u = x.new_empty((m, rank), dtype=torch.float32)
-    elif u.shape != (m, rank) or u.dtype is not torch.float32:
-        _expect(u, "u", (m, rank), (torch.float32,))
-    ws = _lora_workspace(load().w4a16_lora_matmul_workspace_size, x, m, k, n, group_size, scales, y)
-    _launch(dev, load().w4a16_lora_matmul, _ptr(x), _dtype_code(x.dtype), m, k, _ptr(packed), _ptr(scales),
-            _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
-            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(u), _ptr(y), _dtype_code(y.dtype),
-            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    u = _low(u, "u", m, rank, x)
+    ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_lora_matmul_workspace_size", x, m, k, n, group_size, scales, y)
+    _launch(dev, load().w4a16_lora_matmul, x.data_ptr(), _DT[x.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr(), _DT[scales.dtype], n, group_size, a.data_ptr(), b.data_ptr(), _DT[a.dtype], count, rank,
+            scaling.data_ptr(), offsets.data_ptr(), adapters.data_ptr(), s, u.data_ptr(), y.data_ptr(), _DT[y.dtype],
+            ws_ptr, ws_bytes)
     return y
 
 
@@ -729,10 +754,9 @@ def w4a16_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
     dev = _device(dy, packed, scales, zeros) if out is None else _device(dy, packed, scales, zeros, out)
     dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
-    ws = _lora_workspace(load().w4a16_matmul_t_workspace_size, dy, m, k, n, group_size, scales, dx)
-    _launch(dev, load().w4a16_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales), _ptr(zeros),
-            _dtype_code(scales.dtype), n, group_size, _ptr(dx), _dtype_code(dx.dtype),
-            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_matmul_t_workspace_size", dy, m, k, n, group_size, scales, dx)
+    _launch(dev, load().w4a16_matmul_t, dy.data_ptr(), _DT[dy.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr(), _DT[scales.dtype], n, group_size, dx.data_ptr(), _DT[dx.dtype], ws_ptr, ws_bytes)
     return dx
 
 
@@ -747,18 +771,15 @@ def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Te
     adapter are left as they were).  out_dtype defaults to dy's dtype."""
     m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
     count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
-    given = tuple(t for t in (out, v) if t is not None)
+    given = () if out is None and v is None else tuple(t for t in (out, v) if t is not None)
     dev = _device(dy, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
     dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
-    if v is None:
-        v = dy.new_empty((m, rank), dtype=torch.float32)
-    elif v.shape != (m, rank) or v.dtype is not torch.float32:
-        _expect(v, "v", (m, rank), (torch.float32,))
-    ws = _lora_workspace(load().w4a16_matmul_t_workspace_size, dy, m, k, n, group_size, scales, dx)
-    _launch(dev, load().w4a16_lora_matmul_t, _ptr(dy), _dtype_code(dy.dtype), m, k, _ptr(packed), _ptr(scales),
-            _ptr(zeros), _dtype_code(scales.dtype), n, group_size, _ptr(a), _ptr(b), _dtype_code(a.dtype), count, rank,
-            _ptr(scaling), _ptr(offsets), _ptr(adapters), s, _ptr(v), _ptr(dx), _dtype_code(dx.dtype),
-            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    v = _low(v, "v", m, rank, dy)
+    ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_matmul_t_workspace_size", dy, m, k, n, group_size, scales, dx)
+    _launch(dev, load().w4a16_lora_matmul_t, dy.data_ptr(), _DT[dy.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr(), _DT[scales.dtype], n, group_size, a.data_ptr(), b.data_ptr(), _DT[a.dtype], count, rank,
+            scaling.data_ptr(), offsets.data_ptr(), adapters.data_ptr(), s, v.data_ptr(), dx.data_ptr(), _DT[dx.dtype],
+            ws_ptr, ws_bytes)
     return dx
 
 
@@ -794,7 +815,7 @@ def lora_grads(xq: torch.Tensor, xs: torch.Tensor, dy: torch.Tensor, u: torch.Te
     else:
         dev = _device(xq, xs, dy, u, v, offsets, adapters)
         da, db = u.new_empty(shapes[0]), u.new_empty(shapes[1])
-    nbytes = load().lora_grads_workspace_size(m, k, n, _DT[dy.dtype], num_adapters, rank)
+    nbytes = _workspace_bytes("lora_grads_workspace_size", m, k, n, _DT[dy.dtype], num_adapters, rank)
     ws = u.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     _launch(dev, load().lora_grads, _ptr(xq), _ptr(xs), m, k, _ptr(dy), _dtype_code(dy.dtype), n, _ptr(u), _ptr(v),
             _ptr(offsets), _ptr(adapters), s, num_adapters, rank, _ptr(da), _ptr(db),
