@@ -60,10 +60,11 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
   const bool few = back ? m <= 32 : m <= 64 || m * n * k <= ((int64_t)1 << 31);
   p.tiles = x_dtype == W4_BF16 && !few && d % 8 == 0 && d <= ((int64_t)1 << 21) &&
             (back || sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
+  p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
+  p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
+  p.strips = (c + 127) / 128;
+  if (p.rows * p.strips > (1 << 22)) p.tiles = false;  // a launch has fewer than 2^32 threads
   if (p.tiles) {
-    p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
-    p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
-    p.strips = (c + 127) / 128;
     const int64_t all = (d + 63) / 64, parts = 256 / (p.rows * p.strips);
     split(p, all, parts < all / 8 ? parts : all / 8);
     p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)c * 4;

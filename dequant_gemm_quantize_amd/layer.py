@@ -348,7 +348,9 @@ class LoRALinear(torch.nn.Module):
         self.register_buffer("scales", base.scales)
         self.register_buffer("zeros", base.zeros)
         self.register_buffer("scaling", torch.full((adapters,), self.alpha / rank, dtype=torch.float32, device=dev))
-        self.register_buffer("_all", torch.zeros((1,), dtype=torch.int32, device=dev), persistent=False)
+        # one segment of all rows: (0, 1) times their number, and adapter 0
+        self.register_buffer("_ends", torch.tensor([0, 1], dtype=torch.int32, device=dev), persistent=False)
+        self.register_buffer("_first", torch.zeros((1,), dtype=torch.int32, device=dev), persistent=False)
         self.a = torch.nn.Parameter(torch.randn((adapters, rank, self.in_features), device=dev).mul_(
             self.in_features ** -0.5).to(dtype))
         self.b = torch.nn.Parameter(torch.zeros((adapters, self.out_features, rank), dtype=dtype, device=dev))
@@ -361,8 +363,7 @@ class LoRALinear(torch.nn.Module):
             raise ValueError("offsets and which come together")
         x2 = _activations(x.reshape(-1, self.in_features).contiguous())
         if offsets is None:
-            which = self._all
-            offsets = torch.nn.functional.pad(which.new_full((1,), x2.shape[0]), (1, 0))
+            offsets, which = self._ends * x2.shape[0], self._first
         y = lora_linear(x2, self.packed, self.scales, self.zeros, self.group_size, self.a, self.b, self.scaling,
                         offsets, which)
         return y.to(_result_dtype(x, None)).reshape(*x.shape[:-1], self.out_features)

@@ -168,6 +168,82 @@ def test_a_training_run_of_the_operators():
     assert C.rel(da, da64) <= C.sum_tol(c["m"])
 
 
+# rows, out, in, group, x, adapters and scales: what the tiles take (forward above 64 rows and 2^31 products, back
+# above 32 rows), by the edges of a tile (256 or 128 rows, 128 columns), of a step (64) and of the parts of a split sum
+TILES = [
+    (300, 2056, 4096, 128, ("bf16", "bf16", "f16")),   # split forward and back, ragged columns
+    (300, 2051, 4096, 128, ("bf16", "bf16", "f16")),   # odd columns forward; back on the kernel for few rows
+    (257, 11016, 1056, 96, ("bf16", "f32", "f32")),    # one part forward, groups across steps and tiles, K ends inside a step
+    (129, 8200, 2080, 32, ("bf16", "bf16", "f16")),    # groups of 32, K ends inside a step
+    (66, 10248, 3264, 64, ("bf16", "f32", "f16")),     # tiles of 128 rows, most of them empty
+    (1025, 1032, 2112, 2112, ("bf16", "bf16", "f32")),  # groups as long as a row
+    (700, 4104, 1024, 256, ("bf16", "bf16", "f16")),
+    (40, 8, 32, 32, ("bf16", "bf16", "f16")),          # back: one step of eight rows
+    (33, 72, 160, 32, ("bf16", "bf16", "f32")),
+    (200, 4096, 32, 32, ("bf16", "f32", "f16")),       # back: a tile wider than the result
+]
+
+
+@pytest.mark.parametrize("m,n,k,g,types", TILES, ids=[f"{t[0]}x{t[1]}x{t[2]}g{t[3]}" for t in TILES])
+def test_whole_numbers_in_tiles(m, n, k, g, types):
+    bounds, which = [0, 5, 5, m // 3, m // 3 + 40 if m > 60 else m // 3 + 1, m - 3], [1, 0, -1, 2, 0]
+    c = C.case(m, n, k, g, 24, bounds, which, 3, *types)
+    y64, u64 = C.forward64(c)
+    dx64, v64 = C.back64(c)
+    assert float(y64.abs().max()) < 2 ** 23 and float(dx64.abs().max()) < 2 ** 23  # halves: 2^24 units
+    for dt in (torch.float32, torch.bfloat16):
+        y, dx = Canary((m, n), dt), Canary((m, k), dt)
+        w4.w4a16_lora_matmul(c["x"], *c["weight"], *c["adapter"], out=y.tensor)
+        w4.w4a16_lora_matmul_t(c["dy"], *c["weight"], *c["adapter"], out=dx.tensor)
+        y.check(), dx.check()
+        assert torch.equal(y.tensor, y64.to(dt))
+        assert torch.equal(dx.tensor, dx64.to(dt))
+        assert torch.equal(w4.w4a16_matmul_t(c["dy"], *c["weight"], out_dtype=dt), (c["dy"].double() @ c["dense"]).to(dt))
+
+
+@pytest.mark.parametrize("m,n,k,g,types", TILES[:6], ids=[f"{t[0]}x{t[1]}x{t[2]}g{t[3]}" for t in TILES[:6]])
+def test_random_in_tiles(m, n, k, g, types):
+    c = C.case(m, n, k, g, 40, [0, m // 2, m], [1, 0], 2, *types, whole=False, seed=9)
+    y64, _ = C.forward64(c)
+    dx64, _ = C.back64(c)
+    for dt, steps in ((torch.float32, 0.0), (torch.bfloat16, rounded(types))):
+        y = w4.w4a16_lora_matmul(c["x"], *c["weight"], *c["adapter"], out_dtype=dt)
+        dx = w4.w4a16_lora_matmul_t(c["dy"], *c["weight"], *c["adapter"], out_dtype=dt)
+        assert C.rel(y, y64) <= steps + 4 * C.sum_tol(k)
+        assert C.rel(dx, dx64) <= steps + C.sum_tol(n)
+
+
+def test_rows_that_are_not_numbers_stay_alone():
+    """A row with NaN and infinities beside others, in every kernel: the others' results do not change."""
+    for m, n, k in ((300, 2056, 4096), (24, 264, 256), (3, 64, 96)):
+        c = C.case(m, n, k, 32, 16, [0, m // 2, m], [0, 1], 2)
+        bad = m // 3
+        keep = torch.arange(m, device="cuda") != bad
+        x, dy = c["x"].clone(), c["dy"].clone()
+        x[bad, ::3], x[bad, 1::3] = float("nan"), float("inf")
+        dy[bad, ::3], dy[bad, 1::3] = float("nan"), float("-inf")
+        y = w4.w4a16_lora_matmul(x, *c["weight"], *c["adapter"])
+        dx = w4.w4a16_lora_matmul_t(dy, *c["weight"], *c["adapter"])
+        assert torch.equal(y[keep], C.forward64(c)[0].bfloat16()[keep])
+        assert torch.equal(dx[keep], C.back64(c)[0].bfloat16()[keep])
+        assert y[bad].isnan().any() and dx[bad].isnan().any()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 9])
+def test_segments_of_few_rows(rows):
+    """Every number of rows that the vector kernel of the way into the rank has, more than 64 segments, twice the same adapter."""
+    s = 70
+    c = C.case(rows * s, 48, 1056, 96, 16, [rows * i for i in range(s + 1)], [i % 5 - 1 for i in range(s)], 4)
+    u = torch.zeros((rows * s, 16), device="cuda")
+    y64, u64 = C.forward64(c)
+    y = w4.w4a16_lora_matmul(c["x"], *c["weight"], *c["adapter"], out_dtype=torch.float32, u=u)
+    assert torch.equal(u, u64.float()) and torch.equal(y, y64.float())
+    v = torch.zeros_like(u)
+    dx64, v64 = C.back64(c)
+    dx = w4.w4a16_lora_matmul_t(c["dy"], *c["weight"], *c["adapter"], out_dtype=torch.float32, v=v)
+    assert torch.equal(v, v64.float()) and torch.equal(dx, dx64.float())
+
+
 @pytest.mark.parametrize("m", [0, 4])
 def test_empty_calls(m):
     c = C.case(m, 32, 64, 32, 8, [0, m], [0], 1)
