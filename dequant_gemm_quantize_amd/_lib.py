@@ -686,13 +686,13 @@ def _workspace_bytes(name: str, *args) -> int:
     return int(getattr(load(), name)(*args))
 
 
-def _low(given: Optional[torch.Tensor], name: str, m: int, rank: int, like: torch.Tensor) -> torch.Tensor:
-    """The tensor that takes the rows' low-rank values: the caller's, checked, or a new one."""
-    if given is None:
-        return like.new_empty((m, rank), dtype=torch.float32)
-    if given.dtype is not torch.float32 or given.shape != (m, rank):
-        _expect(given, name, (m, rank), (torch.float32,))
-    return given
+def _given(out, shape, low, name: str, m: int, rank: int) -> tuple:
+    """The caller's tensors for the result and for the rows' low-rank values, checked."""
+    if out is not None:
+        _expect(out, "out", shape, Y_DTYPES)
+    if low is not None and (low.dtype is not torch.float32 or low.shape != (m, rank)):
+        _expect(low, name, (m, rank), (torch.float32,))
+    return tuple(t for t in (out, low) if t is not None)
 
 
 def w4a16_lora_matmul_workspace_size(m: int, k: int, n: int, group_size: int, x_dtype: torch.dtype = torch.bfloat16,
@@ -726,10 +726,11 @@ def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
     were).  out_dtype defaults to x's dtype.  The workspace comes from torch."""
     m, k, n = _int4_product(x, "x", packed, scales, zeros, group_size, False)
     count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
-    given = () if out is None and u is None else tuple(t for t in (out, u) if t is not None)
+    given = () if out is None and u is None else _given(out, (m, n), u, "u", m, rank)
     dev = _device(x, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
     y = _y_out(out, out_dtype or x.dtype, (m, n), x)
-    u = _low(u, "u", m, rank, x)
+    if u is None:
+        u = x.new_empty((m, rank), dtype=torch.float32)
     ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_lora_matmul_workspace_size", x, m, k, n, group_size, scales, y)
     _launch(dev, load().w4a16_lora_matmul, x.data_ptr(), _DT[x.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
             zeros.data_ptr(), _DT[scales.dtype], n, group_size, a.data_ptr(), b.data_ptr(), _DT[a.dtype], count, rank,
@@ -771,10 +772,11 @@ def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Te
     adapter are left as they were).  out_dtype defaults to dy's dtype."""
     m, k, n = _int4_product(dy, "dy", packed, scales, zeros, group_size, True)
     count, rank, s = _check_lora(a, b, scaling, offsets, adapters, k, n)
-    given = () if out is None and v is None else tuple(t for t in (out, v) if t is not None)
+    given = () if out is None and v is None else _given(out, (m, k), v, "v", m, rank)
     dev = _device(dy, packed, scales, zeros, a, b, scaling, offsets, adapters, *given)
     dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
-    v = _low(v, "v", m, rank, dy)
+    if v is None:
+        v = dy.new_empty((m, rank), dtype=torch.float32)
     ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_matmul_t_workspace_size", dy, m, k, n, group_size, scales, dx)
     _launch(dev, load().w4a16_lora_matmul_t, dy.data_ptr(), _DT[dy.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
             zeros.data_ptr(), _DT[scales.dtype], n, group_size, a.data_ptr(), b.data_ptr(), _DT[a.dtype], count, rank,
