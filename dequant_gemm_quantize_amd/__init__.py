@@ -10,7 +10,8 @@ from ._lib import (  # noqa: F401
     w4a16_matmul, w4a16_matmul_workspace_size, w4a8_matmul, w4a8_matmul_workspace_size, version,
     quantize_mxfp4, dequant_mxfp4, mxfp4_matmul, mxfp4_grouped_matmul, w4a16_grouped_matmul,
     quantize_checkpoint_int8, dequant_checkpoint_int8, w4a16_matmul_t, w4a16_matmul_t_workspace_size,
-    w4a16_lora_matmul, w4a16_lora_matmul_workspace_size, w4a16_lora_matmul_t, lora_grads, lora_grads_workspace_size,
+    w4a16_lora_matmul, w4a16_lora_matmul_workspace_size, w4a16_lora_matmul_t,
+    w4a16_lora_matmul_t_workspace_size, lora_grads, lora_grads_workspace_size,
     LIB_PATH,
     W4_F32, W4_F16, W4_BF16, W4_OK, W4_EINVAL, W4_EUNSUPPORTED, W4_EHIP,
 )

@@ -56,6 +56,7 @@ SIGNATURES = [
                                _VP, _I64, _VP, _VP, _I, _VP, ctypes.c_size_t, _VP]),
     ("w4a16_matmul_t_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I32, _I, _I, _I]),
     ("w4a16_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _I, _VP, ctypes.c_size_t, _VP]),
+    ("w4a16_lora_matmul_t_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I32, _I, _I, _I, _I32, _I64]),
     ("w4a16_lora_matmul_t", _I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _I64, _I32, _VP, _VP, _I, _I64, _I32, _VP,
                                  _VP, _VP, _I64, _VP, _VP, _I, _VP, ctypes.c_size_t, _VP]),
     ("lora_grads_workspace_size", ctypes.c_size_t, [_I64, _I64, _I64, _I, _I64, _I32]),
@@ -703,9 +704,9 @@ def w4a16_lora_matmul_workspace_size(m: int, k: int, n: int, group_size: int, x_
                                                        _dtype_code(y_dtype)))
 
 
-def _lora_workspace(name: str, x, m, k, n, group_size, scales, y):
+def _lora_workspace(name: str, x, m, k, n, group_size, scales, y, *more):
     """The workspace that a product asks for, from torch, beside x: (tensor that keeps it, pointer, bytes)."""
-    nbytes = _workspace_bytes(name, m, k, n, group_size, _DT[x.dtype], _DT[scales.dtype], _DT[y.dtype])
+    nbytes = _workspace_bytes(name, m, k, n, group_size, _DT[x.dtype], _DT[scales.dtype], _DT[y.dtype], *more)
     if not nbytes:
         return None, None, 0
     ws = x.new_empty((nbytes,), dtype=torch.uint8)
@@ -742,7 +743,7 @@ def w4a16_lora_matmul(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
 def w4a16_matmul_t_workspace_size(m: int, k: int, n: int, group_size: int, dy_dtype: torch.dtype = torch.bfloat16,
                                   sz_dtype: torch.dtype = torch.float16,
                                   dx_dtype: torch.dtype = torch.bfloat16) -> int:
-    """Bytes of workspace that w4a16_matmul_t and w4a16_lora_matmul_t need for this shape."""
+    """Bytes of workspace that w4a16_matmul_t needs for this shape (0: none)."""
     return int(load().w4a16_matmul_t_workspace_size(m, k, n, group_size, _dtype_code(dy_dtype), _dtype_code(sz_dtype),
                                                     _dtype_code(dx_dtype)))
 
@@ -761,6 +762,14 @@ def w4a16_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     return dx
 
 
+def w4a16_lora_matmul_t_workspace_size(m: int, k: int, n: int, group_size: int, rank: int, segments: int,
+                                       dy_dtype: torch.dtype = torch.bfloat16, sz_dtype: torch.dtype = torch.float16,
+                                       dx_dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that w4a16_lora_matmul_t needs for this shape (0: none)."""
+    return int(load().w4a16_lora_matmul_t_workspace_size(m, k, n, group_size, _dtype_code(dy_dtype),
+                                                         _dtype_code(sz_dtype), _dtype_code(dx_dtype), rank, segments))
+
+
 def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
                         group_size: int, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor,
                         offsets: torch.Tensor, adapters: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
@@ -777,7 +786,8 @@ def w4a16_lora_matmul_t(dy: torch.Tensor, packed: torch.Tensor, scales: torch.Te
     dx = _y_out(out, out_dtype or dy.dtype, (m, k), dy)
     if v is None:
         v = dy.new_empty((m, rank), dtype=torch.float32)
-    ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_matmul_t_workspace_size", dy, m, k, n, group_size, scales, dx)
+    ws, ws_ptr, ws_bytes = _lora_workspace("w4a16_lora_matmul_t_workspace_size", dy, m, k, n, group_size, scales, dx,
+                                           rank, s)
     _launch(dev, load().w4a16_lora_matmul_t, dy.data_ptr(), _DT[dy.dtype], m, k, packed.data_ptr(), scales.data_ptr(),
             zeros.data_ptr(), _DT[scales.dtype], n, group_size, a.data_ptr(), b.data_ptr(), _DT[a.dtype], count, rank,
             scaling.data_ptr(), offsets.data_ptr(), adapters.data_ptr(), s, v.data_ptr(), dx.data_ptr(), _DT[dx.dtype],

@@ -661,6 +661,14 @@ static size_t lora_workspace(bool back, int64_t m, int64_t k, int64_t n, int32_t
   return w4::w4a16_lora_workspace_bytes(back, m, k, n, group_size, x_dtype, sz_dtype, y_dtype);
 }
 
+// Parts of v of the transposed product with adapters, and their bytes behind the product's own workspace.
+static size_t low_parts(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype, int sz_dtype, int dx_dtype,
+                        int32_t rank, int64_t segments) {
+  if (!w4::w4a16_lora_sums(true, m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype)) return 1;
+  return w4::lora_into_parts(m, n, segments, rank);
+}
+static size_t low_bytes(size_t parts, int64_t m, int32_t rank) { return parts > 1 ? parts * (size_t)m * (size_t)rank * 4 : 0; }
+
 static int lora_product(const char* fn, int x_dtype, const w4::TilesArgs& p, const w4::LoraInto& in,
                         const w4::LoraOut& out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const char* low_name = p.back ? "v" : "u";
@@ -681,14 +689,19 @@ static int lora_product(const char* fn, int x_dtype, const w4::TilesArgs& p, con
   W4_TRY(check_ptr(fn, "scales", p.scales));
   W4_TRY(check_ptr(fn, "zeros", p.zeros));
   W4_TRY(check_ptr(fn, p.back ? "dx" : "y", p.y));
-  const size_t need = w4::w4a16_lora_workspace_bytes(p.back, p.m, p.k, p.n, p.g, x_dtype, p.sz_dtype, p.y_dtype);
+  const size_t own = w4::w4a16_lora_workspace_bytes(p.back, p.m, p.k, p.n, p.g, x_dtype, p.sz_dtype, p.y_dtype);
+  const bool any = in.rank != 0 && in.count != 0 && in.segments != 0;
+  const size_t parts = any && p.back
+                           ? low_parts(p.m, p.k, p.n, p.g, x_dtype, p.sz_dtype, p.y_dtype, in.rank, in.segments)
+                           : 1;
+  const size_t need = own + low_bytes(parts, p.m, in.rank);
   if (need > 0) {
     W4_TRY(check_ptr(fn, "workspace", workspace));
     if (workspace_bytes < need)
       return fail(W4_EINVAL, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
   }
   w4::LoraOut lo = out;
-  if (in.rank == 0 || in.count == 0 || in.segments == 0) {
+  if (!any) {
     lo.count = lo.segments = 0;
   } else {
     W4_TRY(check_ptr(fn, "a", in.down ? in.weights : out.out));
@@ -697,7 +710,14 @@ static int lora_product(const char* fn, int x_dtype, const w4::TilesArgs& p, con
     W4_TRY(check_ptr4(fn, "offsets", in.offsets));
     W4_TRY(check_ptr4(fn, "which", in.which));
     W4_TRY(check_ptr(fn, low_name, in.low));
-    const hipError_t e = w4::launch_lora_into(in, stream);
+    w4::LoraInto into = in;
+    if (parts > 1) {
+      into.low = (float*)((uint8_t*)workspace + own);  // `own` is a multiple of 128: m * k floats, k % 32 == 0
+      into.parts = lo.parts = (int)parts;
+      lo.low = into.low;
+      lo.whole = in.low;
+    }
+    const hipError_t e = w4::launch_lora_into(into, stream);
     if (e != hipSuccess) return hip_status(e, fn);
   }
   return hip_status(w4::launch_w4a16_lora(p.x, x_dtype, p, lo, workspace, stream), fn);
@@ -716,8 +736,8 @@ int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const ui
   static const char* fn = "w4a16_lora_matmul";
   if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
   const w4::TilesArgs p{false, x, m, k, n, packed, scales, zeros, sz_dtype, group_size, y, y_dtype, 0, 0, 0, 0};
-  const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u};
-  const w4::LoraOut out{u, b, ab_dtype, adapters, rank, offsets, which, segments};
+  const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u, 1};
+  const w4::LoraOut out{u, b, ab_dtype, adapters, rank, offsets, which, segments, 1, nullptr};
   return lora_product(fn, x_dtype, p, in, out, workspace, workspace_bytes, stream);
 }
 
@@ -733,6 +753,15 @@ int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uin
   return lora_product("w4a16_matmul_t", dy_dtype, p, w4::LoraInto{}, w4::LoraOut{}, workspace, workspace_bytes, stream);
 }
 
+size_t w4a16_lora_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype,
+                                          int sz_dtype, int dx_dtype, int32_t rank, int64_t segments) {
+  const size_t own = lora_workspace(true, m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
+  const bool valid = check_adapters("w4a16_lora_matmul_t_workspace_size", m, k, n, 1, rank, segments) == W4_OK;
+  ok();
+  if (own == 0 || !valid || segments == 0) return own;
+  return own + low_bytes(low_parts(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype, rank, segments), m, rank);
+}
+
 int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                         const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
                         int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
@@ -740,8 +769,8 @@ int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, cons
                         size_t workspace_bytes, hipStream_t stream) {
   static const char* fn = "w4a16_lora_matmul_t";
   if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
-  const w4::LoraInto in{false, dy, dy_dtype, m, n, b, ab_dtype, adapters, rank, scaling, offsets, which, segments, v};
-  const w4::LoraOut out{v, a, ab_dtype, adapters, rank, offsets, which, segments};
+  const w4::LoraInto in{false, dy, dy_dtype, m, n, b, ab_dtype, adapters, rank, scaling, offsets, which, segments, v, 1};
+  const w4::LoraOut out{v, a, ab_dtype, adapters, rank, offsets, which, segments, 1, nullptr};
   const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0};
   return lora_product(fn, dy_dtype, p, in, out, workspace, workspace_bytes, stream);
 }

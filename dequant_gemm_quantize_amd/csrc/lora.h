@@ -21,6 +21,8 @@ struct Adapters {
   const int* offsets;
   const int* which;
   int segments, count, rank, wide;  // wide: `out` is float32, otherwise bf16
+  int parts;     // > 1: low is [parts, M, R], to be added (k_w4a16_sum alone does)
+  float* whole;  // the sums, of the rows that have an adapter
 };
 struct NoAdapters {
   static constexpr bool any = false;

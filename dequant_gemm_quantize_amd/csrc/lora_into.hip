@@ -189,7 +189,7 @@ template <typename TX, typename TW, bool WIDE>
 __global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
     const TX* __restrict__ x, int64_t M, int64_t D, const TW* __restrict__ weights, int count, int R,
     const float* __restrict__ scaling, const int* __restrict__ offsets, const int* __restrict__ which, int segments,
-    float* __restrict__ low, uint32_t rblocks, int64_t tiles) {
+    float* __restrict__ low, uint32_t rblocks, int64_t tiles, int64_t part_d) {
   typedef UpPlace<TX, TW> P;
   constexpr int CH = P::CH, Q = CH / 32;
   constexpr int XC = CH * (int)sizeof(TX) / 16;          // 16-byte pieces of a row of dy
@@ -236,11 +236,13 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
     };
     f32x4 acc[2];
     acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // this part's values of D, and of those this wave's
     constexpr int64_t stride = CH * kUpWaves;
+    const int64_t begin = part_d * blockIdx.y + (int64_t)CH * w, end = D - part_d * blockIdx.y < part_d ? D : part_d * (blockIdx.y + 1);
     int stage = 0;
-    if ((int64_t)CH * w < D) issue((int64_t)CH * w, 0);
-    for (int64_t d0 = (int64_t)CH * w; d0 < D; d0 += stride, stage ^= 1) {
-      issue(d0 + stride, stage ^ 1);  // past D nothing, as many loads
+    if (begin < end) issue(begin, 0);
+    for (int64_t d0 = begin; d0 < end; d0 += stride, stage ^= 1) {
+      issue(d0 + stride < end ? d0 + stride : D, stage ^ 1);  // past D nothing, as many loads
       bf16x8 a[Q][PX];
       if constexpr (!WIDE) {
 #pragma unroll
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_lora_up(
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[(w * 16 + 4 * h + e) * 16 + l16] = acc[0][e] + acc[1][e];
     __syncthreads();
-    into_store<16, 16>(part, kUpWaves, t, rank0, R, c, low);
+    into_store<16, 16>(part, kUpWaves, t, rank0, R, c, low + (int64_t)blockIdx.y * M * R);
     __syncthreads();  // the next tile writes there again
   }
 }
@@ -311,9 +313,11 @@ static hipError_t up_go(const LoraInto& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   const int64_t rblocks = (a.rank + 15) / 16;
   const int64_t tiles = grouped_max_tiles(a.m, a.segments, 16) * rblocks;
-  k_lora_up<TX, TW, WIDE><<<dim3((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid)), 64 * kUpWaves, lds, st>>>(
+  const int64_t parts = a.parts > 1 ? a.parts : 1, chunks = (a.d + 127) / 128;
+  const dim3 grid((unsigned)(tiles < kIntoGrid ? tiles : kIntoGrid), (unsigned)parts);
+  k_lora_up<TX, TW, WIDE><<<grid, 64 * kUpWaves, lds, st>>>(
       (const TX*)a.x, a.m, a.d, (const TW*)a.weights, (int)a.count, a.rank, a.scaling, a.offsets, a.which,
-      (int)a.segments, a.low, (uint32_t)rblocks, tiles);
+      (int)a.segments, a.low, (uint32_t)rblocks, tiles, 128 * ((chunks + parts - 1) / parts));
   return hipGetLastError();
 }
 
@@ -335,6 +339,16 @@ static hipError_t into_types(const LoraInto& a, hipStream_t st) {
   // 16 rows of dy by byte offsets below 2^31
   if (a.d * (int64_t)sizeof(TX) % 16 == 0 && a.d * (int64_t)sizeof(TX) < ((int64_t)1 << 27)) return up_go<TX, TW, true>(a, st);
   return up_go<TX, TW, false>(a, st);
+}
+
+// Few tiles leave most CUs idle, and a CU's intake is what bounds them (12 rows of three segments against [11008, 16]:
+// 12 us in one part, 5 in ten): parts of 1024 values, one step a wave, on at most 128 CUs.
+size_t lora_into_parts(int64_t m, int64_t d, int64_t segments, int rank) {
+  const int64_t tiles = grouped_max_tiles(m, segments, 16) * ((rank + 15) / 16);
+  int64_t parts = tiles > 0 ? 128 / tiles : 1;
+  if (parts > d / 1024) parts = d / 1024;
+  if (parts > 16) parts = 16;
+  return (size_t)(parts < 1 ? 1 : parts);
 }
 
 hipError_t launch_lora_into(const LoraInto& a, hipStream_t st) {

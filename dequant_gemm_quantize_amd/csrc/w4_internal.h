@@ -151,8 +151,11 @@ struct LoraInto {
   const int* which;
   int64_t segments;
   float* low;
+  int parts;  // > 1, not down: low takes as many partial sums, [parts, M, R]
 };
 hipError_t launch_lora_into(const LoraInto& a, hipStream_t st);
+// The parts of a sum over d that a call without `down` should have where the reader of low can add them.
+size_t lora_into_parts(int64_t m, int64_t d, int64_t segments, int rank);
 // The low-rank part that a product adds: low [M, R] times `out`, [L, N, R] beside
 // x W^T (whose columns are N) and [L, R, K] beside dy W.  count 0: none.
 struct LoraOut {
@@ -164,6 +167,8 @@ struct LoraOut {
   const int* offsets;
   const int* which;
   int64_t segments;
+  int parts;     // > 1: low is as many partial sums, which the product's last kernel adds
+  float* whole;  // and where it leaves the sums of the rows that have an adapter
 };
 // A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles of 64 mi
 // rows, for bf16 x: pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
@@ -188,6 +193,8 @@ hipError_t launch_w4a16_lora_rows(const void* x, int x_dtype, int64_t m, int64_t
 // Either direction, whatever the sizes (args without x, mi, pw, parts and steps), and the workspace's bytes (0: none).
 size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
                                   int y_dtype);
+// Whether the call ends in the kernel that adds partial sums, which takes the low-rank values in parts too (back).
+bool w4a16_lora_sums(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype);
 hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, const LoraOut& lo, void* ws,
                              hipStream_t st);
 // Gradients of the adapters from the 8-bit checkpoint of x, dy and the low-rank values.

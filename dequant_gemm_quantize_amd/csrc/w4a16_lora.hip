@@ -294,6 +294,7 @@ template <bool BACK, int V, typename TY>
 __global__ __launch_bounds__(64) void k_w4a16_sum(const float* __restrict__ part, int parts, int64_t M, int64_t C,
                                                   Adapters ad, TY* __restrict__ y) {
   typedef float fV __attribute__((ext_vector_type(V)));
+  __shared__ __attribute__((aligned(16))) float lows[kLoraMaxRank];  // the row's low-rank values (back)
   const int lane = threadIdx.x;
   const int64_t strips = (C + 64 * V - 1) / (64 * V), tiles = M * strips;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -304,17 +305,48 @@ __global__ __launch_bounds__(64) void k_w4a16_sum(const float* __restrict__ part
     fV first[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s) first[s] = *(const fV*)(p + (int64_t)(s < parts ? s : 0) * M * C);
+    float u[kLoraMaxRank / kWave] = {};
+    if (BACK && ad.count > 0) {  // the same in every lane
+#pragma unroll
+      for (int i = 0; i < kLoraMaxRank / kWave; ++i) {
+        const int r = lane + kWave * i;
+        if (kWave * i >= ad.rank) break;
+        const float* low = ad.low + m * ad.rank + (r < ad.rank ? r : 0);
+        // at most 16 parts, all of them under way at once
+        float w[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s) w[s] = low[(int64_t)(s < ad.parts ? s : 0) * M * ad.rank];
+        u[i] = w[0];
+#pragma unroll
+        for (int s = 1; s < 16; ++s) u[i] += s < ad.parts ? w[s] : 0.0f;
+      }
+    }
     asm volatile("" ::: "memory");
     const int l = ad.count > 0 ? row_adapter(ad, m, lane) : -1;
     fV v = first[0];
 #pragma unroll
     for (int s = 1; s < 8; ++s)
       if (s < parts) v += first[s];
-#pragma unroll 8
-    for (int s = 8; s < parts; ++s) v += *(const fV*)(p + (int64_t)s * M * C);
+    for (int s0 = 8; s0 < parts; s0 += 8) {  // eight at a time
+#pragma unroll
+      for (int s = 0; s < 8; ++s) first[s] = *(const fV*)(p + (int64_t)(s0 + s < parts ? s0 + s : 0) * M * C);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < parts) v += first[s];
+    }
+    if (BACK && l >= 0) {
+#pragma unroll
+      for (int i = 0; i < kLoraMaxRank / kWave; ++i) {
+        const int r = lane + kWave * i;
+        if (r >= ad.rank) break;
+        lows[r] = u[i];
+        if (ad.parts > 1 && tile % strips == 0) ad.whole[m * ad.rank + r] = u[i];
+      }
+      __builtin_amdgcn_wave_barrier();  // LDS operations of a wave complete in order
+    }
     if (in && l >= 0) {
-      const float* low = ad.low + m * ad.rank;
       if constexpr (!BACK) {
+        const float* low = ad.low + m * ad.rank;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += rank_dot(low, ad.out, ((int64_t)l * C + c + i) * ad.rank, ad.rank, ad.wide);
       } else {
@@ -326,21 +358,22 @@ __global__ __launch_bounds__(64) void k_w4a16_sum(const float* __restrict__ part
           for (int r = 0; r < ad.rank; ++r) {
             const f32x4 e = *(const f32x4*)(a + r * C);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = fmaf(low[r], e[i], d[i]);
+            for (int i = 0; i < 4; ++i) d[i] = fmaf(lows[r], e[i], d[i]);
           }
         } else {
           const uint16_t* a = (const uint16_t*)ad.out + (int64_t)l * ad.rank * C + c;
 #pragma unroll 8
           for (int r = 0; r < ad.rank; ++r) {
             const u32x2 e = *(const u32x2*)(a + r * C);
-            d[0] = fmaf(low[r], bf16_lo(e.x), d[0]);
-            d[1] = fmaf(low[r], bf16_hi(e.x), d[1]);
-            d[2] = fmaf(low[r], bf16_lo(e.y), d[2]);
-            d[3] = fmaf(low[r], bf16_hi(e.y), d[3]);
+            d[0] = fmaf(lows[r], bf16_lo(e.x), d[0]);
+            d[1] = fmaf(lows[r], bf16_hi(e.x), d[1]);
+            d[2] = fmaf(lows[r], bf16_lo(e.y), d[2]);
+            d[3] = fmaf(lows[r], bf16_hi(e.y), d[3]);
           }
         }
         v += d;
       }
+      __builtin_amdgcn_wave_barrier();  // the next row's values take the place
     }
     if (in) {
       TY* out = y + m * C + c;
@@ -366,6 +399,10 @@ static hipError_t sum_go(const float* part, int parts, int64_t m, int64_t c, con
   if (y_dtype == W4_F32) k_w4a16_sum<BACK, V><<<grid, 64, 0, st>>>(part, parts, m, c, ad, (float*)y);
   else k_w4a16_sum<BACK, V><<<grid, 64, 0, st>>>(part, parts, m, c, ad, (uint16_t*)y);
   return hipGetLastError();
+}
+
+bool w4a16_lora_sums(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype) {
+  return lora_plan(back, m, k, n, g, x_dtype, sz_dtype, y_dtype).bytes > 0;
 }
 
 size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
@@ -422,7 +459,7 @@ hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, 
   }
   if (e != hipSuccess) return e;
   const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
-                    (int)lo.count, lo.rank, lo.dtype == W4_F32};
+                    (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
   if (a.back) return sum_go<true, 4>(part, (int)p.parts, a.m, a.k, ad, args.y, args.y_dtype, st);
   if (a.n % 4 == 0) return sum_go<false, 4>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);
   return sum_go<false, 1>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);

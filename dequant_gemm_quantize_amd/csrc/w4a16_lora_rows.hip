@@ -8,7 +8,7 @@
 namespace w4 {
 
 static Adapters adapters_of(const LoraOut& lo) {
-  return Adapters{lo.low, lo.out, lo.offsets, lo.which, (int)lo.segments, (int)lo.count, lo.rank, lo.dtype == W4_F32};
+  return Adapters{lo.low, lo.out, lo.offsets, lo.which, (int)lo.segments, (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
 }
 
 template <typename TX>

@@ -25,7 +25,7 @@ static hipError_t tiles_types(const TilesArgs& a, const Adapters& ad, hipStream_
 
 hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st) {
   const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
-                    (int)lo.count, lo.rank, lo.dtype == W4_F32};
+                    (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
   if (a.back) return a.sz_dtype == W4_F16 ? tiles_types<true, _Float16>(a, ad, st) : tiles_types<true, float>(a, ad, st);
   return a.sz_dtype == W4_F16 ? tiles_types<false, _Float16>(a, ad, st) : tiles_types<false, float>(a, ad, st);
 }

@@ -446,9 +446,8 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *   In all three sums are float32, and the result is rounded once.  With bf16 x (dy) and a
  *   bf16 result the weight may be rounded to bf16 before the product, as in
  *   w4a16_matmul; otherwise no operand loses bits that float32 has.
- *   workspace: device memory, 16-byte aligned, of at least the bytes that
- *   w4a16_lora_matmul_workspace_size and w4a16_matmul_t_workspace_size (for both
- *   transposed products) give (W4_EINVAL below; 0: may be NULL), its contents ignored on
+ *   workspace: device memory, 16-byte aligned, of at least the bytes that the
+ *   call's own size function gives (W4_EINVAL below; 0: may be NULL), its contents ignored on
  *   entry and unspecified on return.  Calls that overlap on one workspace
  *   race.  The size depends only on the arguments, and is 0 for arguments the call rejects.
  *
@@ -473,6 +472,8 @@ size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t gr
 int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                    const void* zeros, int sz_dtype, int64_t n, int32_t group_size, void* dx, int dx_dtype,
                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t w4a16_lora_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int dy_dtype,
+                                          int sz_dtype, int dx_dtype, int32_t rank, int64_t segments);
 int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                         const void* zeros, int sz_dtype, int64_t n, int32_t group_size, const void* a, const void* b,
                         int ab_dtype, int64_t adapters, int32_t rank, const float* scaling, const int32_t* offsets,
