@@ -73,7 +73,8 @@ __device__ __forceinline__ int raw_slot_forward(int n, int c) {
 }
 
 // acc += low out for the wave's 32 MI rows from m0 (those before mend) and 64
-// columns from n, segment by segment: rows of other segments are zero in the operand.
+// columns from c0, segment by segment: rows of other segments are zero in the operand, and
+// keep their sums, since zero times an adapter that is not finite would be NaN.
 // BACK: out is [L, R, C], otherwise [L, C, R].
 template <bool BACK, int MI>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, int lane, f32x16 (&acc)[MI][2], int64_t C, int64_t m0,
@@ -122,19 +123,23 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int lane, f32x1
       for (int i = 0; i < MI; ++i) {
         const int64_t m = m0 + 32 * i + r;
         if (m0 + 32 * i >= hi || m0 + 32 * i + 32 <= lo) continue;  // the same in every lane
+        const bool own = m >= lo && m < hi;  // a lane's sums are all of row m
         bf16x8 a[3] = {zero8(), zero8(), zero8()};
-        if (in && m >= lo && m < hi) load8(ad.low + m * ad.rank + r0 + 8 * h, a);
+        if (in && own) load8(ad.low + m * ad.rank + r0 + 8 * h, a);
 #pragma unroll
-        for (int p = 2; p >= 0; --p)
+        for (int j = 0; j < 2; ++j) {
+          f32x16 sum = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][0], a[p], acc[i][j], 0, 0, 0);
+          for (int p = 2; p >= 0; --p) {
+            sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][0], a[p], sum, 0, 0, 0);
             if (ad.wide) {
 #pragma unroll
-              for (int q = 1; q + p < 3; ++q)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][q], a[p], acc[i][j], 0, 0, 0);
+              for (int q = 1; q + p < 3; ++q) sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j][q], a[p], sum, 0, 0, 0);
             }
           }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] += own ? sum[e] : 0.0f;
+        }
       }
     }
   }

@@ -229,6 +229,27 @@ def test_rows_that_are_not_numbers_stay_alone():
         assert y[bad].isnan().any() and dx[bad].isnan().any()
 
 
+def test_adapters_that_are_not_numbers_stay_alone():
+    """One request's adapter holds NaN and infinities: the rows of the others do not change, in any kernel."""
+    for m, n, k in ((300, 2056, 4096), (90, 2056, 512), (24, 264, 256), (3, 64, 96)):
+        for ab in ("bf16", "f32"):
+            c = C.case(m, n, k, 32, 24, [0, m // 3, 2 * m // 3, m], [0, 1, 2], 3, ab=ab)
+            a, b, *rest = c["adapter"]
+            a, b = a.clone(), b.clone()
+            a[1, ::3], a[1, 1::3], b[1, ::2], b[1, 1::2] = float("nan"), float("inf"), float("nan"), float("-inf")
+            keep = torch.ones(m, dtype=torch.bool, device="cuda")
+            keep[m // 3:2 * m // 3] = False
+            u, v = torch.zeros((m, 24), device="cuda"), torch.zeros((m, 24), device="cuda")
+            y = w4.w4a16_lora_matmul(c["x"], *c["weight"], a, b, *rest, u=u)
+            dx = w4.w4a16_lora_matmul_t(c["dy"], *c["weight"], a, b, *rest, v=v)
+            xq, xs = w4.quantize_checkpoint_int8(c["x"])
+            da, db = w4.lora_grads(xq, xs, c["dy"], u, v, c["offsets"], c["which"], 3)
+            assert torch.equal(y[keep], C.forward64(c)[0].bfloat16()[keep])
+            assert torch.equal(dx[keep], C.back64(c)[0].bfloat16()[keep])
+            assert not y[~keep].isfinite().any() and not dx[~keep].isfinite().any()
+            assert da[0::2].isfinite().all() and db[0::2].isfinite().all()
+
+
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 9])
 def test_segments_of_few_rows(rows):
     """Every number of rows that the vector kernel of the way into the rank has, more than 64 segments, twice the same adapter."""
