@@ -172,7 +172,8 @@ struct LoraOut {
 };
 // A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles of 64 mi
 // rows, for bf16 x: pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
-// ones for a float32 result), and with parts > 1 float32 partial sums, without adapters.
+// ones for a float32 result), and with parts > 1 float32 partial sums, the first of
+// them with the low-rank part.
 struct TilesArgs {
   bool back;
   const void* x;
