@@ -170,10 +170,10 @@ struct LoraOut {
   int parts;     // > 1: low is as many partial sums, which the product's last kernel adds
   float* whole;  // and where it leaves the sums of the rows that have an adapter
 };
-// A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles of 64 mi
-// rows, for bf16 x: pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
-// ones for a float32 result), and with parts > 1 float32 partial sums, the first of
-// them with the low-rank part.
+// A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles, for bf16 x: of 32 mi
+// rows forward; back of 64 mi, with pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
+// ones for a float32 result).  With parts > 1 float32 partial sums of `steps` steps each (256 columns
+// forward, 64 weight rows back), forward the first of them with the low-rank part.
 struct TilesArgs {
   bool back;
   const void* x;
@@ -186,7 +186,8 @@ struct TilesArgs {
   int y_dtype;
   int mi, pw, parts, steps;
 };
-hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st);
+hipError_t launch_w4a16_lora_gemm(const TilesArgs& a, const LoraOut& lo, hipStream_t st);  // forward
+hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st);      // back
 // Forward for few rows, and for float32 x.
 hipError_t launch_w4a16_lora_rows(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed,
                                   const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y,

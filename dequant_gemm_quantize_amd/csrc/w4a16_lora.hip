@@ -1,7 +1,8 @@
 // W4A16 products with low-rank adapters, x W^T forward and dy W back: the choice of
 // a kernel, the kernel for few rows back, and the sum of split products.
 //
-// Forward, few rows and float32 x take the few-row kernel (w4a16_lora_rows.hip).
+// Forward, few rows and float32 x take the few-row kernel (w4a16_lora_rows.hip), many
+// rows of bf16 x the product's by expert (w4a16_lora_gemm.hip).
 // Back, few rows and float32 dy take k_w4a16_back_rows, on v_mfma_f32_16x16x32_bf16.  A wave has
 // 256 columns of 16 MB rows of dx and goes through N 32 weight rows at a time.
 // The sum runs over weight rows, the codes of a word over columns: lane (l16,
@@ -12,11 +13,11 @@
 // in LDS and in the workspace, where k_w4a16_sum adds them in order, and the low-rank part.  12 rows of
 // [11008, 4096]: 16 us and 5, the first loads 6 of them, the rest 2.75 vector instructions a code.
 //
-// Many rows of bf16 x take tiles in both directions (w4a16_tiles.h), split over the sum where
-// the tiles are few.
+// Back, many rows of bf16 dy take tiles (w4a16_tiles.h).  Both products of many rows split the
+// sum where the tiles are few.
 //
-// Rounding: bf16 x with a bf16 result takes, in tiles and back, a weight rounded to bf16, as
-// w4a16_matmul does (half a step, 2^-8 at most, beside the result's own).  Otherwise the weight is the
+// Rounding: forward none of a weight.  Back, bf16 dy with a bf16 result takes a weight rounded to bf16, as
+// w4a16_matmul does (half a step, 2^-8 at most, beside the result's own); otherwise the weight is the
 // exact sum of bf16 parts, two with fp16 scales (15 bits), three with float32 ones (24).
 #include "lds_gemm.h"
 #include "lora.h"
@@ -31,11 +32,11 @@ constexpr int kTStrip = 256;  // columns of a workgroup
 constexpr int64_t kTGrid = 1 << 20;  // workgroups of a part; more tiles than that loop
 constexpr int64_t kTSumGrid = 1 << 22;
 
-// How a call is computed: in tiles (w4a16_tiles.h) or by a kernel for few rows, and
-// how it splits the sum: parts of `steps` steps of 64 or 32.
+// How a call is computed: in tiles (w4a16_lora_gemm.hip, w4a16_tiles.h) or by a kernel for few rows, and
+// how it splits the sum: parts of `steps` steps of 256 columns forward, of 64 weight rows in tiles back, of 32 otherwise.
 struct LoraPlan {
   bool tiles;
-  int mi, pw;          // tiles of 64 mi rows; bf16 parts of a weight
+  int mi, pw;          // tiles of 32 mi rows forward, 64 mi back; bf16 parts of a weight (back)
   int mb;              // blocks of 16 rows a workgroup of k_w4a16_back_rows
   int64_t rows, strips, parts, steps;
   size_t bytes;        // of workspace
@@ -48,36 +49,51 @@ void split(LoraPlan& p, int64_t all, int64_t parts) {
 }
 
 LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype) {
-  const int64_t d = back ? n : k, c = back ? k : n;
   const bool exact = x_dtype != W4_BF16 || y_dtype != W4_BF16;  // weights keep their bits
   LoraPlan p{};
   p.pw = !exact ? 1 : sz_dtype == W4_F16 ? 2 : 3;
   p.parts = 1;
-  // Rows of x start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
-  // below 2^31 bytes; 2^16 blocks of 32 columns; forward, an even number of fp16 scales.
-  // Few rows, forward: us of the few-row kernel / tiles: [4096, 11008] 64 rows 27 / 31, 96 rows 50 / 32;
-  // [11008, 4096] 64 rows 32 / 36, 96 rows 46 / 37; [4096, 4096] 128 rows 22 / 24, 200 rows
-  // 44 / 27; [2050, 2048] 300 rows 28 / 35.
-  const bool few = back ? m <= 32 : m <= 64 || m * n * k <= ((int64_t)1 << 31);
-  p.tiles = x_dtype == W4_BF16 && !few && d % 8 == 0 && d <= ((int64_t)1 << 21) &&
-            (back || sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
+  if (!back) {
+    // us of the few-row kernel / tiles, one request: [4096, 11008] 65 rows 52 / 35, 128 rows 63 / 39; [11008, 4096] 65 rows
+    // 51 / 33; [4096, 4096] 128 rows 33 / 28, 200 rows 57 / 32; [2050, 2048] 300 rows 29 / 30, 500 rows 40 / 30.
+    // (The few-row kernel adds the adapters of requests of one row faster.)  128 rows of x stay below 2^31 bytes.
+    p.tiles = x_dtype == W4_BF16 && m > 64 && m * n * k > ((int64_t)1 << 31) && k <= ((int64_t)1 << 21);
+    if (!p.tiles) return p;
+    p.strips = (n + 127) / 128;
+    // us with 64 / 128 rows a tile, each with its best parts: [4096, 4096] 200 rows 32 / 36, 600 rows 56 / 55; [2050, 2048] 500
+    // rows 30 / 37; [4096, 11008] 333 rows 67 / 68; [11008, 4096] 1024 rows 143 / 137, 2048 rows 247 / 241.  (A launch has fewer than
+    // 2^32 threads.)
+    p.mi = m > 512 || (m + 63) / 64 * p.strips >= (1 << 24) - 8 ? 4 : 2;
+    p.rows = (m + 32 * p.mi - 1) / (32 * p.mi);
+    // Parts of 1024 columns at least, so many that a CU has its two or three workgroups; two parts gain less
+    // than their sum costs.  us in one, two and four parts: 65 rows of [11008, 4096] 39, 35 and 32; [4096, 4096] 333
+    // rows 42, 38 and 39, 1024 rows 61, 64 and 76; [2050, 2048] 500 rows 30, 35 and 33.
+    const int64_t all = (k + 255) / 256, room = (p.mi == 4 ? 512 : 768) / (p.rows * p.strips);
+    const int64_t parts = room < all / 4 ? room : all / 4;
+    split(p, all, parts < 3 ? 1 : parts);
+    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)n * 4;
+    return p;
+  }
+  // Rows of dy start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
+  // below 2^31 bytes.
+  p.tiles = x_dtype == W4_BF16 && m > 32 && n % 8 == 0 && n <= ((int64_t)1 << 21);
   p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
   p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
-  p.strips = (c + 127) / 128;
+  p.strips = (k + 127) / 128;
   if (p.rows * p.strips > (1 << 22)) p.tiles = false;  // a launch has fewer than 2^32 threads
   if (p.tiles) {
-    const int64_t all = (d + 63) / 64, parts = 256 / (p.rows * p.strips);
+    const int64_t all = (n + 63) / 64, parts = 256 / (p.rows * p.strips);
     split(p, all, parts < all / 8 ? parts : all / 8);
-    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)c * 4;
-  } else if (back) {
+    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)k * 4;
+  } else {
     p.mb = exact || m <= 16 ? 1 : 2;
     p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
-    p.strips = (c + kTStrip - 1) / kTStrip;
+    p.strips = (k + kTStrip - 1) / kTStrip;
     // a workgroup a CU; two steps a wave at least, for the partial sums cost as much as
     // the codes with 16 rows and 44 parts of [11008, 4096]
-    const int64_t all = (d + 31) / 32, parts = 256 / (p.rows * p.strips), most = (all + 2 * kTWaves - 1) / (2 * kTWaves);
+    const int64_t all = (n + 31) / 32, parts = 256 / (p.rows * p.strips), most = (all + 2 * kTWaves - 1) / (2 * kTWaves);
     split(p, all, parts < most ? parts : most);
-    p.bytes = (size_t)p.parts * (size_t)m * (size_t)c * 4;
+    p.bytes = (size_t)p.parts * (size_t)m * (size_t)k * 4;
   }
   return p;
 }
@@ -444,10 +460,11 @@ hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, 
   float* part = (float*)ws;
   hipError_t e;
   if (p.tiles) {
-    if (p.parts == 1) return launch_w4a16_tiles(a, lo, st);
-    a.y = ws, a.y_dtype = W4_F32;
-    // forward, the first part's tiles add the low-rank part, back the sum, which low may come to in parts
-    e = launch_w4a16_tiles(a, a.back ? LoraOut{} : lo, st);
+    if (p.parts > 1) a.y = ws, a.y_dtype = W4_F32;
+    // With parts, forward the first one's tiles add the low-rank part, back the sum, which low may come to in parts.
+    if (!a.back) e = launch_w4a16_lora_gemm(a, lo, st);
+    else e = launch_w4a16_tiles(a, p.parts == 1 ? lo : LoraOut{}, st);
+    if (p.parts == 1) return e;
   } else if (!a.back) {
     return launch_w4a16_lora_rows(x, x_dtype, a.m, a.k, a.packed, a.scales, a.zeros, a.sz_dtype, a.n, a.g, a.y,
                                   a.y_dtype, lo, st);

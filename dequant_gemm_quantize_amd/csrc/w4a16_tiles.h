@@ -1,14 +1,12 @@
-// W4A16 products of many rows of bf16 x, in both directions, with low-rank adapters:
-//   forward  y[m, n]  = sum_k x[m, k] (q[n, k] - zp[n, j]) s[n, j]   (+ sum_r low[m, r] B[l(m), n, r])
-//   back     dx[m, k] = sum_n dy[m, n] (q[n, k] - zp[n, j]) s[n, j]  (+ sum_r low[m, r] A[l(m), r, k])
+// Transposed W4A16 product of many rows of bf16 dy, with low-rank adapters:
+//   dx[m, k] = sum_n dy[m, n] (q[n, k] - zp[n, j]) s[n, j]  (+ sum_r low[m, r] A[l(m), r, k])
 // on v_mfma_f32_32x32x16_bf16 with float32 accumulation; j is the group of column k.
-// Below, x is the dense operand [M, D], D what the sum runs over, C the columns of the result.
 //
-// Workgroup tile 64 MI x 128, 64 values of D a step.  Four waves multiply, each 32 MI x 64
-// of the tile, and four load and convert, one of each on every SIMD.  x, codes,
+// Workgroup tile 64 MI x 128, 64 weight rows a step.  Four waves multiply, each 32 MI x 64
+// of the tile, and four load and convert, one of each on every SIMD.  dy, codes,
 // scales and zero-points go from memory to LDS directly; the converting waves turn codes into weights,
-// once a workgroup, in the operand tile [128 columns of the result][64 values of D].
-// Back, a word of codes holds eight columns of one weight row while the sum runs over rows: a
+// once a workgroup, in the operand tile [128 columns of dx][64 weight rows].
+// A word of codes holds eight columns of one weight row while the sum runs over rows: a
 // thread takes the same eight columns of four rows and stores four rows of each column
 // as one 8-byte piece.  The pairs that v_cvt_pk_bf16_f32 makes are two rows of one
 // column, so turning costs no instruction of its own.
@@ -17,7 +15,7 @@
 // does: half a step, 2^-8 at most, beside that of a bf16 result), two (exact with fp16 scales:
 // 15 bits) or three (float32 scales).
 //
-// Bound by feeding the matrix cores, busy half the time: 2048 rows of [11008, 4096] back 169 us (1.09
+// Bound by feeding the matrix cores, busy half the time: 2048 rows of [11008, 4096] 169 us (1.09
 // PFLOP/s), 333 rows of [4096, 11008] in two parts 100.  All waves doing everything took 201.
 #pragma once
 
@@ -32,27 +30,24 @@ namespace w4 {
 
 namespace {
 
-constexpr int kTileN = 128;  // columns of the result a tile
-constexpr int kTileD = 64;   // values of D a step
+constexpr int kTileK = 128;  // columns of dx a tile
+constexpr int kTileN = 64;   // weight rows a step
 
-// SUBS: scale columns of an operand tile.  Back, groups of columns of the result: 1
-// (groups of a multiple of 128) or 4.  Forward, groups of a step: 1 (of a multiple of 64) or 2.
-template <bool BACK_, int MI_, int PW_, int SUBS_> struct TilePlan {
-  static constexpr bool BACK = BACK_;
+// SUBS: groups of an operand tile's columns, 1 (groups of a multiple of 128) or 4.
+template <int MI_, int PW_, int SUBS_> struct TilePlan {
   static constexpr int MI = MI_, PW = PW_, SUBS = SUBS_;
   static constexpr int BM = 64 * MI;  // four multiplying waves, two by two of 32 MI x 64
-  static constexpr int AS = MI * PW <= 4 ? 3 : 2;  // stages of x: what fits in 160 KB
-  // bytes of a stage: x (AS of them), weights (two), codes, and scales with zero-points (three).
-  // Forward, a stage of codes is two steps: 64 bytes of a row.
-  static constexpr int A_STAGE = BM * 128, B_PART = kTileN * 128, B_STAGE = PW * B_PART;
-  static constexpr int RAW_STAGE = kTileD * kTileN / 2 * (BACK ? 1 : 2), TAB_HALF = SUBS * (BACK ? 256 : 512);
+  static constexpr int AS = MI * PW <= 4 ? 3 : 2;  // stages of dy: what fits in 160 KB
+  // bytes of a stage: dy (AS of them), weights (two), codes, and scales with zero-points (three)
+  static constexpr int A_STAGE = BM * 128, B_PART = kTileK * 128, B_STAGE = PW * B_PART;
+  static constexpr int RAW_STAGE = kTileN * kTileK / 2, TAB_HALF = SUBS * 256;
   static constexpr int TAB_STAGE = 2 * TAB_HALF;
   static constexpr int B_AT = AS * A_STAGE, RAW_AT = B_AT + 2 * B_STAGE, TAB_AT = RAW_AT + 3 * RAW_STAGE;
   static constexpr size_t lds = TAB_AT + 3 * TAB_STAGE;
   static_assert(lds <= 160 * 1024, "LDS of a CU");
 };
 
-// Back: slot (16 bytes) of chunk c (0 .. 3) of row n of a stage of codes: the 16 lanes
+// Slot (16 bytes) of chunk c (0 .. 3) of row n of a stage of codes: the 16 lanes
 // that read one chunk of rows 4 b + i, b = 0 .. 15, meet every bank twice, the least there is.
 __device__ __forceinline__ int raw_row(int slot) {  // the row that a slot has
   const int p = slot >> 2;
@@ -63,25 +58,13 @@ __device__ __forceinline__ int raw_slot(int n, int c) {
   return 4 * p + (c ^ ((n >> 3) & 3));
 }
 
-// Forward: the same for row n of 128.  The 8 lanes that read together have rows
-// of four neighbouring places and two chunks of a step, which lie on all banks.
-__device__ __forceinline__ int raw_row_forward(int slot) {
-  const int p = slot >> 2;
-  return (p & 63) * 2 + (p >> 6);
-}
-__device__ __forceinline__ int raw_slot_forward(int n, int c) {
-  const int p = (n >> 1) | (n & 1) << 6;
-  return 4 * p + (c ^ ((p >> 1 & 1) << 1));
-}
-
 // acc += low out for the wave's 32 MI rows from m0 (those before mend) and 64
 // columns from c0, segment by segment: rows of other segments are zero in the operand, and
 // keep their sums, since zero times an adapter that is not finite would be NaN.  (Loads of a block
-// of ranks all issued ahead need registers that the sums have: 1024 rows of [11008, 4096], 16 ranks, 126 -> 162 us.)
-// BACK: out is [L, R, C], otherwise [L, C, R].
-template <bool BACK, int MI>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, int lane, f32x16 (&acc)[MI][2], int64_t C, int64_t m0,
-                                             int64_t mend, int64_t c0) {
+// of ranks all issued ahead need registers that the sums have: forward, 1024 rows of [11008, 4096], 16 ranks, 126 -> 162 us.)
+template <int MI>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int lane, f32x16 (&acc)[MI][2], int64_t K, int64_t m0,
+                                             int64_t mend, int64_t k0) {
   const int r = lane & 31, h = lane >> 5;
   const int64_t top = mend < m0 + 32 * MI ? mend : m0 + 32 * MI;
   for (int s = segments_before(ad.offsets, ad.segments, m0, lane); s < ad.segments; ++s) {
@@ -94,32 +77,21 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int lane, f32x1
       bf16x8 w[2][3];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int64_t c = c0 + 32 * j + r;
-        const bool real = in && c < C;
+        const int64_t k = k0 + 32 * j + r, at = ((int64_t)l * ad.rank + r0 + 8 * h) * K + k;
+        const bool real = in && k < K;
         w[j][0] = w[j][1] = w[j][2] = zero8();
-        bf16x8 one[1];
-        if constexpr (BACK) {
-          const int64_t at = ((int64_t)l * ad.rank + r0 + 8 * h) * C + c;
-          if (ad.wide) {
-            float v[8];
+        if (ad.wide) {
+          float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = real ? ((const float*)ad.out)[at + i * C] : 0.0f;
-            pack8(v, w[j]);
-          } else {
-            uint16_t v[8];
+          for (int i = 0; i < 8; ++i) v[i] = real ? ((const float*)ad.out)[at + i * K] : 0.0f;
+          pack8(v, w[j]);
+        } else {
+          uint16_t v[8];
+          bf16x8 one[1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = real ? ((const uint16_t*)ad.out)[at + i * C] : (uint16_t)0;
-            pack8(v, one);
-            w[j][0] = one[0];
-          }
-        } else if (real) {
-          const int64_t at = ((int64_t)l * C + c) * ad.rank + r0 + 8 * h;
-          if (ad.wide) {
-            load8((const float*)ad.out + at, w[j]);
-          } else {
-            load8((const uint16_t*)ad.out + at, one);
-            w[j][0] = one[0];
-          }
+          for (int i = 0; i < 8; ++i) v[i] = real ? ((const uint16_t*)ad.out)[at + i * K] : (uint16_t)0;
+          pack8(v, one);
+          w[j][0] = one[0];
         }
       }
 #pragma unroll
@@ -162,26 +134,24 @@ __device__ __forceinline__ void slice_order() {
 
 }  // namespace
 
-// Steps first .. first + steps - 1 of 64 values of D are part blockIdx.y's; with
-// parts its float32 sums go to y + blockIdx.y * M * C (TY float), the first part's with the adapters, else the result to y.
+// Steps first .. first + steps - 1 of 64 weight rows are part blockIdx.y's; with
+// parts its float32 sums go to dx + blockIdx.y * M * K (TY float), without adapters, else the result to dx.
 template <typename T, typename TS, typename TY>
 __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
-    const uint16_t* __restrict__ x, int64_t M, const uint8_t* __restrict__ packed, const void* __restrict__ scales,
-    const void* __restrict__ zeros, int64_t N, int64_t K, int g, int steps, Adapters ad, TY* __restrict__ y,
-    uint32_t tiles_m, uint32_t tiles_c) {
+    const uint16_t* __restrict__ dy, int64_t M, const uint8_t* __restrict__ packed, const void* __restrict__ scales,
+    const void* __restrict__ zeros, int64_t N, int64_t K, int g, int steps, Adapters ad, TY* __restrict__ dx,
+    uint32_t tiles_m, uint32_t tiles_k) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
-  constexpr bool BACK = T::BACK;
   constexpr int MI = T::MI, BM = T::BM, PW = T::PW, SUBS = T::SUBS;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t t, tm, tc;
+  uint32_t t, tm, tk;
   int whole;
-  if (!xcd_tile<32, false>(tiles_m * tiles_c, t, whole)) return;
-  band(t, tiles_m, tiles_c, tm, tc);
-  const int64_t D = BACK ? N : K, C = BACK ? K : N;
-  const int64_t m0 = (int64_t)BM * tm, c0 = (int64_t)kTileN * tc;
-  const uint32_t half = (uint32_t)(K / 2), ng = (uint32_t)(K / g), drow = (uint32_t)(2 * D);
-  const int all = (int)((D + kTileD - 1) / kTileD), first = (int)blockIdx.y * steps;
+  if (!xcd_tile<32, false>(tiles_m * tiles_k, t, whole)) return;
+  band(t, tiles_m, tiles_k, tm, tk);
+  const int64_t m0 = (int64_t)BM * tm, k0 = (int64_t)kTileK * tk;
+  const uint32_t half = (uint32_t)(K / 2), ng = (uint32_t)(K / g), drow = (uint32_t)(2 * N);
+  const int all = (int)((N + kTileN - 1) / kTileN), first = (int)blockIdx.y * steps;
   const int nst = all - first < steps ? all - first : steps;  // steps of this part
 
   constexpr std::integral_constant<int, 0> n0{};
@@ -216,10 +186,10 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
   // the operands of step t have all been read, and those of t + 1 are whole, is passed by all.
   if (w >= 4) {
     const int pw = w - 4;
-    // x -> LDS: 8 rows x 128 bytes a load; slot s of row r holds chunk s ^ ((r / 2) % 8)
+    // dy -> LDS: 8 rows x 128 bytes a load; slot s of row r holds chunk s ^ ((r / 2) % 8)
     constexpr int LA = BM / 32;
     const uint32_t mrows = (uint32_t)(M - m0 < BM ? M - m0 : BM);
-    const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(x + m0 * D), mrows * drow);
+    const __amdgpu_buffer_rsrc_t ar = buf_rsrc_n(uniform_ptr(dy + m0 * N), mrows * drow);
     uint32_t ao[LA];
     const int lrow = lane >> 3, slot = lane & 7;
 #pragma unroll
@@ -228,77 +198,39 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
       ao[i] = (uint32_t)row * drow + 16u * (slot ^ ((row >> 1) & 7));
     }
     auto a_issue = [&](int st, int stage, int i) {  // load i of a step
-      const uint32_t d0 = st < nst ? (uint32_t)(first + st) * kTileD : (uint32_t)D, left = (uint32_t)D - d0;
-      const int row = 8 * (pw * LA + i) + lrow;  // chunks past the last value of D read as zero
+      const uint32_t n0 = st < nst ? (uint32_t)(first + st) * kTileN : (uint32_t)N, left = (uint32_t)N - n0;
+      const int row = 8 * (pw * LA + i) + lrow;  // chunks past the last weight row read as zero
       load_lds_at(ar, sm + stage * T::A_STAGE + 1024 * (pw * LA + i),
-                  8u * (slot ^ ((row >> 1) & 7)) < left ? ao[i] : kPastEnd, 2 * d0);
+                  8u * (slot ^ ((row >> 1) & 7)) < left ? ao[i] : kPastEnd, 2 * n0);
     };
     // Codes, scales and zero-points -> LDS.  Codes: 16 bytes a lane.  Scales: for
     // each weight row the 4 bytes that hold the value of a group (with fp16 two values,
     // of which the value's number in the array, odd or even, says which; the
-    // array has an even number, so no word lies across its end).
-    //
-    // Back, a step is 64 weight rows.  SUBS 1: the first of these waves loads scales, the second
-    // zero-points; SUBS 4: wave i those of columns 32 i .. 32 i + 31.
-    // Forward, the tile is 128 weight rows: waves 0 and 1 load scales, 2 and 3 zero-points.
-    const int sub0 = BACK && SUBS > 1 ? pw : 0;
-    const int64_t kc = c0 + 32 * sub0;
-    const uint32_t gi = BACK ? (uint32_t)((kc < K ? kc : K - 1) / g) : 0;  // forward, the group goes with the step
-    const int64_t crows = C - c0 < kTileN ? C - c0 : kTileN;               // forward: weight rows of the tile
-    // forward: 32-column blocks of a group, and its reciprocal, exact below 2^16 blocks
-    const uint32_t bpg = (uint32_t)g / 32, inv = 0xffffffffu / bpg + 1;
-    auto group = [&](uint32_t block) {
-      const uint32_t j = bpg == 1 ? block : __umulhi(block, inv);
-      return j < ng ? j : ng - 1;
-    };
+    // array has an even number, so no word lies across its end).  SUBS 1: the first of these waves loads
+    // scales, the second zero-points; SUBS 4: wave i those of columns 32 i .. 32 i + 31.
+    const int sub0 = SUBS > 1 ? pw : 0;
+    const int64_t kc = k0 + 32 * sub0;
+    const uint32_t gi = (uint32_t)((kc < K ? kc : K - 1) / g);
     const int rs = 64 * pw + lane;  // the lane's slot of a load of codes by all four waves
-    uint32_t ro[BACK ? 1 : 2];
-    if constexpr (BACK) {
-      const int rn = raw_row(rs), rc = (rs & 3) ^ ((rn >> 3) & 3);
-      ro[0] = c0 / 2 + 16 * rc < half ? (uint32_t)rn * half + (uint32_t)(c0 / 2) + 16u * rc : kPastEnd;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int s = rs + 256 * i, p = s >> 2, rn = raw_row_forward(s), rc = (s & 3) ^ ((p >> 1 & 1) << 1);
-        ro[i] = (uint32_t)rn * half + 16u * rc;
-      }
-    }
-    // codes of step st (back), or of steps 2 st and 2 st + 1 (forward)
+    const int rn = raw_row(rs), rc = (rs & 3) ^ ((rn >> 3) & 3);
+    const uint32_t ro = k0 / 2 + 16 * rc < half ? (uint32_t)rn * half + (uint32_t)(k0 / 2) + 16u * rc : kPastEnd;
     auto r_issue = [&](int st, int stage) {
       uint8_t* dst = sm + T::RAW_AT + stage * T::RAW_STAGE + 1024 * pw;
-      if constexpr (BACK) {
-        const int64_t d0 = (int64_t)(first + st) * kTileD;
-        const int64_t have = st < nst ? (N - d0 < kTileD ? N - d0 : kTileD) : 0;
-        load_lds(buf_rsrc_n(uniform_ptr(packed + (st < nst ? d0 : 0) * half), (uint32_t)have * half), dst, ro[0]);
-      } else {
-        const __amdgpu_buffer_rsrc_t r = buf_rsrc_n(uniform_ptr(packed + c0 * half), (uint32_t)crows * half);
-        const uint32_t o = (uint32_t)(first + 2 * st) * (kTileD / 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) load_lds(r, dst + 4096 * i, 2 * st < nst ? ro[i] + o : kPastEnd);
-      }
+      const int64_t n0 = (int64_t)(first + st) * kTileN;
+      const int64_t have = st < nst ? (N - n0 < kTileN ? N - n0 : kTileN) : 0;
+      load_lds(buf_rsrc_n(uniform_ptr(packed + (st < nst ? n0 : 0) * half), (uint32_t)have * half), dst, ro);
     };
     auto s_issue = [&](int st, int stage) {
       uint8_t* tab = sm + T::TAB_AT + stage * T::TAB_STAGE;
-      if constexpr (BACK) {
-        const int64_t d0 = (int64_t)(first + st) * kTileD;
-        const int64_t have = st < nst ? (N - d0 < kTileD ? N - d0 : kTileD) : 0;
-        const uint32_t bytes = (uint32_t)have * ng * (uint32_t)sizeof(TS);
-        const int64_t byte = (st < nst ? d0 : 0) * ng * (int64_t)sizeof(TS);
-        const uint32_t so = ((uint32_t)lane * ng + gi) * (uint32_t)sizeof(TS) & ~3u;
-        if (SUBS > 1 || pw == 0)
-          load_lds4(buf_rsrc_n(uniform_ptr((const char*)scales + byte), bytes), tab + 256 * sub0, so);
-        if (SUBS > 1 || pw == 1)
-          load_lds4(buf_rsrc_n(uniform_ptr((const char*)zeros + byte), bytes), tab + T::TAB_HALF + 256 * sub0, so);
-      } else {
-        const char* of = (const char*)(pw < 2 ? scales : zeros) + c0 * ng * (int64_t)sizeof(TS);
-        const __amdgpu_buffer_rsrc_t r = buf_rsrc_n(uniform_ptr(of), (uint32_t)crows * ng * (uint32_t)sizeof(TS));
-        const uint32_t row = 64 * (pw & 1) + lane;
-#pragma unroll
-        for (int i = 0; i < SUBS; ++i) {
-          const uint32_t so = (row * ng + group(2 * (uint32_t)(first + st) + i)) * (uint32_t)sizeof(TS) & ~3u;
-          load_lds4(r, tab + (pw < 2 ? 0 : T::TAB_HALF) + 512 * i + 256 * (pw & 1), st < nst ? so : kPastEnd);
-        }
-      }
+      const int64_t n0 = (int64_t)(first + st) * kTileN;
+      const int64_t have = st < nst ? (N - n0 < kTileN ? N - n0 : kTileN) : 0;
+      const uint32_t bytes = (uint32_t)have * ng * (uint32_t)sizeof(TS);
+      const int64_t byte = (st < nst ? n0 : 0) * ng * (int64_t)sizeof(TS);
+      const uint32_t so = ((uint32_t)lane * ng + gi) * (uint32_t)sizeof(TS) & ~3u;
+      if (SUBS > 1 || pw == 0)
+        load_lds4(buf_rsrc_n(uniform_ptr((const char*)scales + byte), bytes), tab + 256 * sub0, so);
+      if (SUBS > 1 || pw == 1)
+        load_lds4(buf_rsrc_n(uniform_ptr((const char*)zeros + byte), bytes), tab + T::TAB_HALF + 256 * sub0, so);
     };
 
     // 4 floats -> two words of bf16, in PW parts
@@ -331,80 +263,46 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
       return PW == 1 ? fmaf(q, s, z) : (q - z) * s;
     };
 
-    // Back: the thread's piece is columns 8 kb .. 8 kb + 7 of weight rows 4 b .. 4 b + 3.
+    // The thread's piece is columns 8 kb .. 8 kb + 7 of weight rows 4 b .. 4 b + 3.
     const int b = lane & 15, kb = 4 * pw + (lane >> 4);
     int rawo[4], bo[4];
     uint32_t odd[4];  // whether the scale is the upper half of its word
-    // Forward: 32 columns (half hf of a step's 64) of weight row n.
-    const int hf = lane & 1, n = 32 * pw + 2 * (lane >> 1 & 15) + (lane >> 5);
-    if constexpr (BACK) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        rawo[i] = T::RAW_AT + 16 * raw_slot(4 * b + i, pw) + 4 * (kb & 3);
-        odd[i] = (gi + i * ng) & 1;
-        // row r of the operand tile has its chunk of D values 8 (b / 2) .. at slot (b / 2) ^ ((r / 2) % 8)
-        bo[i] = T::B_AT + 128 * (8 * kb + 2 * i) + 16 * ((b >> 1) ^ ((4 * kb + i) & 7)) + 8 * (b & 1);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bo[i] = T::B_AT + 128 * n + 16 * ((4 * hf + i) ^ ((n >> 1) & 7));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) rawo[i] = T::RAW_AT + 16 * raw_slot_forward(n, 2 * i + hf);
+    for (int i = 0; i < 4; ++i) {
+      rawo[i] = T::RAW_AT + 16 * raw_slot(4 * b + i, pw) + 4 * (kb & 3);
+      odd[i] = (gi + i * ng) & 1;
+      // row r of the operand tile has its chunk of weight rows 8 (b / 2) .. at slot (b / 2) ^ ((r / 2) % 8)
+      bo[i] = T::B_AT + 128 * (8 * kb + 2 * i) + 16 * ((b >> 1) ^ ((4 * kb + i) & 7)) + 8 * (b & 1);
     }
-    // The weights of step st, from codes and scales of stages rs_ and ss to operands of stage bs; `par` is
-    // st % 2.  `load` is called between the eight parts of the work.
-    auto convert = [&](int st, int rs_, int par, int ss, int bs, auto load) {
+    // The weights of a step, from codes and scales of stages rs_ and ss to operands of stage bs.  `load` is
+    // called between the eight parts of the work.
+    auto convert = [&](int rs_, int ss, int bs, auto load) {
       uint8_t* out = sm + bs * T::B_STAGE;
       const uint8_t* tb = sm + T::TAB_AT + ss * T::TAB_STAGE;
+      const u32x4 sw = *(const u32x4*)(tb + 256 * sub0 + 16 * b),
+                  zw = *(const u32x4*)(tb + T::TAB_HALF + 256 * sub0 + 16 * b);
       uint32_t lo[4], hi[4];
-      if constexpr (BACK) {
-        const u32x4 sw = *(const u32x4*)(tb + 256 * sub0 + 16 * b),
-                    zw = *(const u32x4*)(tb + T::TAB_HALF + 256 * sub0 + 16 * b);
-        float s[4], z[4];
+      float s[4], z[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t p = *(const uint32_t*)(sm + rawo[i] + rs_ * T::RAW_STAGE);
-          s[i] = value(sw[i], odd[i]), z[i] = value(zw[i], odd[i]);
-          if constexpr (PW == 1) z[i] *= -s[i];
-          lo[i] = p & 0x0f0f0f0fu;
-          hi[i] = (p >> 4) & 0x0f0f0f0fu;
-          asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = *(const uint32_t*)(sm + rawo[i] + rs_ * T::RAW_STAGE);
+        s[i] = value(sw[i], odd[i]), z[i] = value(zw[i], odd[i]);
+        if constexpr (PW == 1) z[i] *= -s[i];
+        lo[i] = p & 0x0f0f0f0fu;
+        hi[i] = (p >> 4) & 0x0f0f0f0fu;
+        asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          load(j);
-          float v[4];
+      for (int j = 0; j < 8; ++j) {
+        load(j);
+        float v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = weight((j & 1 ? hi[i] : lo[i]) >> (8 * (j >> 1)), s[i], z[i]);
-          put4(out + bo[j >> 1] + 128 * (j & 1), v);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      } else {
-        const u32x4 p = *(const u32x4*)(sm + rawo[par] + rs_ * T::RAW_STAGE);
-        const int at = 4 * n + (SUBS > 1 ? 512 * hf : 0);
-        const uint32_t e = (uint32_t)n * ng + group(2 * (uint32_t)(first + st) + (SUBS > 1 ? hf : 0));
-        const float s = value(*(const uint32_t*)(tb + at), e & 1);
-        float z = value(*(const uint32_t*)(tb + T::TAB_HALF + at), e & 1);
-        if constexpr (PW == 1) z *= -s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[i] = p[i] & 0x0f0f0f0fu;
-          hi[i] = (p[i] >> 4) & 0x0f0f0f0fu;
-          asm("" : "+v"(lo[i]), "+v"(hi[i]));  // as above
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {  // codes 4 (j % 2) .. of word j / 2
-          load(j);
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = weight((i & 1 ? hi : lo)[j >> 1] >> (16 * (j & 1) + 8 * (i >> 1)), s, z);
-          put4(out + bo[j >> 1] + 8 * (j & 1), v);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = weight((j & 1 ? hi[i] : lo[i]) >> (8 * (j >> 1)), s[i], z[i]);
+        put4(out + bo[j >> 1] + 128 * (j & 1), v);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // Stages of codes go by steps (back) or by pairs of steps (forward).
 #pragma unroll
     for (int i = 0; i < 3; ++i) r_issue(i, i), s_issue(i, i);
 #pragma unroll
@@ -414,29 +312,26 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     barrier();  // all four waves' codes and scales of step 0 are there
-    convert(0, 0, 0, 0, 0, [](int) {});
+    convert(0, 0, 0, [](int) {});
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     barrier();
-    // In step t the loads of x of t + 2 (t + 1 with two stages), of scales of t + 3 and of codes of t + 3 (forward, in
-    // odd steps, of t + 5 and t + 6) are issued, into the places that step t - 1 has
-    // left, and the weights of t + 1 made.  Loads come in from the L2 cache 1000 to 2000 cycles
-    // after their issue: with three stages they have two steps.  The loads of x are
-    // spread over the conversion; issued together they held it up (back, 2048 rows of
+    // In step t the loads of dy of t + 2 (t + 1 with two stages), of scales and of codes of t + 3 are issued, into
+    // the places that step t - 1 has left, and the weights of t + 1 made.  Loads come in from the L2 cache
+    // 1000 to 2000 cycles after their issue: with three stages they have two steps.  The loads of dy are
+    // spread over the conversion; issued together they held it up (2048 rows of
     // [11008, 4096]: 185 us against 169).
     all_steps([&](int st, auto number) {
       constexpr int k = decltype(number)::value;
-      constexpr bool codes = BACK || k % 2 == 1;
-      if constexpr (BACK) r_issue(st + 3, k % 3);
-      else if constexpr (codes) r_issue((st + 5) / 2, (k + 5) / 2 % 3);
+      r_issue(st + 3, k % 3);
       s_issue(st + 3, k % 3);
-      convert(st + 1, BACK ? (k + 1) % 3 : (k + 1) / 2 % 3, (k + 1) % 2, (k + 1) % 3, (k + 1) % 2, [&](int j) {
+      convert((k + 1) % 3, (k + 1) % 3, (k + 1) % 2, [&](int j) {
         if (j % (8 / LA) == 0) a_issue(st + T::AS - 1, (k + T::AS - 1) % T::AS, j / (8 / LA));
       });
-      // all but this step's loads; with two stages of x, those too
-      constexpr int codes_n = !codes ? 0 : BACK ? 1 : 2, scales_n = BACK ? (SUBS > 1 ? 2 : 1) : SUBS;
+      // all but this step's loads; with two stages of dy, those too
+      constexpr int scales_n = SUBS > 1 ? 2 : 1;
       if constexpr (T::AS == 2) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      else if (BACK && SUBS == 1 && pw > 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + codes_n) : "memory");
-      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + codes_n + scales_n) : "memory");
+      else if (SUBS == 1 && pw > 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 1) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LA + 1 + scales_n) : "memory");
       barrier();
     });
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS when the sums are turned there
@@ -505,26 +400,26 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
   });
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   barrier();
-  const int64_t mw = m0 + 32 * MI * wm, cw = c0 + 64 * wn;
-  if (ad.count > 0 && blockIdx.y == 0) add_adapters<BACK, MI>(ad, lane, acc, C, mw, M, cw);
+  const int64_t mw = m0 + 32 * MI * wm, kw = k0 + 64 * wn;
+  if (ad.count > 0) add_adapters<MI>(ad, lane, acc, K, mw, M, kw);
   constexpr int TURN = turn_bytes<TY, 2>();
   static_assert(4 * TURN <= (int)T::lds, "the waves' turning places fit in LDS");
-  turn_store<TY, MI, 2, true>(sm + w * TURN, lane, acc, y + (int64_t)blockIdx.y * M * C, C, mw, M, cw);
+  turn_store<TY, MI, 2, true>(sm + w * TURN, lane, acc, dx + (int64_t)blockIdx.y * M * K, K, mw, M, kw);
 }
 
-template <bool BACK, int MI, int PW, int SUBS, typename TS, typename TY>
+template <int MI, int PW, int SUBS, typename TS, typename TY>
 static hipError_t tiles_go(const TilesArgs& a, const Adapters& ad, hipStream_t st) {
-  typedef TilePlan<BACK, MI, PW, SUBS> T;
+  typedef TilePlan<MI, PW, SUBS> T;
   static std::atomic<uint64_t> attr_done{0};  // LDS above the 64 KB default
   const hipError_t e = once_per_device(attr_done, [] {
     return hipFuncSetAttribute((const void*)k_w4a16_tiles<T, TS, TY>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                (int)T::lds);
   });
   if (e != hipSuccess) return e;
-  const int64_t tiles_m = (a.m + T::BM - 1) / T::BM, tiles_c = ((BACK ? a.k : a.n) + kTileN - 1) / kTileN;
-  const dim3 grid((unsigned)xcd_grid<32, false>(tiles_m * tiles_c), (unsigned)a.parts);
+  const int64_t tiles_m = (a.m + T::BM - 1) / T::BM, tiles_k = (a.k + kTileK - 1) / kTileK;
+  const dim3 grid((unsigned)xcd_grid<32, false>(tiles_m * tiles_k), (unsigned)a.parts);
   k_w4a16_tiles<T, TS, TY><<<grid, 512, T::lds, st>>>((const uint16_t*)a.x, a.m, a.packed, a.scales, a.zeros, a.n, a.k,
-                                                     a.g, a.steps, ad, (TY*)a.y, (uint32_t)tiles_m, (uint32_t)tiles_c);
+                                                     a.g, a.steps, ad, (TY*)a.y, (uint32_t)tiles_m, (uint32_t)tiles_k);
   return hipGetLastError();
 }
 

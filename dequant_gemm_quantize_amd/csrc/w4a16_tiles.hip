@@ -1,33 +1,31 @@
-// W4A16 products of many rows: which kernel of w4a16_tiles.h a call takes.
+// Transposed W4A16 product of many rows: which kernel of w4a16_tiles.h a call takes.
 #include "w4a16_tiles.h"
 
 namespace w4 {
 
-template <bool BACK, int MI, int PW, typename TS, typename TY>
+template <int MI, int PW, typename TS, typename TY>
 static hipError_t tiles_subs(const TilesArgs& a, const Adapters& ad, hipStream_t st) {
-  constexpr int many = BACK ? 4 : 2;
-  if (a.g % (BACK ? 128 : 64) == 0) return tiles_go<BACK, MI, PW, 1, TS, TY>(a, ad, st);
-  return tiles_go<BACK, MI, PW, many, TS, TY>(a, ad, st);
+  if (a.g % 128 == 0) return tiles_go<MI, PW, 1, TS, TY>(a, ad, st);
+  return tiles_go<MI, PW, 4, TS, TY>(a, ad, st);
 }
 
-template <bool BACK, typename TS>
+template <typename TS>
 static hipError_t tiles_types(const TilesArgs& a, const Adapters& ad, hipStream_t st) {
   if (a.pw == 1) {
     if (a.y_dtype == W4_F32)
-      return a.mi == 2 ? tiles_subs<BACK, 2, 1, TS, float>(a, ad, st) : tiles_subs<BACK, 4, 1, TS, float>(a, ad, st);
-    return a.mi == 2 ? tiles_subs<BACK, 2, 1, TS, __bf16>(a, ad, st) : tiles_subs<BACK, 4, 1, TS, __bf16>(a, ad, st);
+      return a.mi == 2 ? tiles_subs<2, 1, TS, float>(a, ad, st) : tiles_subs<4, 1, TS, float>(a, ad, st);
+    return a.mi == 2 ? tiles_subs<2, 1, TS, __bf16>(a, ad, st) : tiles_subs<4, 1, TS, __bf16>(a, ad, st);
   }
   if constexpr (sizeof(TS) == 2)
-    return a.mi == 2 ? tiles_subs<BACK, 2, 2, TS, float>(a, ad, st) : tiles_subs<BACK, 4, 2, TS, float>(a, ad, st);
+    return a.mi == 2 ? tiles_subs<2, 2, TS, float>(a, ad, st) : tiles_subs<4, 2, TS, float>(a, ad, st);
   else
-    return tiles_subs<BACK, 2, 3, TS, float>(a, ad, st);
+    return tiles_subs<2, 3, TS, float>(a, ad, st);
 }
 
 hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st) {
   const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
                     (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
-  if (a.back) return a.sz_dtype == W4_F16 ? tiles_types<true, _Float16>(a, ad, st) : tiles_types<true, float>(a, ad, st);
-  return a.sz_dtype == W4_F16 ? tiles_types<false, _Float16>(a, ad, st) : tiles_types<false, float>(a, ad, st);
+  return a.sz_dtype == W4_F16 ? tiles_types<_Float16>(a, ad, st) : tiles_types<float>(a, ad, st);
 }
 
 }  // namespace w4

@@ -443,7 +443,8 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *     dx[m, k] = sum_n dy[m, n] W[n, k] + sum_r v[m, r] A[l, r, k]
  *   v is an output; rows of no adapter are left as they were.
  *
- *   In all three sums are float32, and the result is rounded once.  With bf16 x (dy) and a
+ *   In all three sums are float32, and the result is rounded once.
+ *   w4a16_lora_matmul rounds no weight.  In the transposed products with bf16 dy and a
  *   bf16 result the weight may be rounded to bf16 before the product, as in
  *   w4a16_matmul; otherwise no operand loses bits that float32 has.
  *   workspace: device memory, 16-byte aligned, of at least the bytes that the
