@@ -111,6 +111,26 @@ __device__ __forceinline__ void split8(u32x4 v0, u32x4 v1, bf16x8 (&out)[3]) {
   }
 }
 
+// 8 float32 as hi + lo, each 8 bf16: the upper halves, and what they lack rounded to nearest; off by 2^-16 of a value at
+// most, and exact where it has no more than 16 bits.
+__device__ __forceinline__ void split8(u32x4 v0, u32x4 v1, bf16x8 (&out)[2]) {
+  u32x4 r;
+  r.x = __builtin_amdgcn_perm(v0.y, v0.x, 0x07060302u);
+  r.y = __builtin_amdgcn_perm(v0.w, v0.z, 0x07060302u);
+  r.z = __builtin_amdgcn_perm(v1.y, v1.x, 0x07060302u);
+  r.w = __builtin_amdgcn_perm(v1.w, v1.z, 0x07060302u);
+  out[0] = __builtin_bit_cast(bf16x8, r);
+  float left[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    left[i] = __uint_as_float(v0[i]) - __uint_as_float(v0[i] & 0xffff0000u);
+    left[4 + i] = __uint_as_float(v1[i]) - __uint_as_float(v1[i] & 0xffff0000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)left[2 * i], (__bf16)left[2 * i + 1]});
+  out[1] = __builtin_bit_cast(bf16x8, r);
+}
+
 __device__ __forceinline__ bf16x8 zero8() { return __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0}); }
 
 // bf16 parts of a type's values: what a value is the exact sum of.

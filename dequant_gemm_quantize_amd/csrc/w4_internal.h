@@ -171,8 +171,8 @@ struct LoraOut {
   float* whole;  // and where it leaves the sums of the rows that have an adapter
 };
 // A W4A16 product of m rows: forward x [m, k] W^T, back x [m, n] W.  In tiles, for bf16 x: of 32 mi
-// rows forward; back of 64 mi, with pw bf16 parts of a weight (1, or 2 with fp16 scales and 3 with float32
-// ones for a float32 result).  With parts > 1 float32 partial sums of `steps` steps each (256 columns
+// rows forward; back of 64 mi, with pw bf16 parts of a weight (2, or 3 with float32
+// scales and a float32 result).  With parts > 1 float32 partial sums of `steps` steps each (256 columns
 // forward, 64 weight rows back), forward the first of them with the low-rank part.
 struct TilesArgs {
   bool back;

@@ -16,9 +16,9 @@
 // Back, many rows of bf16 dy take tiles (w4a16_tiles.h).  Both products of many rows split the
 // sum where the tiles are few.
 //
-// Rounding: forward none of a weight.  Back, bf16 dy with a bf16 result takes a weight rounded to bf16, as
-// w4a16_matmul does (half a step, 2^-8 at most, beside the result's own); otherwise the weight is the
-// exact sum of bf16 parts, two with fp16 scales (15 bits), three with float32 ones (24).
+// Rounding: forward none of a weight.  Back, a weight is the sum of bf16 parts: two with fp16 scales
+// (15 bits, so exact) and for a bf16 result of bf16 dy (16 bits, off by 2^-16 at most beside
+// the result's 2^-8), otherwise three (24 bits).
 #include "lds_gemm.h"
 #include "lora.h"
 #include "w4_internal.h"
@@ -49,9 +49,9 @@ void split(LoraPlan& p, int64_t all, int64_t parts) {
 }
 
 LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype) {
-  const bool exact = x_dtype != W4_BF16 || y_dtype != W4_BF16;  // weights keep their bits
+  const bool whole = x_dtype != W4_BF16 || y_dtype != W4_BF16;  // weights of float32 scales keep all their bits
   LoraPlan p{};
-  p.pw = !exact ? 1 : sz_dtype == W4_F16 ? 2 : 3;
+  p.pw = whole && sz_dtype == W4_F32 ? 3 : 2;
   p.parts = 1;
   if (!back) {
     // us of the few-row kernel / tiles, one request: [4096, 11008] 65 rows 52 / 35, 128 rows 63 / 39; [11008, 4096] 65 rows
@@ -75,8 +75,12 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
     return p;
   }
   // Rows of dy start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
-  // below 2^31 bytes.
+  // below 2^31 bytes.  us of the few-row kernel / tiles: [11008, 4096] 32 rows 27 / 29, 48 rows 34 / 30; [4096, 11008] 32
+  // rows 27 / 36, 48 rows 41 / 38; [4096, 4096] 24 rows 16 / 17, 48 rows 20 / 19.
   p.tiles = x_dtype == W4_BF16 && m > 32 && n % 8 == 0 && n <= ((int64_t)1 << 21);
+  // us in tiles of 128 / 256 rows: [11008, 4096] 100 rows 34 / 41, 200 rows 52 / 46, 2048 rows 358 / 266; [4096, 4096] 128
+  // rows 25 / 29, 256 rows 29 / 30, 333 rows 40 / 37; [4096, 11008] 333 rows 120 / 77 (600 rows, where the larger ones need a
+  // second round for two tiles, 124 / 167).  Three parts of a weight leave room for the smaller ones only.
   p.mi = p.pw == 3 || m <= 128 ? 2 : 4;
   p.rows = (m + 64 * p.mi - 1) / (64 * p.mi);
   p.strips = (k + 127) / 128;
@@ -86,12 +90,16 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
     split(p, all, parts < all / 8 ? parts : all / 8);
     p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)k * 4;
   } else {
-    p.mb = exact || m <= 16 ? 1 : 2;
-    p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
     p.strips = (k + kTStrip - 1) / kTStrip;
     // a workgroup a CU; two steps a wave at least, for the partial sums cost as much as
     // the codes with 16 rows and 44 parts of [11008, 4096]
-    const int64_t all = (n + 31) / 32, parts = 256 / (p.rows * p.strips), most = (all + 2 * kTWaves - 1) / (2 * kTWaves);
+    const int64_t all = (n + 31) / 32, most = (all + 2 * kTWaves - 1) / (2 * kTWaves);
+    // Two blocks of 16 rows a workgroup where those fill the CUs: us with one / two, 32 rows of [11008, 4096] 28 / 27, [4096,
+    // 11008] 35 / 27, [4096, 4096] 16 / 19; 128 rows of [2050, 2048] 18 / 19, 333 rows 35 / 28, of [11001, 4096] 255 / 162.
+    const bool two = x_dtype == W4_BF16 && p.pw == 2 && m > 16 && (m + 31) / 32 * p.strips * most >= 256;
+    p.mb = two ? 2 : 1;
+    p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
+    const int64_t parts = 256 / (p.rows * p.strips);
     split(p, all, parts < most ? parts : most);
     p.bytes = (size_t)p.parts * (size_t)m * (size_t)k * 4;
   }
@@ -107,7 +115,7 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
     const void* __restrict__ scales, const void* __restrict__ zeros, int64_t K, int g, int steps,
     float* __restrict__ part) {
   constexpr int PX = Parts<TX>::n;
-  constexpr int NA = PX + PW > 2 ? 2 : 1;  // sums: the upper parts' and the others'
+  constexpr int NA = MB == 1 ? 2 : 1;  // sums: the upper parts' and the others', or of both (registers)
   extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves / 2][16][256], then the waves' scales
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -191,7 +199,7 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
       const f32x4 s0 = *(const f32x4*)sp, s1 = *(const f32x4*)(sp + 4);
       f32x4 z0 = *(const f32x4*)(sp + 256), z1 = *(const f32x4*)(sp + 260);
       __builtin_amdgcn_wave_barrier();
-      if constexpr (PW == 1) {
+      if constexpr (PW == 2) {  // -zp s: exact with fp16 scales, 11 bits times 11
 #pragma unroll
         for (int i = 0; i < 4; ++i) z0[i] *= -s0[i], z1[i] *= -s1[i];
       }
@@ -211,55 +219,29 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
         for (int i = 0; i < 8; ++i) {
           const float q = (float)(uint8_t)((j & 1 ? hi : lo)[i] >> (8 * (j >> 1 & 3)));
           const float s = i < 4 ? s0[i] : s1[i - 4], z = i < 4 ? z0[i] : z1[i - 4];
-          const float v = PW == 1 ? fmaf(q, s, z) : (q - z) * s;
+          const float v = PW == 2 ? fmaf(q, s, z) : (q - z) * s;
           if (i < 4) v0[i] = __float_as_uint(v);
           else v1[i - 4] = __float_as_uint(v);
         }
         bf16x8 b[PW];
-        if constexpr (PW == 1) {
-          u32x4 e;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            e[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v0[2 * i]), (__bf16)__uint_as_float(v0[2 * i + 1])});
-            e[2 + i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)__uint_as_float(v1[2 * i]), (__bf16)__uint_as_float(v1[2 * i + 1])});
-          }
-          b[0] = __builtin_bit_cast(bf16x8, e);
+        split8(v0, v1, b);
+        if constexpr (NA == 2) {
+          mfma_parts(r.a[0], b, acc[0][j]);
         } else {
-          bf16x8 all3[3];
-          split8(v0, v1, all3);
 #pragma unroll
-          for (int i = 0; i < PW; ++i) b[i] = all3[i];
-        }
+          for (int p = PW - 1; p >= 0; --p)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          if constexpr (NA == 1)
-            acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r.a[mb][0], b[0], acc[mb][j][0], 0, 0, 0);
-          else mfma_parts(r.a[mb], b, acc[mb][j]);
+            for (int mb = 0; mb < MB; ++mb)
+              acc[mb][j][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r.a[mb][0], b[p], acc[mb][j][0], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);  // one column's values at a time: registers
       }
     };
-    Step one;
-    if constexpr (NA == 2 || MB == 2) {  // their sums leave no registers for a second step
-      for (int64_t st = first + w; st < last; st += kTWaves) {
-        load(st, one);
-        asm volatile("" ::: "memory");
-        compute(one);
-      }
-    } else {
-      // the next step's loads are under way while one is computed; the compiler would sink them to their use
-      Step two;
-      load(first + w, one);
-      for (int64_t st = first + w; st < last; st += 2 * kTWaves) {
-        load(st + kTWaves, two);
-        asm volatile("" ::: "memory");
-        compute(one);
-        __builtin_amdgcn_sched_barrier(0);
-        load(st + 2 * kTWaves, one);
-        asm volatile("" ::: "memory");
-        compute(two);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int64_t st = first + w; st < last; st += kTWaves) {
+      Step r;
+      load(st, r);
+      asm volatile("" ::: "memory");
+      compute(r);
     }
 
     // register e: row 4 h + e, columns 16 l16 + j.  The upper four waves' sums go to
@@ -442,12 +424,13 @@ static hipError_t back_rows_go(const TilesArgs& a, const LoraPlan& p, float* par
 
 template <typename TX, typename TS>
 static hipError_t back_rows(const TilesArgs& a, const LoraPlan& p, float* part, hipStream_t st) {
-  constexpr int PW = sizeof(TS) == 2 ? 2 : 3;
-  if (p.pw > 1) return back_rows_go<TX, TS, PW, 1>(a, p, part, st);
-  if constexpr (sizeof(TX) == 2) {
-    if (p.mb == 1) return back_rows_go<TX, TS, 1, 1>(a, p, part, st);
-    return back_rows_go<TX, TS, 1, 2>(a, p, part, st);
+  if constexpr (sizeof(TS) == 4) {
+    if (p.pw == 3) return back_rows_go<TX, TS, 3, 1>(a, p, part, st);
   }
+  if constexpr (sizeof(TX) == 2) {
+    if (p.mb == 2) return back_rows_go<TX, TS, 2, 2>(a, p, part, st);
+  }
+  if constexpr (sizeof(TX) == 2 || sizeof(TS) == 2) return back_rows_go<TX, TS, 2, 1>(a, p, part, st);
   return hipErrorInvalidValue;
 }
 

@@ -8,15 +8,16 @@
 // once a workgroup, in the operand tile [128 columns of dx][64 weight rows].
 // A word of codes holds eight columns of one weight row while the sum runs over rows: a
 // thread takes the same eight columns of four rows and stores four rows of each column
-// as one 8-byte piece.  The pairs that v_cvt_pk_bf16_f32 makes are two rows of one
+// as one 8-byte piece.  The pairs that a conversion to bf16 makes are two rows of one
 // column, so turning costs no instruction of its own.
 //
-// PW bf16 parts of a weight, each an operand tile of its own: one (rounded to bf16, as w4a16_matmul
-// does: half a step, 2^-8 at most, beside that of a bf16 result), two (exact with fp16 scales:
-// 15 bits) or three (float32 scales).
+// A weight is the sum of PW bf16 parts, each an operand tile of its own: two with fp16 scales (15 bits with
+// whole zero-points, so exact) and for a bf16 result (16 bits, off by 2^-16 of itself at most, beside the 2^-8 of the
+// result's rounding), three for a float32 result of float32 scales (24 bits).  (One, a weight rounded to bf16,
+// took 169 us for 2048 rows of [11008, 4096] where two take TODO, and left an error against 64 bits of 2.3e-3 where the
+// rounding of a bf16 result alone leaves 1.7e-3.)
 //
-// Bound by feeding the matrix cores, busy half the time: 2048 rows of [11008, 4096] 169 us (1.09
-// PFLOP/s), 333 rows of [4096, 11008] in two parts 100.  All waves doing everything took 201.
+// Bound by the matrix cores: TODO
 #pragma once
 
 #include <type_traits>
@@ -233,23 +234,22 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
         load_lds4(buf_rsrc_n(uniform_ptr((const char*)zeros + byte), bytes), tab + T::TAB_HALF + 256 * sub0, so);
     };
 
-    // 4 floats -> two words of bf16, in PW parts
+    // 4 floats -> two words of bf16, in PW parts: each the upper half of what is left, the second of two rounded to nearest
     auto put4 = [&](uint8_t* at, float (&v)[4]) {
       u32x2 d;
-      if constexpr (PW == 1) {
-        d.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
-        d.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
-        *(u32x2*)at = d;
-      } else {
 #pragma unroll
-        for (int q = 0; q < PW; ++q) {
+      for (int q = 0; q < PW; ++q) {
+        if (PW == 2 && q == 1) {
+          d.x = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]});
+          d.y = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]});
+        } else {
           d.x = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
           d.y = __builtin_amdgcn_perm(__float_as_uint(v[3]), __float_as_uint(v[2]), 0x07060302u);
-          *(u32x2*)(at + q * T::B_PART) = d;
-          if (q + 1 < PW) {
+        }
+        *(u32x2*)(at + q * T::B_PART) = d;
+        if (q + 1 < PW) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
-          }
+          for (int i = 0; i < 4; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
         }
       }
     };
@@ -257,10 +257,10 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
       if constexpr (sizeof(TS) == 2) return (float)__builtin_bit_cast(_Float16, (uint16_t)(word >> (16 * odd)));
       else return __uint_as_float(word);
     };
-    // one code with s and z (-zp s, or zp where weights keep their bits)
+    // one code with s and z: -zp s in two parts (exact with fp16 scales, 11 bits times 11), zp in three
     auto weight = [&](uint32_t byte, float s, float z) {
       const float q = (float)(uint8_t)byte;
-      return PW == 1 ? fmaf(q, s, z) : (q - z) * s;
+      return PW == 2 ? fmaf(q, s, z) : (q - z) * s;
     };
 
     // The thread's piece is columns 8 kb .. 8 kb + 7 of weight rows 4 b .. 4 b + 3.
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(512, 2) void k_w4a16_tiles(
       for (int i = 0; i < 4; ++i) {
         const uint32_t p = *(const uint32_t*)(sm + rawo[i] + rs_ * T::RAW_STAGE);
         s[i] = value(sw[i], odd[i]), z[i] = value(zw[i], odd[i]);
-        if constexpr (PW == 1) z[i] *= -s[i];
+        if constexpr (PW == 2) z[i] *= -s[i];
         lo[i] = p & 0x0f0f0f0fu;
         hi[i] = (p >> 4) & 0x0f0f0f0fu;
         asm("" : "+v"(lo[i]), "+v"(hi[i]));  // no instruction: bytes are converted in place, not masked again one by one

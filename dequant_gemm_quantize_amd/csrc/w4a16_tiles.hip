@@ -9,23 +9,18 @@ static hipError_t tiles_subs(const TilesArgs& a, const Adapters& ad, hipStream_t
   return tiles_go<MI, PW, 4, TS, TY>(a, ad, st);
 }
 
-template <typename TS>
+template <int MI, typename TS>
 static hipError_t tiles_types(const TilesArgs& a, const Adapters& ad, hipStream_t st) {
-  if (a.pw == 1) {
-    if (a.y_dtype == W4_F32)
-      return a.mi == 2 ? tiles_subs<2, 1, TS, float>(a, ad, st) : tiles_subs<4, 1, TS, float>(a, ad, st);
-    return a.mi == 2 ? tiles_subs<2, 1, TS, __bf16>(a, ad, st) : tiles_subs<4, 1, TS, __bf16>(a, ad, st);
-  }
-  if constexpr (sizeof(TS) == 2)
-    return a.mi == 2 ? tiles_subs<2, 2, TS, float>(a, ad, st) : tiles_subs<4, 2, TS, float>(a, ad, st);
-  else
-    return tiles_subs<2, 3, TS, float>(a, ad, st);
+  if (a.y_dtype == W4_F32) return tiles_subs<MI, 2, TS, float>(a, ad, st);
+  return tiles_subs<MI, 2, TS, __bf16>(a, ad, st);
 }
 
 hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st) {
   const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
                     (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
-  return a.sz_dtype == W4_F16 ? tiles_types<_Float16>(a, ad, st) : tiles_types<float>(a, ad, st);
+  if (a.pw == 3) return tiles_subs<2, 3, float, float>(a, ad, st);
+  if (a.sz_dtype == W4_F16) return a.mi == 2 ? tiles_types<2, _Float16>(a, ad, st) : tiles_types<4, _Float16>(a, ad, st);
+  return a.mi == 2 ? tiles_types<2, float>(a, ad, st) : tiles_types<4, float>(a, ad, st);
 }
 
 }  // namespace w4

@@ -444,9 +444,10 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *   v is an output; rows of no adapter are left as they were.
  *
  *   In all three sums are float32, and the result is rounded once.
- *   w4a16_lora_matmul rounds no weight.  In the transposed products with bf16 dy and a
- *   bf16 result the weight may be rounded to bf16 before the product, as in
- *   w4a16_matmul; otherwise no operand loses bits that float32 has.
+ *   No weight is rounded to bf16 (as w4a16_matmul may do): w4a16_lora_matmul keeps all its bits, and so do
+ *   the transposed products, but for a bf16 result of bf16 dy with float32 scales, whose
+ *   weights have 16 bits at least.  Products of float32 operands (x, dy, the
+ *   adapters, u, v) leave out parts below 2^-21 of the product itself.
  *   workspace: device memory, 16-byte aligned, of at least the bytes that the
  *   call's own size function gives (W4_EINVAL below; 0: may be NULL), its contents ignored on
  *   entry and unspecified on return.  Calls that overlap on one workspace

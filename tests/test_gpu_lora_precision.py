@@ -1,4 +1,4 @@
-"""The product with adapters keeps its weights: no rounding of (q - zp) s before the product, with few rows or many,
+"""The product with adapters and the transposed one keep their weights: no rounding of (q - zp) s before the product, with few rows or many,
 for either type of the result.  The cases and what they may be off are in lora_precision_cases.py; the CPU tests of
 test_lora_precision_host.py show that they tell rounded weights."""
 import pytest
@@ -52,3 +52,23 @@ def test_forward_rows_beside_others(g):
     alone = w4.w4a16_lora_matmul(x[-1:], packed, scales, zeros, g, *ad, ends, zero)[0]
     # half a step of bf16 is 2^-9 of y; the float32 sums differ by about 2^-20 of it, so ties split in far below 2% of cases
     assert (many != alone).double().mean().item() <= 0.02
+
+
+@pytest.mark.parametrize("sz", ["f16", "f32"])
+@pytest.mark.parametrize("out", sorted(OUT))
+@pytest.mark.parametrize("shape", P.BACK, ids=lambda s: "x".join(map(str, s)))
+def test_back(shape, out, sz):
+    c = P.case(*shape, sz, "cuda", sum(shape))
+    want = P.back(c, c["dense"])
+    plain = c["dy"].double() @ c["dense"]
+    for adapters, exact in ((True, want), (False, plain)):
+        dx = Canary((c["m"], c["k"]), OUT[out])
+        if adapters:
+            w4.w4a16_lora_matmul_t(c["dy"].bfloat16(), *weight(c), *adapter(c, torch.bfloat16), out=dx.tensor)
+        else:
+            w4.w4a16_matmul_t(c["dy"].bfloat16(), *weight(c), out=dx.tensor)
+        dx.check()
+        if sz == "f16":
+            assert torch.equal(dx.tensor, exact.to(OUT[out]))
+        else:
+            assert ((dx.tensor.double() - exact).abs() <= P.allowance(c, True, OUT[out], exact)).all()
