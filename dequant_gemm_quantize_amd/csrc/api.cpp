@@ -735,7 +735,7 @@ int w4a16_lora_matmul(const void* x, int x_dtype, int64_t m, int64_t k, const ui
                       size_t workspace_bytes, hipStream_t stream) {
   static const char* fn = "w4a16_lora_matmul";
   if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
-  const w4::TilesArgs p{false, x, m, k, n, packed, scales, zeros, sz_dtype, group_size, y, y_dtype, 0, 0, 0, 0};
+  const w4::TilesArgs p{false, x, m, k, n, packed, scales, zeros, sz_dtype, group_size, y, y_dtype, 0, 0, 0, 0, 0};
   const w4::LoraInto in{true, x, x_dtype, m, k, a, ab_dtype, adapters, rank, scaling, offsets, which, segments, u, 1};
   const w4::LoraOut out{u, b, ab_dtype, adapters, rank, offsets, which, segments, 1, nullptr};
   return lora_product(fn, x_dtype, p, in, out, workspace, workspace_bytes, stream);
@@ -749,7 +749,7 @@ size_t w4a16_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32_t gr
 int w4a16_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                    const void* zeros, int sz_dtype, int64_t n, int32_t group_size, void* dx, int dx_dtype,
                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0};
+  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0, 0};
   return lora_product("w4a16_matmul_t", dy_dtype, p, w4::LoraInto{}, w4::LoraOut{}, workspace, workspace_bytes, stream);
 }
 
@@ -771,7 +771,7 @@ int w4a16_lora_matmul_t(const void* dy, int dy_dtype, int64_t m, int64_t k, cons
   if (rank == 0) return fail(W4_EINVAL, "%s: rank = 0 must be a multiple of 8", fn);
   const w4::LoraInto in{false, dy, dy_dtype, m, n, b, ab_dtype, adapters, rank, scaling, offsets, which, segments, v, 1};
   const w4::LoraOut out{v, a, ab_dtype, adapters, rank, offsets, which, segments, 1, nullptr};
-  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0};
+  const w4::TilesArgs p{true, dy, m, k, n, packed, scales, zeros, sz_dtype, group_size, dx, dx_dtype, 0, 0, 0, 0, 0};
   return lora_product(fn, dy_dtype, p, in, out, workspace, workspace_bytes, stream);
 }
 

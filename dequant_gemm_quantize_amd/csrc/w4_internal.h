@@ -185,6 +185,7 @@ struct TilesArgs {
   void* y;
   int y_dtype;
   int mi, pw, parts, steps;
+  int64_t row;  // back: values from a row of x to the next, a multiple of 8; zeros behind the n'th
 };
 hipError_t launch_w4a16_lora_gemm(const TilesArgs& a, const LoraOut& lo, hipStream_t st);  // forward
 hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st);      // back
@@ -192,7 +193,7 @@ hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t
 hipError_t launch_w4a16_lora_rows(const void* x, int x_dtype, int64_t m, int64_t k, const uint8_t* packed,
                                   const void* scales, const void* zeros, int sz_dtype, int64_t n, int g, void* y,
                                   int y_dtype, const LoraOut& lo, hipStream_t st);
-// Either direction, whatever the sizes (args without x, mi, pw, parts and steps), and the workspace's bytes (0: none).
+// Either direction, whatever the sizes (args without x and what follows y_dtype), and the workspace's bytes (0: none).
 size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
                                   int y_dtype);
 // Whether the call ends in the kernel that adds partial sums, which takes the low-rank values in parts too (back).

@@ -39,7 +39,8 @@ struct LoraPlan {
   int mi, pw;          // tiles of 32 mi rows forward, 64 mi back; bf16 parts of a weight (back)
   int mb;              // blocks of 16 rows a workgroup of k_w4a16_back_rows
   int64_t rows, strips, parts, steps;
-  size_t bytes;        // of workspace
+  int64_t pad;         // > 0: dy is copied into rows of as many values first
+  size_t sums, bytes;  // of the partial sums in the workspace, and of all of it
 };
 
 void split(LoraPlan& p, int64_t all, int64_t parts) {
@@ -71,13 +72,17 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
     const int64_t all = (k + 255) / 256, room = (p.mi == 4 ? 512 : 768) / (p.rows * p.strips);
     const int64_t parts = room < all / 4 ? room : all / 4;
     split(p, all, parts < 3 ? 1 : parts);
-    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)n * 4;
+    p.bytes = p.sums = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)n * 4;
     return p;
   }
-  // Rows of dy start at 16-byte addresses; 256 of them, and 128 of codes and scales, stay
-  // below 2^31 bytes.  us of the few-row kernel / tiles: [11008, 4096] 32 rows 27 / 29, 48 rows 34 / 30; [4096, 11008] 32
-  // rows 27 / 36, 48 rows 41 / 38; [4096, 4096] 24 rows 16 / 17, 48 rows 20 / 19.
-  p.tiles = x_dtype == W4_BF16 && m > 32 && n % 8 == 0 && n <= ((int64_t)1 << 21);
+  // 256 rows of dy, and 64 of codes and scales, stay below 2^31 bytes; an even number of fp16 scales.  us of the few-row
+  // kernel / tiles: [11008, 4096] 32 rows 27 / 29, 48 rows 34 / 30; [4096, 11008] 32 rows 27 / 36, 48 rows 41 / 38;
+  // [4096, 4096] 24 rows 16 / 17, 48 rows 20 / 19.  Where rows of dy do not start at 16-byte addresses they are copied
+  // into ones that do, 4 to 8 us more: [11001, 4096] 65 rows 34 / 38, 128 rows 53 / 44, 2048 rows 620 / 317; [4095, 4096] 65 rows
+  // 22 / 25, 128 rows 29 / 30, 333 rows 72 / 44; [2050, 2048] 128 rows 18 / 21, 333 rows 28 / 27.
+  const bool aligned = n % 8 == 0;
+  p.tiles = x_dtype == W4_BF16 && m > (aligned ? 32 : 96) && n <= ((int64_t)1 << 21) &&
+            (sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
   // us in tiles of 128 / 256 rows: [11008, 4096] 100 rows 34 / 41, 200 rows 52 / 46, 2048 rows 358 / 266; [4096, 4096] 128
   // rows 25 / 29, 256 rows 29 / 30, 333 rows 40 / 37; [4096, 11008] 333 rows 120 / 77 (600 rows, where the larger ones need a
   // second round for two tiles, 124 / 167).  Three parts of a weight leave room for the smaller ones only.
@@ -88,7 +93,9 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
   if (p.tiles) {
     const int64_t all = (n + 63) / 64, parts = 256 / (p.rows * p.strips);
     split(p, all, parts < all / 8 ? parts : all / 8);
-    p.bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)k * 4;
+    p.sums = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)m * (size_t)k * 4;
+    p.pad = aligned ? 0 : (n + 7) / 8 * 8;
+    p.bytes = p.sums + ((size_t)m * (size_t)p.pad * 2 + 127) / 128 * 128;
   } else {
     p.strips = (k + kTStrip - 1) / kTStrip;
     // a workgroup a CU; two steps a wave at least, for the partial sums cost as much as
@@ -101,7 +108,7 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
     p.rows = (m + 16 * p.mb - 1) / (16 * p.mb);
     const int64_t parts = 256 / (p.rows * p.strips);
     split(p, all, parts < most ? parts : most);
-    p.bytes = (size_t)p.parts * (size_t)m * (size_t)k * 4;
+    p.bytes = p.sums = (size_t)p.parts * (size_t)m * (size_t)k * 4;
   }
   return p;
 }
@@ -286,6 +293,17 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
   }
 }
 
+// Rows of dy into rows of `pad` values, a multiple of 8, zeros behind the last.  Bound by bytes, and by a launch where they are few.
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ dy, int64_t M, int64_t N, int64_t pad,
+                                                  uint16_t* __restrict__ out) {
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x)
+    for (int64_t n = 8 * (int64_t)threadIdx.x; n < pad; n += 8 * 256) {
+      bf16x8 v[1];
+      row8(dy + m * N, n, N, true, v);
+      *(bf16x8*)(out + m * pad + n) = v[0];
+    }
+}
+
 // A wave has 64 V columns of one row of the result at a time (V 4: at 16-byte
 // addresses): the partial sums, in order, and, back, the low-rank part of the row's
 // adapter from `out` [L, R, C].  (Forward the first part's tiles have added it: a dot product an output here,
@@ -398,7 +416,7 @@ static hipError_t sum_go(const float* part, int parts, int64_t m, int64_t c, con
 }
 
 bool w4a16_lora_sums(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype, int y_dtype) {
-  return lora_plan(back, m, k, n, g, x_dtype, sz_dtype, y_dtype).bytes > 0;
+  return lora_plan(back, m, k, n, g, x_dtype, sz_dtype, y_dtype).sums > 0;
 }
 
 size_t w4a16_lora_workspace_bytes(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtype, int sz_dtype,
@@ -439,11 +457,18 @@ hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, 
   const LoraPlan p = lora_plan(args.back, args.m, args.k, args.n, args.g, x_dtype, args.sz_dtype, args.y_dtype);
   TilesArgs a = args;
   a.x = x;
-  a.mi = p.mi, a.pw = p.pw, a.parts = (int)p.parts, a.steps = (int)p.steps;
+  a.mi = p.mi, a.pw = p.pw, a.parts = (int)p.parts, a.steps = (int)p.steps, a.row = a.n;
   float* part = (float*)ws;
   hipError_t e;
   if (p.tiles) {
     if (p.parts > 1) a.y = ws, a.y_dtype = W4_F32;
+    if (p.pad > 0) {
+      uint16_t* rows = (uint16_t*)((uint8_t*)ws + p.sums);
+      k_pad_rows<<<dim3((unsigned)(a.m < 16384 ? a.m : 16384)), 256, 0, st>>>((const uint16_t*)x, a.m, a.n, p.pad, rows);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      a.x = rows, a.row = p.pad;
+    }
     // With parts, forward the first one's tiles add the low-rank part, back the sum, which low may come to in parts.
     if (!a.back) e = launch_w4a16_lora_gemm(a, lo, st);
     else e = launch_w4a16_tiles(a, p.parts == 1 ? lo : LoraOut{}, st);
