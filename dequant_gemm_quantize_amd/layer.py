@@ -134,6 +134,13 @@ def _activations(x2: torch.Tensor) -> torch.Tensor:
     return x2 if x2.dtype in (torch.bfloat16, torch.float32) else x2.to(torch.float32)
 
 
+def _at_16_bytes(t: torch.Tensor) -> torch.Tensor:
+    """t dense and at a 16-byte address, as the kernels take it.  A dense view into a larger tensor, as the backward
+    of torch.cat makes them, may begin at any element."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _result_dtype(x: torch.Tensor, out_dtype: Optional[torch.dtype]) -> torch.dtype:
     return out_dtype or (x.dtype if x.is_floating_point() else torch.float32)
 
@@ -287,7 +294,7 @@ class _LoRALinear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         packed, scales, zeros, a, b, scaling, offsets, adapters, *kept = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = _at_16_bytes(dy)
         v = dy.new_empty((dy.shape[0], a.shape[1]), dtype=torch.float32)
         dx = _lib.w4a16_lora_matmul_t(dy, packed, scales, zeros, ctx.group_size, a, b, scaling, offsets, adapters, v=v)
         da = db = None
@@ -361,7 +368,7 @@ class LoRALinear(torch.nn.Module):
             raise ValueError(f"x has {x.shape[-1]} features, the layer takes {self.in_features}")
         if (offsets is None) != (which is None):
             raise ValueError("offsets and which come together")
-        x2 = _activations(x.reshape(-1, self.in_features).contiguous())
+        x2 = _at_16_bytes(_activations(x.reshape(-1, self.in_features)))
         if offsets is None:
             offsets, which = self._ends * x2.shape[0], self._first
         y = lora_linear(x2, self.packed, self.scales, self.zeros, self.group_size, self.a, self.b, self.scaling,
