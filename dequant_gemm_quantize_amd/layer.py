@@ -8,8 +8,10 @@ Every numeric step runs in the HIP kernels behind libw4.so: quantization at
 construction (asymmetric, symmetric, symmetric with a percentile or MSE
 calibrated scale, or GPTQ with calibration activations), the product in forward (W4A16, or W4A8 with per-token
 INT8 activations).  This module only reshapes tensors and keeps the buffers.
-The layers are for inference: no gradient flows through their results, but
-for LoRALinear, which trains low-rank adapters beside a frozen INT4 weight.
+Their weights are frozen.  Gradients pass a QuantizedLinear of bf16 or fp32
+activations to its input, and LoRALinear trains low-rank adapters beside such a
+weight; no gradient flows through the results of the layers that quantize
+their activations (act_int8, MXFP4Linear) or of QuantizedExperts.
 """
 from __future__ import annotations
 
@@ -45,6 +47,22 @@ def _gptq(w: torch.Tensor, g: int, sz: torch.dtype, x: Optional[torch.Tensor], s
     return _lib.gptq_quantize_pack_int4(wf, u, g, symmetric, sz, overwrite_w=owned)
 
 
+class _FrozenLinear(torch.autograd.Function):
+    """y of w4a16_matmul, differentiable with respect to x: keeps the weight (not copied), nothing of x."""
+
+    @staticmethod
+    def forward(ctx, x, packed, scales, zeros, group_size, out_dtype):
+        ctx.save_for_backward(packed, scales, zeros)
+        ctx.group_size, ctx.dtype = group_size, x.dtype
+        return _lib.w4a16_matmul(x, packed, scales, zeros, group_size, out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dx = _lib.w4a16_matmul_t(_at_16_bytes(dy), *ctx.saved_tensors, ctx.group_size, out_dtype=ctx.dtype)
+        return dx, None, None, None, None, None
+
+
 class QuantizedLinear(torch.nn.Module):
     """y = x . dequant(Wq)^T with W [out_features, in_features] held as packed
     INT4 codes [N, K/2], scales and zero-points [N, K/g].
@@ -52,7 +70,10 @@ class QuantizedLinear(torch.nn.Module):
     forward(x): x [..., in_features] in bf16 or fp32 on the weight's GPU;
     returns [..., out_features] in ``out_dtype`` (default: x's dtype).  With
     ``act_int8=True`` the activations are quantized per token to INT8 first
-    and the W4A8 product is used (bf16 output)."""
+    and the W4A8 product is used (bf16 output, which carries no gradient).
+
+    Differentiable once with respect to x (w4a16_matmul_t; not with
+    ``act_int8``); the weight is frozen."""
 
     def __init__(self, in_features: int, out_features: int, group_size: int = 128,
                  scale_dtype: torch.dtype = torch.float16, act_int8: bool = False,
@@ -110,8 +131,8 @@ class QuantizedLinear(torch.nn.Module):
             y = _lib.w4a8_matmul(xq, xs, self.packed, self.scales, self.zeros, self.group_size,
                                  out_dtype=self.out_dtype or torch.bfloat16)
         else:
-            y = _lib.w4a16_matmul(x2, self.packed, self.scales, self.zeros, self.group_size,
-                                  out_dtype=self.out_dtype or x.dtype)
+            args = (x2, self.packed, self.scales, self.zeros, self.group_size, self.out_dtype or x.dtype)
+            y = _FrozenLinear.apply(*args) if x2.requires_grad and torch.is_grad_enabled() else _lib.w4a16_matmul(*args)
         return y.reshape(*lead, self.out_features)
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
