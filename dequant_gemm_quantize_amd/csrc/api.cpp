@@ -758,7 +758,8 @@ size_t w4a16_lora_matmul_t_workspace_size(int64_t m, int64_t k, int64_t n, int32
   const size_t own = lora_workspace(true, m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype);
   const bool valid = check_adapters("w4a16_lora_matmul_t_workspace_size", m, k, n, 1, rank, segments) == W4_OK;
   ok();
-  if (own == 0 || !valid || segments == 0) return own;
+  if (!valid) return 0;
+  if (own == 0 || segments == 0) return own;
   return own + low_bytes(low_parts(m, k, n, group_size, dy_dtype, sz_dtype, dx_dtype, rank, segments), m, rank);
 }
 
