@@ -11,7 +11,7 @@
 // behind: 4096 x 11008 bf16 into codes 23 us (34 with the borders looked at for every value), back 22.
 #include <type_traits>
 
-#include "w4_common.h"
+#include "lora.h"
 #include "w4_internal.h"
 
 namespace w4 {
@@ -19,20 +19,6 @@ namespace w4 {
 namespace {
 
 constexpr int CB = 128;  // columns of a block
-
-template <typename TX>
-__device__ __forceinline__ void read8(const TX* p, float (&v)[8]) {
-  if constexpr (sizeof(TX) == 2) {
-    const u32x4 b = *(const u32x4*)p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(b[i]), v[2 * i + 1] = bf16_hi(b[i]);
-  } else {
-    const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  }
-}
-
 
 // The codes of 8 values where a first guess may be off by one or a border is met.
 __device__ __forceinline__ void codes_at_borders(const float (&v)[8], float s, uint32_t (&out)[2]) {
@@ -62,7 +48,7 @@ __device__ __forceinline__ void quantize_block(const TX* __restrict__ x, uint32_
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (in) read8(x + row * K + col, v);
+  if (in) values8(x + row * K + col, v);
   // magnitudes compare as their bits do, infinities and NaN above all others
   uint32_t top = 0;
 #pragma unroll

@@ -9,6 +9,7 @@
 
 #include "grouped.h"
 #include "w4_common.h"
+#include "w4_internal.h"
 
 namespace w4 {
 
@@ -24,6 +25,10 @@ struct Adapters {
   int parts;     // > 1: low is [parts, M, R], to be added (k_w4a16_sum alone does)
   float* whole;  // the sums, of the rows that have an adapter
 };
+inline Adapters adapters_of(const LoraOut& lo) {
+  return Adapters{lo.low, lo.out, lo.offsets, lo.which, (int)lo.segments, (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts,
+                  lo.whole};
+}
 struct NoAdapters {
   static constexpr bool any = false;
 };
@@ -131,6 +136,20 @@ __device__ __forceinline__ void split8(u32x4 v0, u32x4 v1, bf16x8 (&out)[2]) {
   out[1] = __builtin_bit_cast(bf16x8, r);
 }
 
+// 8 consecutive bf16 or float32 at p (16-byte aligned) as float32.
+template <typename T>
+__device__ __forceinline__ void values8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 b = *(const u32x4*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(b[i]), v[2 * i + 1] = bf16_hi(b[i]);
+  } else {
+    const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  }
+}
+
 __device__ __forceinline__ bf16x8 zero8() { return __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0}); }
 
 // bf16 parts of a type's values: what a value is the exact sum of.
@@ -182,7 +201,9 @@ __device__ __forceinline__ void row8(const TX* row, int64_t d, int64_t D, bool r
 
 // acc += a b, 16 x 16 with 32 products each, of operands in parts.  The upper
 // parts' product goes to acc[0], the others, small and rounded finely, to
-// acc[1]; products below 2^-24 of the largest are left out.
+// acc[1].  Of two operands in three parts the products mid lo, lo mid and lo lo are left out: the parts
+// are cut off, so mid is below 2^-7 of its value and lo below 2^-15, and what is left out is below 2^-21 of the whole
+// product (2^-24 on average) and has its sign.
 template <int PA, int PB>
 __device__ __forceinline__ void mfma_parts(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], f32x4 (&acc)[2]) {
 #pragma unroll

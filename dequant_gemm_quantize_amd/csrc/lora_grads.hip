@@ -173,7 +173,8 @@ __device__ __forceinline__ void strip(float* sums, const T* __restrict__ src, co
         column(p.t, j, v);
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          // the lower parts first; products below 2^-24 of the largest are left out
+          // the lower parts first; with float32 dy the products mid lo, lo mid and lo lo are left out, below 2^-21 of
+          // the whole product (2^-24 on average)
 #pragma unroll
           for (int q = 2; q >= 0; --q)
 #pragma unroll

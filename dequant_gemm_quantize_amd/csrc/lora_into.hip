@@ -43,18 +43,6 @@ constexpr int kDownWaves = 16;
 // The same for tiles of up to four rows, four ranks a workgroup: a lane has 8 values of D of
 // each, on the vector unit, so every load is 1 KB (2 KB) of one row.
 constexpr int kFewWaves = 8;
-template <typename T>
-__device__ __forceinline__ void values8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const u32x4 b = *(const u32x4*)p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(b[i]), v[2 * i + 1] = bf16_hi(b[i]);
-  } else {
-    const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  }
-}
 template <int ROWS, typename TX, typename TW>
 __device__ __forceinline__ void few_rows(const TX* x, int64_t D, const TW* weights, int w, int lane, float* part) {
   float acc[ROWS][4];

@@ -11,7 +11,8 @@
 // columns are 16 l16 + j.  So nothing is transposed in memory or LDS.  The waves of
 // a workgroup and the workgroups of a strip share N; the partial sums, float32, meet
 // in LDS and in the workspace, where k_w4a16_sum adds them in order, and the low-rank part.  12 rows of
-// [11008, 4096]: 16 us and 5, the first loads 6 of them, the rest 2.75 vector instructions a code.
+// [11008, 4096]: 18 us and 5, the first loads 6 of them, the rest about five vector instructions a code, of which
+// half make the two bf16 parts of a weight (one, rounded to bf16: 16 us).
 //
 // Back, many rows of bf16 dy take tiles (w4a16_tiles.h).  Both products of many rows split the
 // sum where the tiles are few.
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(64 * kTWaves, 2) void k_w4a16_back_rows(
   }
 }
 
-// Rows of dy into rows of `pad` values, a multiple of 8, zeros behind the last.  Bound by bytes, and by a launch where they are few.
+// Rows of dy into rows of `pad` values, a multiple of 8, zeros behind the last.  Bound by bytes: 2048 rows of 11001 15 us.
 __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ dy, int64_t M, int64_t N, int64_t pad,
                                                   uint16_t* __restrict__ out) {
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x)
@@ -304,6 +305,9 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ d
     }
 }
 
+// Back every row reads its adapter's [R, C] for itself: bound by that from about 64 ranks on (256 rows of 4096 columns in
+// eight parts, ranks 16, 64, 128 and 256: 12, 18, 26 and 42 us; the tiles before it 22).
+//
 // A wave has 64 V columns of one row of the result at a time (V 4: at 16-byte
 // addresses): the partial sums, in order, and, back, the low-rank part of the row's
 // adapter from `out` [L, R, C].  (Forward the first part's tiles have added it: a dot product an output here,
@@ -482,8 +486,7 @@ hipError_t launch_w4a16_lora(const void* x, int x_dtype, const TilesArgs& args, 
     e = a.sz_dtype == W4_F16 ? back_rows<uint16_t, _Float16>(a, p, part, st) : back_rows<uint16_t, float>(a, p, part, st);
   }
   if (e != hipSuccess) return e;
-  const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
-                    (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
+  const Adapters ad = adapters_of(lo);
   if (a.back) return sum_go<true, 4>(part, (int)p.parts, a.m, a.k, ad, args.y, args.y_dtype, st);
   if (a.n % 4 == 0) return sum_go<false, 4>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);
   return sum_go<false, 1>(part, (int)p.parts, a.m, a.n, ad, args.y, args.y_dtype, st);

@@ -1,7 +1,14 @@
 // W4A16 product with the adapters of its rows' requests, for many rows of bf16 x:
 //   y[m, n] = sum over groups j of s (sum_{k in j} x q - zp sum_{k in j} x) + sum_r low[m, r] B[l(m), n, r]
 // The kernel is the many-row product's by expert, with one expert, so no weight is
-// rounded whatever the types.  The low-rank part joins the sums before they are stored.
+// rounded whatever the types.  The low-rank part joins the sums of the first part before they are stored,
+// request by request.  One part where the tiles fill the CUs; otherwise the sum over K
+// is split, and k_w4a16_sum (w4a16_lora.hip) adds the parts.
+//
+// Bound by the matrix cores and the vector instructions of conversions and scales, which wait for each other (matrix
+// cores busy 41% of the time): 2048 rows of [11008, 4096], rank 64, 250 us, of which
+// the low-rank part takes about 25; [4096, 4096], rank 16, 86; 128 rows of [4096, 11008] in nine parts 23 and their sum 6.
+// (Tiles with weights rounded to bf16 took 236, 72 and 31, with two bf16 parts a weight for a float32 result 360.)
 #include "w4a16_grouped_gemm.h"
 
 namespace w4 {
@@ -24,8 +31,7 @@ static hipError_t lg_pick(const TilesArgs& a, const Adapters& ad, hipStream_t st
 }
 
 hipError_t launch_w4a16_lora_gemm(const TilesArgs& a, const LoraOut& lo, hipStream_t st) {
-  const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
-                    (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
+  const Adapters ad = adapters_of(lo);
   if (a.sz_dtype == W4_F16)
     return a.y_dtype == W4_F32 ? lg_pick<_Float16, float>(a, ad, st) : lg_pick<_Float16, __bf16>(a, ad, st);
   return a.y_dtype == W4_F32 ? lg_pick<float, float>(a, ad, st) : lg_pick<float, __bf16>(a, ad, st);

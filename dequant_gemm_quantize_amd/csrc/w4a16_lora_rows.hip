@@ -7,10 +7,6 @@
 
 namespace w4 {
 
-static Adapters adapters_of(const LoraOut& lo) {
-  return Adapters{lo.low, lo.out, lo.offsets, lo.which, (int)lo.segments, (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
-}
-
 template <typename TX>
 static hipError_t lr_types(const void* x, int64_t m, int64_t k, const uint8_t* packed, const void* scales,
                            const void* zeros, int sz_dtype, int64_t n, int g, void* y, int y_dtype, const Adapters& ad,

@@ -16,8 +16,7 @@ static hipError_t tiles_types(const TilesArgs& a, const Adapters& ad, hipStream_
 }
 
 hipError_t launch_w4a16_tiles(const TilesArgs& a, const LoraOut& lo, hipStream_t st) {
-  const Adapters ad{lo.low,           lo.out,        lo.offsets, lo.which, (int)lo.segments,
-                    (int)lo.count, lo.rank, lo.dtype == W4_F32, lo.parts, lo.whole};
+  const Adapters ad = adapters_of(lo);
   if (a.pw == 3) return tiles_subs<2, 3, float, float>(a, ad, st);
   if (a.sz_dtype == W4_F16) return a.mi == 2 ? tiles_types<2, _Float16>(a, ad, st) : tiles_types<4, _Float16>(a, ad, st);
   return a.mi == 2 ? tiles_types<2, float>(a, ad, st) : tiles_types<4, float>(a, ad, st);

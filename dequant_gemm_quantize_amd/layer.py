@@ -331,8 +331,8 @@ def lora_linear(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     """w4a16_lora_matmul (arguments as there; y in x's dtype), differentiable
     once with respect to x, a and b; the INT4 weight stays frozen and scaling is a
     constant.  Between forward and backward it keeps the weight (not copied),
-    u [M, R] and, if a or b needs a gradient, x in 8 bits: their gradients are those at
-    the values that the checkpoint stands for."""
+    u [M, R] and, if a or b needs a gradient, x in 8 bits: a's gradient is the one
+    at the values that the checkpoint stands for, b's that of u from x itself."""
     args = (x, packed, scales, zeros, group_size, a, b, scaling, offsets, adapters)
     if torch.is_grad_enabled() and (x.requires_grad or a.requires_grad or b.requires_grad):
         return _LoRALinear.apply(*args)
