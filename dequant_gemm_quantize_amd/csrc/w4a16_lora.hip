@@ -80,9 +80,11 @@ LoraPlan lora_plan(bool back, int64_t m, int64_t k, int64_t n, int g, int x_dtyp
   // kernel / tiles: [11008, 4096] 32 rows 27 / 29, 48 rows 34 / 30; [4096, 11008] 32 rows 27 / 36, 48 rows 41 / 38;
   // [4096, 4096] 24 rows 16 / 17, 48 rows 20 / 19.  Where rows of dy do not start at 16-byte addresses they are copied
   // into ones that do, 4 to 8 us more: [11001, 4096] 64 rows 34 / 38, 65 rows 47 / 38, 2048 rows 620 / 317; [4095, 4096] 64 rows
-  // 22 / 25, 128 rows 29 / 30, 333 rows 72 / 44; [2050, 2048] 128 rows 18 / 21, 333 rows 28 / 27.
+  // 22 / 25, 128 rows 29 / 30, 333 rows 72 / 44; [2050, 2048] 128 rows 18 / 21, 333 rows 28 / 27; [9010, 256] 200 rows 19 / 30;
+  // [1500, 1024] 1000 rows 27 / 29.
   const bool aligned = n % 8 == 0;
-  p.tiles = x_dtype == W4_BF16 && m > (aligned ? 32 : 64) && n <= ((int64_t)1 << 21) &&
+  const bool many = aligned ? m > 32 : m > 64 && m * n * k > ((int64_t)3 << 29);
+  p.tiles = x_dtype == W4_BF16 && many && n <= ((int64_t)1 << 21) &&
             (sz_dtype == W4_F32 || n * (k / g) % 2 == 0);
   // us in tiles of 128 / 256 rows: [11008, 4096] 100 rows 34 / 41, 200 rows 52 / 46, 2048 rows 358 / 266; [4096, 4096] 128
   // rows 25 / 29, 256 rows 29 / 30, 333 rows 40 / 37; [4096, 11008] 333 rows 120 / 77 (600 rows, where the larger ones need a

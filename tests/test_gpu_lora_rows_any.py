@@ -10,8 +10,10 @@ from tests.gpu_util import Canary
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(70, 2051, 512, 128), (100, 100, 96, 32), (129, 1001, 4096, 128), (300, 2050, 1056, 96), (1030, 333, 640, 64),
-          (65, 4097, 128, 128), (257, 9, 32, 32), (400, 1023, 768, 768), (66, 2047, 96, 32), (2100, 515, 2176, 128)]
+# rows, out, in, group: above 64 rows and 3 . 2^29 products in tiles; the last three by the kernel for few rows
+SHAPES = [(100, 8001, 2112, 32), (129, 4097, 4096, 128), (300, 2051, 2816, 64), (1030, 2050, 1056, 96), (65, 8190, 4128, 32),
+          (2100, 515, 2176, 128), (400, 1023, 4224, 4224), (9000, 33, 5632, 128), (70, 2051, 512, 128), (66, 2047, 96, 32),
+          (257, 9, 32, 32)]
 
 
 @pytest.mark.parametrize("types", [("bf16", "bf16", "f16"), ("bf16", "f32", "f32")], ids="-".join)
@@ -28,7 +30,7 @@ def test_whole_numbers(m, n, k, g, types):
         assert torch.equal(w4.w4a16_matmul_t(c["dy"], *c["weight"], out_dtype=dt), (c["dy"].double() @ c["dense"]).to(dt))
 
 
-@pytest.mark.parametrize("m,n,k", [(300, 2051, 1024), (1000, 101, 4096)])
+@pytest.mark.parametrize("m,n,k", [(300, 2051, 2816), (700, 1001, 2560)])
 def test_captured_and_replayed(m, n, k):
     """The copy of dy is part of a captured call: replays with other dy in the same buffer, two graphs of one pool."""
     c = C.case(m, n, k, 128, 16, [0, m // 2, m], [1, 0], 2, seed=3)
@@ -51,7 +53,7 @@ def test_captured_and_replayed(m, n, k):
 
 
 def test_rows_that_are_not_numbers_stay_alone():
-    m, n, k = 300, 2051, 1024
+    m, n, k = 300, 2051, 2816
     c = C.case(m, n, k, 32, 16, [0, m // 2, m], [0, 1], 2)
     bad = m // 3
     dy = c["dy"].clone()
