@@ -460,7 +460,8 @@ int dequant_checkpoint_int8(const int8_t* xq, const float* xs, int64_t m, int64_
  *   An adapter without rows gets zeros.  Rows of no adapter are not read.
  *   workspace as above, lora_grads_workspace_size bytes.
  *
- * All are deterministic.  A row that holds an infinity may give NaN.
+ * All are deterministic.  A row that holds an infinity may give NaN, and so may one of w4a16_lora_matmul
+ * with values from 2^116 on: up to 128 of them are summed times codes (16 + codes) before the scale.
  */
 size_t w4a16_lora_matmul_workspace_size(int64_t m, int64_t k, int64_t n, int32_t group_size, int x_dtype, int sz_dtype,
                                         int y_dtype);

@@ -100,3 +100,36 @@ def test_views_and_no_second_derivative():
         dx.sum().backward()
     empty = torch.randn(0, 128, device="cuda", requires_grad=True)
     assert torch.autograd.grad(one(empty).sum(), empty)[0].shape == (0, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_layers_of_many_rows(dtype):
+    """Adapters of several requests, then a frozen layer of an odd width, at sizes that take the many-row kernels: every
+    gradient against the formula in 64 bits at the values that the layers passed on."""
+    torch.manual_seed(3)
+    m, k, h, n = 900, 1280, 2048, 1033
+    lora, frozen = w4.LoRALinear(layer(h, k, 128), rank=24, adapters=3, dtype=torch.float32), layer(n, h, 128)
+    with torch.no_grad():
+        lora.b.copy_(torch.randn_like(lora.b) * 0.1)
+    offsets = torch.tensor([0, 100, 777, m], dtype=torch.int32, device="cuda")
+    which = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
+    x = torch.randint(-126, 127, (m, k), device="cuda").to(dtype)  # whole numbers, 127 the largest of each block: kept exactly in 8 bits
+    x[:, ::128] = 127
+    x.requires_grad_()
+    z = lora(x, offsets, which)
+    y = frozen(z)
+    dy = (torch.randn(m, n, device="cuda") * 1e-2).to(dtype)
+    dx, dz, da, db = torch.autograd.grad(y, (x, z, lora.a, lora.b), dy)
+    w1 = w4.QuantizedLinear(k, h, 128, device="cuda")
+    w1.packed, w1.scales, w1.zeros = lora.packed, lora.scales, lora.zeros
+    w1, w2 = w1.dequantize(torch.float32).double(), frozen.dequantize(torch.float32).double()
+    assert C.rel(dz, dy.double() @ w2) <= C.HALF[dtype] + C.sum_tol(n)
+    d, a, b = dz.double(), lora.a.detach().double(), lora.b.detach().double()
+    want_x, want_a, want_b = d @ w1, torch.zeros_like(a), torch.zeros_like(b)
+    for rows, l in ((slice(0, 100), 2), (slice(777, m), 0)):
+        u, v = x[rows].detach().double() @ a[l].t(), d[rows] @ b[l]
+        want_x[rows] += v @ a[l]
+        want_a[l], want_b[l] = v.t().contiguous() @ x[rows].detach().double(), d[rows].t().contiguous() @ u
+    assert C.rel(dx, want_x) <= C.HALF[dtype] + 4 * C.sum_tol(h)
+    assert C.rel(da, want_a) <= 4 * C.sum_tol(h) and C.rel(db, want_b) <= 4 * C.sum_tol(k)
+    assert not da[1].any() and not db[1].any()

@@ -40,3 +40,21 @@ def test_adapters_that_are_not_numbers_stay_alone():
     y = w4.w4a16_lora_matmul(c["x"], *c["weight"], a, b, *rest)
     assert torch.equal(y[0::2], C.forward64(c)[0].bfloat16()[0::2])
     assert not y[1::2].isfinite().any()
+
+
+def test_weights_beyond_4_gb():
+    """[2^18 + 8, 2^15] codes, 4.3 GB, many rows: the last weight rows."""
+    n, k, m = (1 << 18) + 8, 1 << 15, 70
+    packed = torch.full((n, k // 2), 0x88, dtype=torch.uint8, device="cuda")  # weight 0 but for the last rows
+    scales, zeros = torch.ones((n, k // 128), dtype=torch.float16, device="cuda"), torch.full((n, k // 128), 8.0, dtype=torch.float16, device="cuda")
+    packed[-3:] = torch.randint(0, 256, (3, k // 2), device="cuda").to(torch.uint8)
+    q = torch.stack([packed[-3:] & 15, packed[-3:] >> 4], -1).reshape(3, k).double() - 8
+    x = torch.randint(-1, 2, (m, k), device="cuda").bfloat16()
+    a = torch.randint(-1, 2, (2, 8, k), device="cuda").bfloat16()
+    b = torch.zeros((2, n, 8), dtype=torch.bfloat16, device="cuda")
+    b[1, -2:] = 1
+    off, ad = torch.tensor([0, 69, m], dtype=torch.int32, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    y = w4.w4a16_lora_matmul(x, packed, scales, zeros, 128, a, b, torch.ones(2, device="cuda"), off, ad, out_dtype=torch.float32)
+    want = x.double() @ q.t()
+    want[-1, -2:] += (x[-1:].double() @ a[1].double().t()).sum()
+    assert torch.equal(y[:, -3:], want.float()) and not y[:, :-3].any()

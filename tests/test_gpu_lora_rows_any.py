@@ -61,3 +61,15 @@ def test_rows_that_are_not_numbers_stay_alone():
     dx = w4.w4a16_lora_matmul_t(dy, *c["weight"], *c["adapter"])
     keep = torch.arange(m, device="cuda") != bad
     assert torch.equal(dx[keep], C.back64(c)[0].bfloat16()[keep]) and dx[bad].isnan().any()
+
+
+def test_rows_beyond_4_gb():
+    """2^17 + 5 rows of 2^14 + 1 values, 4.3 GB of dy and of its copy: the last rows."""
+    m, n, k = (1 << 17) + 5, (1 << 14) + 1, 64
+    c = C.case(8, n, k, 32, 8, [0, 8], [1], 2)
+    dy = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+    dy[-8:] = c["dy"]
+    off = torch.tensor([0, m - 8, m], dtype=torch.int32, device="cuda")
+    ad = torch.tensor([-1, 1], dtype=torch.int32, device="cuda")
+    dx = w4.w4a16_lora_matmul_t(dy, *c["weight"], c["a"], c["b"], c["scaling"], off, ad, out_dtype=torch.float32)
+    assert torch.equal(dx[-8:], C.back64(c)[0].float()) and not dx[:-8].any()
