@@ -392,8 +392,8 @@ class LoRALinear(torch.nn.Module):
         x2 = _at_16_bytes(_activations(x.reshape(-1, self.in_features)))
         if offsets is None:
             offsets, which = self._ends * x2.shape[0], self._first
-        y = lora_linear(x2, self.packed, self.scales, self.zeros, self.group_size, self.a, self.b, self.scaling,
-                        offsets, which)
+        y = lora_linear(x2, self.packed, self.scales, self.zeros, self.group_size, _at_16_bytes(self.a),
+                        _at_16_bytes(self.b), self.scaling, offsets, which)
         return y.to(_result_dtype(x, None)).reshape(*x.shape[:-1], self.out_features)
 
     def extra_repr(self) -> str:

@@ -49,3 +49,20 @@ def test_strided_and_expanded_gradients():
     assert torch.equal(got, want)
     dy = torch.randn(96, 6, device="cuda")
     assert torch.equal(torch.autograd.grad(lora(x), x, dy.t())[0], torch.autograd.grad(lora(x), x, dy.t().contiguous())[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_parameters_that_are_views_of_one_vector(dtype):
+    """Parameters in one vector, as optimizers that flatten them leave them, behind one of an odd length."""
+    lora = layer(101, 256, dtype)
+    x = torch.randn(6, 256, device="cuda").to(dtype)
+    dy = torch.randn(6, 101, device="cuda").to(dtype)
+    want = lora(x)
+    wanted = torch.autograd.grad(want, (lora.a, lora.b), dy)
+    odd = torch.zeros(3, device="cuda", dtype=dtype)
+    vector = torch.nn.utils.parameters_to_vector([odd, lora.a, lora.b]).detach().clone()
+    torch.nn.utils.vector_to_parameters(vector, [odd, lora.a, lora.b])
+    assert lora.a.data_ptr() % 16 != 0
+    got = lora(x)
+    assert torch.equal(got, want)
+    assert all(torch.equal(g, w) for g, w in zip(torch.autograd.grad(got, (lora.a, lora.b), dy), wanted))
